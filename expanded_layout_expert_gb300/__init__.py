@@ -4,7 +4,9 @@ A thin binding over libmoe_expand.so (include/moe_expand.h): each function
 marshals torch tensors (device memory, owned by the caller) and the current
 CUDA stream into one C call; every step of the layer runs in the library's
 CUDA kernels. ``ExpandedMoELayer`` strings the calls together with buffers
-allocated once.
+allocated once. The experts' training in 16 bits over the same layout is in
+``training.py``: grouped products with both gradients, SwiGLU, AdamW, and
+``TrainableExperts``, which strings those together.
 """
 from __future__ import annotations
 
@@ -19,6 +21,8 @@ from ._capi import (MOE_BLOCK_M, MOE_FFN_UNFUSED, MOE_FOLD_WEIGHT_INTO_SCALE,
                     MOE_GEMM_TILE_N128,
                     MOE_SCALE_F32_ROWMAJOR, MOE_SCALE_UE8M0_PACKED_COLMAJOR,
                     MOE_WEIGHT_OUTPUT_ROWS, MoEError, check, load)
+from .training import (AdamW, TrainableExperts, collect_row_grads, expand_rows, grouped_matmul,
+                       grouped_matmul_dgrad, grouped_matmul_wgrad, swiglu, swiglu_backward)
 
 __all__ = [
     "expanded_capacity", "workspace_size", "expand_layout", "expand_scatter",
@@ -30,6 +34,8 @@ __all__ = [
     "MOE_WEIGHT_OUTPUT_ROWS", "MOE_GEMM_TILE_N128",
     "MOE_GEMM_PER_KBLOCK_PROMOTION", "MOE_FFN_UNFUSED", "MOE_BLOCK_M",
     "scale_layout_of",
+    "expand_rows", "collect_row_grads", "grouped_matmul", "grouped_matmul_dgrad",
+    "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "AdamW", "TrainableExperts",
 ]
 
 

@@ -28,6 +28,10 @@ MOE_GEMM_TILE_N128 = 16
 MOE_GEMM_PER_KBLOCK_PROMOTION = 64
 MOE_FFN_UNFUSED = 128
 
+MOE_BF16 = 0
+MOE_F16 = 1
+MOE_F32 = 2
+
 MOE_BLOCK_M = 128
 
 ERROR_NAMES = {
@@ -40,7 +44,7 @@ ERROR_NAMES = {
 }
 
 # Every symbol include/moe_expand.h declares, with (restype, argtypes).
-P, I32, I64, SZ = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
+P, I32, I64, SZ, F64 = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_double
 SIGNATURES = {
     "moe_expanded_capacity": (I64, [I64, I32, I32, I32]),
     "moe_workspace_size": (SZ, [I64, I32, I32]),
@@ -61,6 +65,14 @@ SIGNATURES = {
     "moe_expand_to_masked_slab": (I32, [P, P, I32, I64, P, P, I32, I32, I64, P, P, I64, P, P, P,
                                         P, P, P]),
     "moe_masked_slab_to_expand": (I32, [P, I64, P, P, P, P, I32, I32, I64, P, P]),
+    "moe_expand_rows": (I32, [P, I64, P, P, P, P, I64, I32, I32, I32, I32, I64, P, I64, P, P, P]),
+    "moe_collect_row_grads": (I32, [P, P, P, I64, I32, I64, P, P]),
+    "moe_grouped_mm": (I32, [P, I64, P, P, P, I32, I32, I32, I32, I64, P, I64, P, P]),
+    "moe_grouped_mm_dgrad": (I32, [P, I64, P, P, P, I32, I32, I32, I32, I64, P, I64, P, P]),
+    "moe_grouped_mm_wgrad": (I32, [P, I64, P, I64, P, P, I32, I32, I32, I32, I64, P, I32, I32, P, P]),
+    "moe_swiglu": (I32, [P, I64, I32, I32, P, P, I64, P, I64, P]),
+    "moe_swiglu_backward": (I32, [P, I64, P, I64, I32, I32, P, P, I64, P, I64, P, P]),
+    "moe_adamw_step": (I32, [P, I32, I32, F64, F64, F64, F64, F64, I64, P, P]),
     "moe_gemm_set_trace": (I32, [P]),
     "moe_selftest_bounded_wait": (I32, [I64, P, P, P]),
     "moe_last_error_string": (C.c_char_p, []),

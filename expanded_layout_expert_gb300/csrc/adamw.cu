@@ -1,0 +1,336 @@
+// moe_adamw_step: one AdamW step over many tensors in one launch (a launch
+// per 400 of them), with the two moments held in fp32 or in 8 bits.
+//   g' = scale g
+//   m = b1 m + (1 - b1) g',   v = b2 v + (1 - b2) g'^2,   r = sqrt(v)
+//   p = p (1 - lr wd) - (m lr / (1 - b1^t)) / (r / sqrt(1 - b2^t) + eps)
+// Every operation is rounded on its own (no contraction into fused
+// multiply-adds), so a step gives the same bits as the formula written with
+// elementwise fp32 tensor operations, whatever the tensors' split over
+// launches, blocks or lanes.
+//
+// 8-bit states: m and r = sqrt(v), not v, are stored as e4m3 codes with an
+// fp32 scale per 128 values (amax / 448). r has half of v's range in powers
+// of two, so within a block it keeps what is down to 2^-18 of the largest (v:
+// 2^-36); an r > 0 that would round to zero is stored as the smallest code
+// instead, because a second moment lost to zero would divide its first moment
+// by eps alone. A block whose largest value is below 1e-30 is stored as
+// zeros (its scale's inverse would overflow). The step itself uses the new m
+// and v before they are rounded.
+//
+// Bytes a value: 8 (p) + 2|4 (g) + 16 (fp32 m, v) or 4 + 16/128 (8 bits) + 2
+// (copy): bound by HBM. A warp takes 128 consecutive values, 4 per lane (16
+// bytes of each fp32 array), which is also one scale block, so its largest
+// values are two warp reductions. The tensors' table is a kernel parameter:
+// nothing is copied to the device before the launch.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cmath>
+
+#include "common.cuh"
+#include "host_util.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlock = 128;                 // values that share a scale = values of a warp
+constexpr int kChunk = 4096;                // values of a block: 4 scale blocks per warp
+constexpr float kTinyAmax = 1e-30f;
+
+struct Tensor {
+  void* p;
+  const void* g;
+  void* copy;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t n;
+  int32_t chunk_end;   // chunks of this and the earlier tensors of the launch
+  uint8_t p_type, g_type, copy_type, vec;
+};
+
+template <int Max>
+struct Table {
+  Tensor t[Max];
+  int count;
+};
+
+struct Hyper {
+  float b1, c1, b2, c2;   // c = 1 - b
+  float decay;            // 1 - lr wd
+  float step_size;        // lr / (1 - b1^t)
+  float root;             // 1 / sqrt(1 - b2^t)
+  float eps;
+  const float* scale;
+};
+
+MOE_DEV float load16(uint16_t b, int type) {
+  return type == MOE_F16 ? __half2float(__ushort_as_half(b)) : __bfloat162float(__ushort_as_bfloat16(b));
+}
+MOE_DEV uint16_t store16(float f, int type) {
+  return type == MOE_F16 ? __half_as_ushort(__float2half_rn(f)) : __bfloat16_as_ushort(__float2bfloat16_rn(f));
+}
+
+// Four values from index i (of n) of an array of the given type; `vec`: all
+// four exist and the address is aligned to them.
+MOE_DEV void load4(const void* a, int type, int64_t i, int64_t n, bool vec, float (&f)[4]) {
+  if (type == MOE_F32) {
+    const float* s = static_cast<const float*>(a) + i;
+    if (vec) {
+      const float4 t = *reinterpret_cast<const float4*>(s);
+      f[0] = t.x; f[1] = t.y; f[2] = t.z; f[3] = t.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = i + j < n ? s[j] : 0.0f;
+    }
+  } else {
+    const uint16_t* s = static_cast<const uint16_t*>(a) + i;
+    if (vec) {
+      const ushort4 t = *reinterpret_cast<const ushort4*>(s);
+      f[0] = load16(t.x, type); f[1] = load16(t.y, type);
+      f[2] = load16(t.z, type); f[3] = load16(t.w, type);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = i + j < n ? load16(s[j], type) : 0.0f;
+    }
+  }
+}
+
+MOE_DEV void store4(void* a, int type, int64_t i, int64_t n, bool vec, const float (&f)[4]) {
+  if (type == MOE_F32) {
+    float* s = static_cast<float*>(a) + i;
+    if (vec) {
+      *reinterpret_cast<float4*>(s) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) s[j] = f[j];
+    }
+  } else {
+    uint16_t* s = static_cast<uint16_t*>(a) + i;
+    if (vec) {
+      *reinterpret_cast<ushort4*>(s) = make_ushort4(store16(f[0], type), store16(f[1], type),
+                                                    store16(f[2], type), store16(f[3], type));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) s[j] = store16(f[j], type);
+    }
+  }
+}
+
+MOE_DEV void load_codes(const void* a, int64_t i, int64_t n, bool vec, float scale, float (&f)[4]) {
+  const uint8_t* s = static_cast<const uint8_t*>(a) + i;
+  uint8_t c[4] = {0, 0, 0, 0};
+  if (vec) {
+    const uchar4 t = *reinterpret_cast<const uchar4*>(s);
+    c[0] = t.x; c[1] = t.y; c[2] = t.z; c[3] = t.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) c[j] = s[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    __nv_fp8_e4m3 q;
+    q.__x = c[j];
+    f[j] = __fmul_rn(static_cast<float>(q), scale);
+  }
+}
+
+// The block's values as codes (Floor: a positive value never becomes zero);
+// returns the block's scale. Warp-collective.
+template <bool Floor>
+MOE_DEV float store_codes(void* a, int64_t i, int64_t n, bool vec, const float (&f)[4]) {
+  float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const bool live = amax >= kTinyAmax;
+  const float inv = live ? __fmul_rn(__frcp_rn(amax), 448.0f) : 0.0f;
+  uint8_t c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    c[j] = __nv_cvt_float_to_fp8(__fmul_rn(f[j], inv), __NV_SATFINITE, __NV_E4M3);
+    if (Floor && live && f[j] > 0.0f && (c[j] & 0x7f) == 0) c[j] = 1;
+  }
+  uint8_t* s = static_cast<uint8_t*>(a) + i;
+  if (vec) {
+    *reinterpret_cast<uchar4*>(s) = make_uchar4(c[0], c[1], c[2], c[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) s[j] = c[j];
+  }
+  return live ? __fmul_rn(amax, 1.0f / 448.0f) : 0.0f;
+}
+
+template <int Bits, int Max>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<Max> tab,
+                                                         const Hyper h) {
+  const int chunk = blockIdx.x;
+  int lo = 0, hi = tab.count - 1;   // first tensor whose chunk_end is past this chunk
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.t[mid].chunk_end > chunk) hi = mid; else lo = mid + 1;
+  }
+  const Tensor& t = tab.t[lo];
+  const int first = lo > 0 ? tab.t[lo - 1].chunk_end : 0;
+  const int64_t n = t.n;
+  const int64_t base = static_cast<int64_t>(chunk - first) * kChunk;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float scale = h.scale != nullptr ? *h.scale : 1.0f;
+  constexpr int kIter = kChunk / kBlock / (kThreads / 32);
+#pragma unroll 2
+  for (int it = 0; it < kIter; ++it) {
+    const int64_t b = base + (it * (kThreads / 32) + warp) * kBlock;
+    if (b >= n) break;   // the whole warp
+    const int64_t i = b + lane * 4;
+    const bool vec = t.vec && i + 4 <= n;
+    float p[4], g[4], m[4], v[4], r[4];
+    load4(t.g, t.g_type, i, n, vec, g);
+    load4(t.p, t.p_type, i, n, vec, p);
+    if (Bits == 32) {
+      load4(t.m, MOE_F32, i, n, vec, m);
+      load4(t.v, MOE_F32, i, n, vec, v);
+    } else {
+      load_codes(t.m, i, n, vec, t.ms[b / kBlock], m);
+      load_codes(t.v, i, n, vec, t.vs[b / kBlock], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (h.scale != nullptr) g[j] = __fmul_rn(g[j], scale);
+      m[j] = __fadd_rn(__fmul_rn(m[j], h.b1), __fmul_rn(g[j], h.c1));
+      v[j] = __fadd_rn(__fmul_rn(v[j], h.b2), __fmul_rn(__fmul_rn(g[j], g[j]), h.c2));
+      r[j] = __fsqrt_rn(v[j]);
+      const float d = __fadd_rn(__fmul_rn(r[j], h.root), h.eps);
+      p[j] = __fsub_rn(__fmul_rn(p[j], h.decay), __fdiv_rn(__fmul_rn(m[j], h.step_size), d));
+    }
+    store4(t.p, t.p_type, i, n, vec, p);
+    if (t.copy != nullptr) store4(t.copy, t.copy_type, i, n, vec, p);
+    if (Bits == 32) {
+      store4(t.m, MOE_F32, i, n, vec, m);
+      store4(t.v, MOE_F32, i, n, vec, v);
+    } else {
+      // values past n are zero and change no maximum
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j >= n) m[j] = r[j] = 0.0f;
+      const float ms = store_codes<false>(t.m, i, n, vec, m);
+      const float vs = store_codes<true>(t.v, i, n, vec, r);
+      if (lane == 0) {
+        t.ms[b / kBlock] = ms;
+        t.vs[b / kBlock] = vs;
+      }
+    }
+  }
+}
+
+// A launch's parameters may take 32,764 bytes: 400 tensors of 72 bytes. A
+// table of 16 keeps the launch of a few tensors small.
+constexpr int kMaxTensors = 400;
+constexpr int kFewTensors = 16;
+
+template <int Bits, int Max>
+int launch(const Table<kMaxTensors>& all, int chunks, const Hyper& h, cudaStream_t s) {
+  if constexpr (Max == kMaxTensors) {
+    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(all, h);
+  } else {
+    Table<Max> few;
+    for (int i = 0; i < all.count; ++i) few.t[i] = all.t[i];
+    few.count = all.count;
+    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(few, h);
+  }
+  return check_launch("adamw_kernel");
+}
+
+int launch_all(const Table<kMaxTensors>& tab, int bits, int chunks, const Hyper& h, cudaStream_t s) {
+  if (bits == 32)
+    return tab.count <= kFewTensors ? launch<32, kFewTensors>(tab, chunks, h, s)
+                                    : launch<32, kMaxTensors>(tab, chunks, h, s);
+  return tab.count <= kFewTensors ? launch<8, kFewTensors>(tab, chunks, h, s)
+                                  : launch<8, kMaxTensors>(tab, chunks, h, s);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int state_bits, double lr,
+                              double beta1, double beta2, double eps, double weight_decay,
+                              int64_t step, const float* d_grad_scale, moe_stream_t stream) {
+  MOE_REQUIRE(count >= 0 && (count == 0 || tensors), "moe_adamw_step: null tensor list");
+  MOE_REQUIRE(state_bits == 32 || state_bits == 8, "moe_adamw_step: state_bits must be 32 or 8");
+  MOE_REQUIRE(step >= 1, "moe_adamw_step: step counts from 1");
+  MOE_REQUIRE(std::isfinite(lr) && beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 &&
+                  eps >= 0.0 && std::isfinite(eps) && std::isfinite(weight_decay),
+              "moe_adamw_step: betas must be in [0, 1), eps >= 0, lr and weight_decay finite");
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& a = tensors[i];
+    MOE_REQUIRE(a.n >= 0, "moe_adamw_step: tensor %d: negative size", i);
+    MOE_REQUIRE((a.n + moe::kChunk - 1) / moe::kChunk <= INT32_MAX,
+                "moe_adamw_step: tensor %d is too large", i);
+    if (a.n == 0) continue;
+    MOE_REQUIRE(a.p && a.g && a.m && a.v && (state_bits == 32 || (a.m_scale && a.v_scale)),
+                "moe_adamw_step: tensor %d: null pointer", i);
+    MOE_REQUIRE(a.p_type >= MOE_BF16 && a.p_type <= MOE_F32 && a.g_type >= MOE_BF16 &&
+                    a.g_type <= MOE_F32 && (!a.copy || (a.copy_type >= MOE_BF16 && a.copy_type <= MOE_F32)),
+                "moe_adamw_step: tensor %d: bad type", i);
+    MOE_REQUIRE(moe::aligned(a.p, a.p_type == MOE_F32 ? 4 : 2) &&
+                    moe::aligned(a.g, a.g_type == MOE_F32 ? 4 : 2) &&
+                    moe::aligned(a.copy, a.copy_type == MOE_F32 ? 4 : 2) &&
+                    (state_bits == 8 || (moe::aligned(a.m, 4) && moe::aligned(a.v, 4))) &&
+                    moe::aligned(a.m_scale, 4) && moe::aligned(a.v_scale, 4),
+                "moe_adamw_step: tensor %d: pointer not aligned to its type", i);
+  }
+  MOE_REQUIRE_DEVICE();
+  const double t = static_cast<double>(step);
+  moe::Hyper h;
+  h.b1 = static_cast<float>(beta1);
+  h.c1 = static_cast<float>(1.0 - beta1);
+  h.b2 = static_cast<float>(beta2);
+  h.c2 = static_cast<float>(1.0 - beta2);
+  h.decay = static_cast<float>(1.0 - lr * weight_decay);
+  h.step_size = static_cast<float>(lr / (1.0 - std::pow(beta1, t)));
+  h.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
+  h.eps = static_cast<float>(eps);
+  h.scale = d_grad_scale;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  moe::Table<moe::kMaxTensors> tab;
+  int64_t chunks = 0;
+  tab.count = 0;
+  const bool eight = state_bits == 8;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& a = tensors[i];
+    if (a.n == 0) continue;
+    const int64_t mine = (a.n + moe::kChunk - 1) / moe::kChunk;
+    if (tab.count == moe::kMaxTensors || chunks + mine > INT32_MAX) {
+      const int rc = moe::launch_all(tab, state_bits, static_cast<int>(chunks), h, s);
+      if (rc != MOE_OK) return rc;
+      tab.count = 0;
+      chunks = 0;
+    }
+    chunks += mine;
+    moe::Tensor& d = tab.t[tab.count++];
+    d.p = a.p;
+    d.g = a.g;
+    d.copy = a.copy;
+    d.m = a.m;
+    d.v = a.v;
+    d.ms = a.m_scale;
+    d.vs = a.v_scale;
+    d.n = a.n;
+    d.chunk_end = static_cast<int32_t>(chunks);
+    d.p_type = static_cast<uint8_t>(a.p_type);
+    d.g_type = static_cast<uint8_t>(a.g_type);
+    d.copy_type = static_cast<uint8_t>(a.copy_type);
+    d.vec = moe::aligned(a.p, a.p_type == MOE_F32 ? 16 : 8) &&
+            moe::aligned(a.g, a.g_type == MOE_F32 ? 16 : 8) &&
+            moe::aligned(a.copy, a.copy_type == MOE_F32 ? 16 : 8) &&
+            moe::aligned(a.m, eight ? 4 : 16) && moe::aligned(a.v, eight ? 4 : 16);
+  }
+  return tab.count > 0 ? moe::launch_all(tab, state_bits, static_cast<int>(chunks), h, s) : MOE_OK;
+}

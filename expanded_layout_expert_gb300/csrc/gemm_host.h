@@ -14,6 +14,15 @@ namespace moe {
 int make_tmap_k128(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t stride, uint32_t box_outer);
 
+// TMA descriptors for 16-bit operands, copied in boxes of 64 values (128
+// bytes, 128-byte swizzling); places past the tensor read as zero.
+// Rows: [rows, width] with a row stride of `ld` values, boxes of box_rows rows.
+// Weights: [E, N, Kd] contiguous, boxes of box_n rows of one expert.
+int make_tmap_rows16(CUtensorMap* tm, const void* base, uint64_t width, uint64_t rows, uint64_t ld,
+                     uint32_t box_rows);
+int make_tmap_weights16(CUtensorMap* tm, const void* base, uint64_t Kd, uint64_t N, uint64_t E,
+                        uint32_t box_n);
+
 // Arguments of the block-scaled (ue8m0) grouped GEMM, already validated.
 struct MxGemmArgs {
   const uint8_t* A;

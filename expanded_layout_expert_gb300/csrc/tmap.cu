@@ -24,7 +24,43 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// 16-bit values are moved as such, whatever they stand for.
+int make_tmap16(CUtensorMap* tm, const void* base, uint32_t rank, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) {
+    set_error("cuTensorMapEncodeTiled is not available from the driver");
+    return MOE_ERR_CUDA;
+  }
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
 }  // namespace
+
+int make_tmap_rows16(CUtensorMap* tm, const void* base, uint64_t width, uint64_t rows, uint64_t ld,
+                     uint32_t box_rows) {
+  const cuuint64_t dims[2] = {width, rows};
+  const cuuint64_t strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64u, box_rows};
+  return make_tmap16(tm, base, 2, dims, strides, box);
+}
+
+int make_tmap_weights16(CUtensorMap* tm, const void* base, uint64_t Kd, uint64_t N, uint64_t E,
+                        uint32_t box_n) {
+  const cuuint64_t dims[3] = {Kd, N, E};
+  const cuuint64_t strides[2] = {Kd * 2, N * Kd * 2};
+  const cuuint32_t box[3] = {64u, box_n, 1u};
+  return make_tmap16(tm, base, 3, dims, strides, box);
+}
 
 int make_tmap_k128(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t stride, uint32_t box_outer) {

@@ -1,0 +1,427 @@
+"""Training the experts in 16 bits over the expanded layout: bindings of the
+training calls of include/moe_expand.h, and the layer that strings them
+together.
+
+Each function marshals torch tensors and the current CUDA stream into one C
+call, as the package's other functions do. Row tensors may have a row stride
+larger than the row (a multiple of 8 values); rows outside the segments
+[start[e], psum[e]) of the layout are neither used nor written.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from typing import List, Optional, Sequence
+
+import torch
+
+from ._capi import MOE_BF16, MOE_F16, MOE_F32, check, load
+
+__all__ = ["expand_rows", "collect_row_grads", "grouped_matmul", "grouped_matmul_dgrad",
+           "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "AdamW", "TrainableExperts"]
+
+TYPE_CODE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+STATE_BLOCK = 128   # values that share a scale in an 8-bit AdamW state
+
+
+def _stream(stream=None):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _code16(t: torch.Tensor, name: str) -> int:
+    if t.dtype is torch.bfloat16:
+        return MOE_BF16
+    if t.dtype is torch.float16:
+        return MOE_F16
+    raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype) -> tuple:
+    """(pointer, row stride) of a [rows, width] tensor with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    ld = t.stride(0) if rows > 1 else max(width, t.stride(0))
+    if (t.stride(1) != 1 and width > 1) or ld < width:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    return t.data_ptr(), ld
+
+
+def _whole(t: Optional[torch.Tensor], name: str, shape: tuple, dtype):
+    """Pointer of a contiguous tensor of the given shape and type (None: NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _word(t: Optional[torch.Tensor], name: str):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.numel() < 1 or not t.is_cuda:
+        raise ValueError(f"{name} must be an int32 GPU tensor of one element")
+    return t.data_ptr()
+
+
+def _segments(lay) -> tuple:
+    E = lay.E
+    return _whole(lay.start, "lay.start", (E,), torch.int32), \
+        _whole(lay.psum, "lay.psum", (E,), torch.int32), E
+
+
+def expand_rows(x: torch.Tensor, lay, topk_w: Optional[torch.Tensor] = None,
+                n_valid: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                row_w: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                stream=None):
+    """16-bit rows of the valid pairs: out[src2dst[t, k]] = x[t], alignment
+    gaps zeroed. With ``topk_w`` also row_w[src2dst[t, k]] = topk_w[t, k] and
+    (out, row_w) is returned, else out."""
+    T, H = x.shape
+    K = lay.src2dst.shape[1]
+    _code16(x, "x")
+    if out is None:
+        out = torch.zeros(lay.M_cap, H, dtype=x.dtype, device=x.device)
+    if topk_w is not None and row_w is None:
+        row_w = torch.zeros(lay.M_cap, dtype=torch.float32, device=x.device)
+    if topk_w is None and row_w is not None:
+        raise ValueError("row_w needs topk_w")
+    xp, ld_x = _rows(x, "x", T, H, x.dtype)
+    op, ld_o = _rows(out, "out", lay.M_cap, H, x.dtype)
+    rc = load().moe_expand_rows(
+        xp, ld_x, _whole(topk_w, "topk_w", (T, K), torch.float32),
+        _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32),
+        _whole(lay.psum, "lay.psum", (lay.E,), torch.int32), _word(n_valid, "n_valid"), T, H, K,
+        lay.E, lay.align, lay.M_cap, op, ld_o,
+        _whole(row_w, "row_w", (lay.M_cap,), torch.float32), _word(status, "status"),
+        _stream(stream))
+    check(rc, "moe_expand_rows")
+    return out if topk_w is None else (out, row_w)
+
+
+def collect_row_grads(rows: torch.Tensor, lay, n_valid: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Per-row values back to their pairs: out[t, k] = rows[src2dst[t, k]], 0
+    where there is no pair (the gradient of the top-k weights)."""
+    T, K = lay.src2dst.shape
+    if out is None:
+        out = torch.zeros(T, K, dtype=torch.float32, device=rows.device)
+    rc = load().moe_collect_row_grads(
+        _whole(rows, "rows", (lay.M_cap,), torch.float32),
+        _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32), _word(n_valid, "n_valid"), T, K,
+        lay.M_cap, _whole(out, "out", (T, K), torch.float32), _stream(stream))
+    check(rc, "moe_collect_row_grads")
+    return out
+
+
+def grouped_matmul(x: torch.Tensor, w: torch.Tensor, lay, out: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[r] = x[r] @ w[e].T for the rows r of expert e; x [M, Kd], w
+    [E, N, Kd], out [M, N], all bfloat16 or all float16."""
+    dt = _code16(x, "x")
+    start, psum, E = _segments(lay)
+    M, Kd = x.shape
+    N = w.shape[1]
+    if out is None:
+        out = torch.zeros(M, N, dtype=x.dtype, device=x.device)
+    xp, ld_x = _rows(x, "x", M, Kd, x.dtype)
+    op, ld_o = _rows(out, "out", M, N, x.dtype)
+    rc = load().moe_grouped_mm(xp, ld_x, _whole(w, "w", (E, N, Kd), x.dtype), start, psum, dt, E, N,
+                               Kd, M, op, ld_o, _word(status, "status"), _stream(stream))
+    check(rc, "moe_grouped_mm")
+    return out
+
+
+def grouped_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, lay, out: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of grouped_matmul's x: out[r] = dy[r] @ w[e]; dy [M, N],
+    out [M, Kd]."""
+    dt = _code16(dy, "dy")
+    start, psum, E = _segments(lay)
+    M, N = dy.shape
+    Kd = w.shape[2]
+    if out is None:
+        out = torch.zeros(M, Kd, dtype=dy.dtype, device=dy.device)
+    dp, ld_d = _rows(dy, "dy", M, N, dy.dtype)
+    op, ld_o = _rows(out, "out", M, Kd, dy.dtype)
+    rc = load().moe_grouped_mm_dgrad(dp, ld_d, _whole(w, "w", (E, N, Kd), dy.dtype), start, psum, dt,
+                                     E, N, Kd, M, op, ld_o, _word(status, "status"), _stream(stream))
+    check(rc, "moe_grouped_mm_dgrad")
+    return out
+
+
+def grouped_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, lay, out: Optional[torch.Tensor] = None,
+                         accumulate: bool = False, out_dtype=None,
+                         status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of grouped_matmul's w: out[e] = dy[rows of e].T @ x[rows of
+    e], in the operands' type or float32 (``out_dtype``); ``accumulate`` adds
+    it to what ``out`` holds, rounded once."""
+    dt = _code16(dy, "dy")
+    start, psum, E = _segments(lay)
+    M, N = dy.shape
+    Kd = x.shape[1]
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(E, N, Kd, dtype=out_dtype or dy.dtype, device=dy.device)
+    elif out_dtype is not None and out.dtype is not out_dtype:
+        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+    if out.dtype is not dy.dtype and out.dtype is not torch.float32:
+        raise ValueError(f"out must be {dy.dtype} or float32, got {out.dtype}")
+    dp, ld_d = _rows(dy, "dy", M, N, dy.dtype)
+    xp, ld_x = _rows(x, "x", M, Kd, dy.dtype)
+    rc = load().moe_grouped_mm_wgrad(dp, ld_d, xp, ld_x, start, psum, dt, E, N, Kd, M,
+                                     _whole(out, "out", (E, N, Kd), out.dtype), TYPE_CODE[out.dtype],
+                                     int(accumulate), _word(status, "status"), _stream(stream))
+    check(rc, "moe_grouped_mm_wgrad")
+    return out
+
+
+def swiglu(gu: torch.Tensor, lay, row_w: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[r] = silu(g) * u * row_w[r] for the rows r < total of gu = [g | u]
+    (row_w None: 1)."""
+    dt = _code16(gu, "gu")
+    M, two = gu.shape
+    if two % 2:
+        raise ValueError("gu must have an even number of columns")
+    if out is None:
+        out = torch.zeros(M, two // 2, dtype=gu.dtype, device=gu.device)
+    gp, ld_g = _rows(gu, "gu", M, two, gu.dtype)
+    op, ld_o = _rows(out, "out", M, two // 2, gu.dtype)
+    rc = load().moe_swiglu(gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32),
+                           _word(lay.total, "lay.total"), M, op, ld_o, _stream(stream))
+    check(rc, "moe_swiglu")
+    return out
+
+
+def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, lay, row_w: Optional[torch.Tensor] = None,
+                    dgu: Optional[torch.Tensor] = None, drow_w: Optional[torch.Tensor] = None,
+                    stream=None):
+    """(dgu, drow_w): the gradients of swiglu's gu and row_w. ``dgu`` may be
+    ``gu`` itself, which is then overwritten."""
+    dt = _code16(gu, "gu")
+    M, two = gu.shape
+    if two % 2:
+        raise ValueError("gu must have an even number of columns")
+    if dgu is None:
+        dgu = torch.zeros(M, two, dtype=gu.dtype, device=gu.device)
+    if drow_w is None:
+        drow_w = torch.zeros(M, dtype=torch.float32, device=gu.device)
+    gp, ld_g = _rows(gu, "gu", M, two, gu.dtype)
+    hp, ld_h = _rows(dh, "dh", M, two // 2, gu.dtype)
+    op, ld_o = _rows(dgu, "dgu", M, two, gu.dtype)
+    rc = load().moe_swiglu_backward(
+        hp, ld_h, gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32),
+        _word(lay.total, "lay.total"), M, op, ld_o, _whole(drow_w, "drow_w", (M,), torch.float32),
+        _stream(stream))
+    check(rc, "moe_swiglu_backward")
+    return dgu, drow_w
+
+
+class _AdamWTensor(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("copy", C.c_void_p), ("m", C.c_void_p),
+                ("v", C.c_void_p), ("m_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n", C.c_int64), ("p_type", C.c_int32), ("g_type", C.c_int32),
+                ("copy_type", C.c_int32), ("reserved", C.c_int32)]
+
+
+class AdamW:
+    """AdamW (decoupled weight decay) over a list of tensors, one launch per
+    step and 400 tensors.
+
+    params   contiguous float32, bfloat16 or float16 tensors, updated in place
+    copies   optional tensors of the same sizes that get the new parameters in
+             their own type (the 16-bit weights the products read, beside
+             float32 parameters); an entry may be None
+    state_bits 32: the moments in float32 (exp_avg, exp_avg_sq). 8: exp_avg and
+             the root of exp_avg_sq as e4m3 codes (uint8) with a float32 scale
+             per 128 values (exp_avg_scale, exp_avg_sq_scale): 2.06 bytes a
+             value instead of 8.
+    exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, step: states to go on
+             from (a checkpoint's); zeros by default. They are the optimizer's
+             from then on.
+
+    step(grads) takes one float32, bfloat16 or float16 gradient per parameter,
+    and optionally ``grad_scale``, a float32 device word they are multiplied
+    by (a clipping factor, say) without a host read.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], *, lr: float = 1e-3, betas=(0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: float = 1e-2, state_bits: int = 32,
+                 copies: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                 exp_avg: Optional[Sequence[torch.Tensor]] = None,
+                 exp_avg_sq: Optional[Sequence[torch.Tensor]] = None,
+                 exp_avg_scale: Optional[Sequence[torch.Tensor]] = None,
+                 exp_avg_sq_scale: Optional[Sequence[torch.Tensor]] = None, step: int = 0):
+        if state_bits not in (32, 8):
+            raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")
+        if step < 0:
+            raise ValueError("step must be >= 0")
+        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
+        self.state_bits = state_bits
+        self.steps = step
+        self.params: List[torch.Tensor] = list(params)
+        n = len(self.params)
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(self.copies) != n:
+            raise ValueError(f"{len(self.copies)} copies for {n} parameters")
+        code = torch.float32 if state_bits == 32 else torch.uint8
+
+        def state(given, name, dtype, count):
+            if given is None:
+                return tuple(torch.zeros(count(p), dtype=dtype, device=p.device) for p in self.params)
+            given = tuple(given)
+            if len(given) != n:
+                raise ValueError(f"{len(given)} tensors in {name} for {n} parameters")
+            for i, (s, p) in enumerate(zip(given, self.params)):
+                if s.dtype is not dtype or s.numel() != count(p) or not s.is_contiguous() \
+                        or s.device != p.device:
+                    raise ValueError(f"{name}[{i}] must be contiguous {dtype} with {count(p)} values "
+                                     "on the parameter's device")
+            return given
+
+        for i, p in enumerate(self.params):
+            if p.dtype not in TYPE_CODE or not p.is_contiguous() or not p.is_cuda:
+                raise ValueError(f"params[{i}] must be a contiguous float32, bfloat16 or float16 GPU tensor")
+            c = self.copies[i]
+            if c is not None and (c.dtype not in TYPE_CODE or c.numel() != p.numel()
+                                  or not c.is_contiguous() or c.device != p.device):
+                raise ValueError(f"copies[{i}] must be a contiguous tensor of the parameter's size and device")
+        whole = lambda p: p.numel()  # noqa: E731
+        self.exp_avg = state(exp_avg, "exp_avg", code, whole)
+        self.exp_avg_sq = state(exp_avg_sq, "exp_avg_sq", code, whole)
+        if state_bits == 8:
+            blocks = lambda p: (p.numel() + STATE_BLOCK - 1) // STATE_BLOCK  # noqa: E731
+            self.exp_avg_scale = state(exp_avg_scale, "exp_avg_scale", torch.float32, blocks)
+            self.exp_avg_sq_scale = state(exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, blocks)
+        else:
+            if exp_avg_scale is not None or exp_avg_sq_scale is not None:
+                raise ValueError("scales belong to 8-bit states")
+            self.exp_avg_scale = self.exp_avg_sq_scale = ()
+        self._table = (_AdamWTensor * max(n, 1))()
+        for i, p in enumerate(self.params):
+            d, c = self._table[i], self.copies[i]
+            d.m, d.v = self.exp_avg[i].data_ptr(), self.exp_avg_sq[i].data_ptr()
+            if state_bits == 8:
+                d.m_scale = self.exp_avg_scale[i].data_ptr()
+                d.v_scale = self.exp_avg_sq_scale[i].data_ptr()
+            d.n, d.p_type = p.numel(), TYPE_CODE[p.dtype]
+            d.copy_type = 0 if c is None else TYPE_CODE[c.dtype]
+
+    def step(self, grads: Sequence[torch.Tensor], *, grad_scale: Optional[torch.Tensor] = None,
+             lr: Optional[float] = None, stream=None) -> None:
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        # parameters, copies and gradients are looked up anew at every step: a
+        # caller may have given them other storage since the last one
+        for d, p, c, g in zip(self._table, self.params, self.copies, grads):
+            code = TYPE_CODE.get(g.dtype)
+            if code is None or g.numel() != d.n or not g.is_cuda or not g.is_contiguous():
+                raise ValueError("a gradient must be a contiguous float32, bfloat16 or float16 GPU "
+                                 f"tensor of its parameter's {d.n} values, got {g.dtype} {tuple(g.shape)}")
+            if p.numel() != d.n or TYPE_CODE.get(p.dtype) != d.p_type or not p.is_contiguous():
+                raise ValueError("a parameter has changed its size, type or layout since this "
+                                 "optimizer was made")
+            d.p, d.g, d.g_type = p.data_ptr(), g.data_ptr(), code
+            if c is not None:
+                if c.numel() != d.n or TYPE_CODE.get(c.dtype) != d.copy_type or not c.is_contiguous():
+                    raise ValueError("a copy has changed its size, type or layout since this "
+                                     "optimizer was made")
+                d.copy = c.data_ptr()
+        if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1
+                                       or not grad_scale.is_cuda):
+            raise ValueError("grad_scale must be a float32 GPU tensor of one element")
+        rc = load().moe_adamw_step(C.cast(self._table, C.c_void_p), len(self.params), self.state_bits,
+                                   self.lr if lr is None else lr, self.betas[0], self.betas[1],
+                                   self.eps, self.weight_decay, self.steps + 1,
+                                   None if grad_scale is None else grad_scale.data_ptr(),
+                                   _stream(stream))
+        check(rc, "moe_adamw_step")
+        self.steps += 1
+
+
+class TrainableExperts:
+    """The experts of an expanded-layout MoE layer in bfloat16, with their
+    backward pass, for up to ``max_tokens`` tokens; every buffer allocated once.
+
+        forward(x, topk_ids, topk_w, n_valid) -> y [T, H]
+        backward(dy) -> (dx [T, H], dtopk_w [T, K]); dw13, dw2 hold the weights'
+                        gradients (float32; ``accumulate`` adds to them)
+        parameters / gradients: [w13, w2] and [dw13, dw2], for AdamW
+
+    y[t] = sum_k w[t, k] * w2[e] (silu(g) * u), [g | u] = w13[e] x[t], e =
+    topk_ids[t, k]. x and topk_ids, topk_w as in ExpandedMoELayer, with x in
+    bfloat16; rows t >= n_valid are neither read nor written. backward belongs
+    to the last forward and overwrites what that kept of gate_up.
+    """
+
+    def __init__(self, w13: torch.Tensor, w2: torch.Tensor, *, K: int, max_tokens: int,
+                 align: int = 1):
+        from . import Layout, expanded_capacity, workspace_size
+        E, twoI, H = w13.shape
+        if twoI % 2 or w2.shape != (E, H, twoI // 2):
+            raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
+        for name, w in (("w13", w13), ("w2", w2)):
+            if w.dtype is not torch.bfloat16 or not w.is_contiguous() or not w.is_cuda:
+                raise ValueError(f"{name} must be a contiguous bfloat16 GPU tensor")
+        self.w13, self.w2 = w13, w2
+        self.E, self.H, self.I, self.K, self.align, self.T = E, H, twoI // 2, K, align, max_tokens
+        dev = w13.device
+        M = self.M_cap = max(1, expanded_capacity(max_tokens, K, E, align))
+        i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=dev)  # noqa: E731
+        b16 = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        f32 = lambda *s: torch.zeros(*s, dtype=torch.float32, device=dev)  # noqa: E731
+        self.ws = torch.zeros(workspace_size(max_tokens, K, E), dtype=torch.uint8, device=dev)
+        self.status = i32(1)
+        self.lay = Layout(psum=i32(E), start=i32(E), total=i32(1), m_indices=i32(M),
+                          src2dst=i32(max_tokens, K), tile_prefix=i32(E + 1), E=E, align=align, M_cap=M)
+        self.xe, self.row_w, self.gu = b16(M, H), f32(M), b16(M, twoI)
+        self.h, self.down = b16(M, self.I), b16(M, H)
+        self.dh, self.drow_w = b16(M, self.I), f32(M)
+        self.y, self.dx, self.dtopk_w = b16(max_tokens, H), b16(max_tokens, H), f32(max_tokens, K)
+        self.dw13, self.dw2 = f32(E, twoI, H), f32(E, H, self.I)
+        self._n_valid = None
+        self._ready = False
+
+    @property
+    def parameters(self) -> list:
+        return [self.w13, self.w2]
+
+    @property
+    def gradients(self) -> list:
+        return [self.dw13, self.dw2]
+
+    def forward(self, x, topk_ids, topk_w, n_valid=None, stream=None) -> torch.Tensor:
+        from . import combine, expand_layout
+        _rows(x, "x", self.T, self.H, torch.bfloat16)
+        _whole(topk_ids, "topk_ids", (self.T, self.K), torch.int32)
+        lay = self.lay
+        expand_layout(topk_ids, self.E, self.align, self.M_cap, n_valid, self.ws, self.status, lay,
+                      stream)
+        expand_rows(x, lay, topk_w, n_valid, self.xe, self.row_w, self.status, stream)
+        grouped_matmul(self.xe, self.w13, lay, self.gu, self.status, stream)
+        swiglu(self.gu, lay, self.row_w, self.h, stream)
+        grouped_matmul(self.h, self.w2, lay, self.down, self.status, stream)
+        combine(self.down, lay.src2dst, None, n_valid, self.y, stream)
+        self._n_valid, self._ready = n_valid, True
+        return self.y
+
+    def backward(self, dy: torch.Tensor, accumulate: bool = False, stream=None):
+        from . import combine
+        if not self._ready:
+            raise RuntimeError("backward needs a forward before it")
+        self._ready = False
+        lay, nv, st = self.lay, self._n_valid, self.status
+        ddown = expand_rows(dy, lay, None, nv, self.down, None, st, stream)
+        grouped_matmul_wgrad(ddown, self.h, lay, self.dw2, accumulate, status=st, stream=stream)
+        grouped_matmul_dgrad(ddown, self.w2, lay, self.dh, st, stream)
+        dgu, drow_w = swiglu_backward(self.dh, self.gu, lay, self.row_w, self.gu, self.drow_w, stream)
+        grouped_matmul_wgrad(dgu, self.xe, lay, self.dw13, accumulate, status=st, stream=stream)
+        dxe = grouped_matmul_dgrad(dgu, self.w13, lay, self.down, st, stream)
+        combine(dxe, lay.src2dst, None, nv, self.dx, stream)
+        collect_row_grads(drow_w, lay, nv, self.dtopk_w, stream)
+        return self.dx, self.dtopk_w

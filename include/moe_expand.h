@@ -71,6 +71,11 @@ typedef struct CUstream_st* moe_stream_t; /* the same type as cudaStream_t */
                                             the tensor core's block scaling */
 #define MOE_FFN_UNFUSED          128 /* moe_grouped_ffn: gate_up, act+quant and down as three launches */
 
+/* Types of the 16-bit training calls and of moe_adamw_step. */
+#define MOE_BF16 0
+#define MOE_F16  1
+#define MOE_F32  2
+
 /* Rows per grouped-GEMM tile; tile_prefix counts tiles of this height. */
 #define MOE_BLOCK_M 128
 
@@ -347,6 +352,113 @@ int moe_expand_to_masked_slab(const uint8_t* xe, const void* xe_scale, int scale
 int moe_masked_slab_to_expand(const uint16_t* slab_out, int64_t max_m, const int32_t* psum,
                               const int32_t* start, const int32_t* d_total, const float* row_w,
                               int E, int H, int64_t M_cap, uint16_t* out, moe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------- training
+ * The calls below train the experts in 16 bits over the same expanded layout:
+ * moe_expand_rows, two moe_grouped_mm with moe_swiglu between them,
+ * moe_combine; back: moe_expand_rows of dy, moe_grouped_mm_dgrad / _wgrad,
+ * moe_swiglu_backward, moe_combine of the row gradients; then moe_adamw_step.
+ * The conventions above hold. Row strides (ld_*) are in values. The pages
+ * have no counterpart of these calls.
+ */
+
+/*
+ * 16-bit rows of the valid pairs:
+ *   xe[src2dst[t,k], :] = x[t, :]; row_w[src2dst[t,k]] = topk_w[t,k]
+ * for t < *d_n_valid; the alignment gaps [psum[e], align(psum[e])) are zeroed
+ * (row_w too). Other rows are not written. Given dy it is the gradient of
+ * moe_combine's unweighted sum; its own gradient is moe_combine.
+ *   x        device 16-bit [T, ld_x >= H], H and the strides multiples of 8, K <= 32
+ *   topk_w   device fp32 [T, K], and row_w fp32 [M_cap]: row_w may be NULL
+ *   xe       device 16-bit [M_cap, ld_xe >= H]; x and xe 16-byte aligned
+ * A destination >= M_cap is skipped and sets MOE_ERR_DEVICE_CHECK.
+ */
+int moe_expand_rows(const uint16_t* x, int64_t ld_x, const float* topk_w, const int32_t* src2dst,
+                    const int32_t* psum, const int32_t* d_n_valid, int64_t T, int H, int K, int E,
+                    int align, int64_t M_cap, uint16_t* xe, int64_t ld_xe, float* row_w,
+                    int32_t* d_status, moe_stream_t stream);
+
+/* Per-row values (the gradient of row_w) back to their pairs:
+ *   out[t,k] = src2dst[t,k] >= 0 ? rows[src2dst[t,k]] : 0   for t < *d_n_valid
+ * rows fp32 [M_cap], out fp32 [T, K]; K <= 32. */
+int moe_collect_row_grads(const float* rows, const int32_t* src2dst, const int32_t* d_n_valid,
+                          int64_t T, int K, int64_t M_cap, float* out, moe_stream_t stream);
+
+/*
+ * Products of the experts over their rows r in [start[e], psum[e]):
+ *   moe_grouped_mm        out[r, n] = sum_k x[r, k] w[e, n, k]
+ *   moe_grouped_mm_dgrad  dx[r, k]  = sum_n dy[r, n] w[e, n, k]
+ *   moe_grouped_mm_wgrad  dw[e, n, k] (+)= sum_r dy[r, n] x[r, k]
+ * Sums in fp32, each result rounded once. Rows outside the segments are
+ * neither used nor written, whatever they hold. Segments are read on the
+ * device and clamped to [0, M_cap]; they need not be aligned.
+ *   dtype    MOE_BF16 or MOE_F16, of every operand and of out / dx
+ *   w        [E, N, Kd] contiguous; x, out, dy, dx row-major with row strides
+ *   dw       [E, N, Kd] contiguous, out_dtype = dtype or MOE_F32; accumulate:
+ *            added to what it holds (an expert without rows is left as it is),
+ *            else overwritten (zeros for an expert without rows)
+ * N, Kd and the row strides are multiples of 8, pointers 16-byte aligned,
+ * E <= 1024. M_cap = 0 is allowed (row pointers may then be NULL).
+ */
+int moe_grouped_mm(const void* x, int64_t ld_x, const void* w, const int32_t* start,
+                   const int32_t* psum, int dtype, int E, int N, int Kd, int64_t M_cap, void* out,
+                   int64_t ld_out, int32_t* d_status, moe_stream_t stream);
+int moe_grouped_mm_dgrad(const void* dy, int64_t ld_dy, const void* w, const int32_t* start,
+                         const int32_t* psum, int dtype, int E, int N, int Kd, int64_t M_cap,
+                         void* dx, int64_t ld_dx, int32_t* d_status, moe_stream_t stream);
+int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                         const int32_t* start, const int32_t* psum, int dtype, int E, int N, int Kd,
+                         int64_t M_cap, void* dw, int out_dtype, int accumulate, int32_t* d_status,
+                         moe_stream_t stream);
+
+/*
+ * SwiGLU with the row's weight, rows r < *d_total of gu = [g | u]:
+ *   h = silu(g) u w_r                             (row_w NULL: w = 1)
+ * and its gradient, s = sigmoid(g):
+ *   dg = dh w u s (1 + g (1 - s)), du = dh w g s, drow_w[r] = sum_i dh g s u
+ * in fp32, rounded once; drow_w is fp32 (NULL: not computed). A row depends
+ * on that row alone. dgu may be gu itself (same stride).
+ *   gu, dgu  [M_cap, ld >= 2I], dh, h [M_cap, ld >= I] of dtype; I and the
+ *            strides multiples of 8, pointers 16-byte aligned
+ */
+int moe_swiglu(const void* gu, int64_t ld_gu, int dtype, int I, const float* row_w,
+               const int32_t* d_total, int64_t M_cap, void* h, int64_t ld_h, moe_stream_t stream);
+int moe_swiglu_backward(const void* dh, int64_t ld_dh, const void* gu, int64_t ld_gu, int dtype,
+                        int I, const float* row_w, const int32_t* d_total, int64_t M_cap, void* dgu,
+                        int64_t ld_dgu, float* drow_w, moe_stream_t stream);
+
+/* One tensor of an AdamW step. All pointers are device memory, any alignment
+ * that fits the type (16 bytes is the fast one). */
+typedef struct {
+  void* p;          /* parameter, updated */
+  const void* g;    /* gradient */
+  void* copy;       /* the new parameter in copy_type, or NULL */
+  void* m;          /* first moment: fp32 [n], or e4m3 codes [n] */
+  void* v;          /* second moment: fp32 [n], or the codes of its root [n] */
+  float* m_scale;   /* 8-bit states: fp32 [ceil(n/128)] */
+  float* v_scale;
+  int64_t n;
+  int32_t p_type, g_type, copy_type; /* MOE_BF16, MOE_F16 or MOE_F32 */
+  int32_t reserved;
+} moe_adamw_tensor;
+
+/*
+ * AdamW over `count` tensors (host array, read before the call returns), in
+ * one launch per 400 of them:
+ *   g' = *d_grad_scale g (NULL: g);  m = b1 m + (1-b1) g';  v = b2 v + (1-b2) g'^2
+ *   p = p (1 - lr wd) - lr/(1-b1^step) m / (sqrt(v)/sqrt(1-b2^step) + eps)
+ * in fp32; p is rounded to its type, copy is rounded from the fp32 result.
+ * state_bits 32: m and v in fp32. 8: m and sqrt(v) as e4m3 codes with a scale
+ * amax/448 per 128 values; the step uses them before they are rounded, a
+ * positive sqrt(v) never becomes zero, a block below 1e-30 becomes zeros. A
+ * gradient that is not finite spoils its value, and with 8-bit states what
+ * shares its block of 128 after this step.
+ * step counts from 1.
+ */
+int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int state_bits, double lr,
+                   double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                   const float* d_grad_scale, moe_stream_t stream);
 
 /* Host. Diagnostics: when d_trace is not NULL, every later grouped-GEMM
  * launch (moe_grouped_gemm, moe_grouped_gemm_act_quant) writes 8 uint64
