@@ -28,10 +28,23 @@
 // Accumulation is in fp32 in tensor memory over the whole contraction; each
 // result is rounded once.
 //
-// One persistent CTA per SM, warp-specialised as in grouped_gemm.cu: warp 0
+// Persistent CTAs, one per SM, warp-specialised as in grouped_gemm.cu: warp 0
 // TMA producer, warp 1 tcgen05.mma issuer, warp 2 zeroes ragged rows (wgrad),
-// warps 4-7 epilogue. Two 256-column accumulators let the epilogue of a tile
-// run under the next tile's products.
+// warps 4-11 epilogue. Two 256-column accumulators let the epilogue of a tile
+// run under the next tile's products. Two CTAs work on one 256 x 256 tile
+// (cta_group::2): each loads half of both operands, so a 64-deep block costs an
+// SM 32 KB instead of 48. With one CTA per 128 x 256 tile a block took 705
+// cycles (1024 rows an expert, 4096 x 4096, forward), with pairs 558; the
+// tensor core's own time is 512. Experts with few rows take the single-CTA
+// form, whose tile wastes less on them.
+//
+// What bounds it: power. Forward and dgrad run at 1.6 PFLOP/s with the SM clock
+// held near 1.4 GHz by the power limit, 92-97 % of what the library's product
+// of the same rows and weights reaches there. wgrad (both operands i/j-contiguous)
+// is bound by the rate at which the tensor core reads such an A: 668 cycles a
+// block on long segments, against 531 for the others.
+#include <atomic>
+
 #include "common.cuh"
 #include "dtype16.cuh"
 #include "gemm_host.h"
@@ -40,31 +53,46 @@
 namespace moe {
 namespace {
 
+
 enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int BM = 128;          // rows of D per tile
+constexpr int BMC = 128;         // rows of D per CTA
 constexpr int BN = 256;          // columns of D per tile
 constexpr int BC = 64;           // contracted per stage: one 128-byte swizzle row of 16-bit values
 constexpr int kUmmaK = 16;       // contracted per tcgen05.mma
-constexpr int kStages = 4;
-constexpr int kABytes = BM * BC * 2;
-constexpr int kBBytes = BN * BC * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kPanel = 64 * 128;   // 64 rows of 128 bytes: one TMA box of an i/j-contiguous operand
+constexpr int kPanel = 64 * 128; // 64 rows of 128 bytes: one TMA box of an i/j-contiguous operand
 constexpr int kAcc = 2;
 constexpr int kTmemCols = kAcc * BN;
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 256;
+constexpr int kEpiWarps = 8;     // two per TMEM lane quarter
+constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kMaxE = 1024;
-constexpr int kRaster = 8;       // tiles in a column of the raster (see tile_at)
+constexpr int kRaster = 8;       // row tiles in a column of the raster (see tile_at)
 
-constexpr int kStoreOffset = kStages * kStageBytes;             // per epilogue warp: 32 rows x 128 bytes
-constexpr int kBarOffset = kStoreOffset + kEpiWarps * 32 * 128;
-constexpr int kNumBars = 3 * kStages + 2 * kAcc + 1;
-constexpr int kMiscOffset = kBarOffset + kNumBars * 8;          // tmem slot, abort flag
-constexpr int kTableOffset = (kMiscOffset + 8 + 15) / 16 * 16;  // tile prefix [E+1], start [E], end [E]
-constexpr int smem_bytes(int E) { return 1024 + kTableOffset + (3 * E + 1) * 4; }
-static_assert(smem_bytes(kMaxE) <= 227 * 1024, "shared memory");
+// kCtas CTAs work on one tile of kCtas * 128 x 256.
+template <int kMode, int kCtas, bool Out16 = true>
+struct Cfg {
+  // Results leave through shared memory and TMA, except for the single-CTA
+  // forward and dgrad, which serve experts with few rows (see the epilogue).
+  static constexpr bool kTmaStore = kCtas == 2 || kMode == kWgrad;
+  static constexpr int BM = kCtas * BMC;
+  static constexpr int kBRows = BN / kCtas;             // columns of D whose operand this CTA loads
+  static constexpr int kABytes = BMC * BC * 2;
+  static constexpr int kBBytes = kBRows * BC * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  // Of a row of D, staged at a time: 64 bytes leave room for six stages (at
+  // 1024 ragged rows an expert and 4096 x 4096 weights wgrad took 767 cycles a
+  // block so, 785 with five stages and 128 bytes; forward 558 and 577). fp32
+  // rows take 128, so that a piece is 32 columns in either type.
+  static constexpr int kPieceBytes = Out16 ? 64 : 128;
+  static constexpr int kStages = kCtas == 2 ? (Out16 ? 6 : 5) : (kTmaStore ? 3 : 4);
+  static constexpr int kStoreOffset = kStages * kStageBytes;   // per epilogue warp: 32 rows of a piece
+  static constexpr int kBarOffset = kStoreOffset + (kTmaStore ? kEpiWarps * 32 * kPieceBytes : 0);
+  static constexpr int kNumBars = 4 * kStages + 2 * kAcc + 1;
+  static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;          // tmem slot, abort flag
+  static constexpr int kTableOffset = (kMiscOffset + 8 + 15) / 16 * 16;  // prefix [E+1], start, end [E]
+  static constexpr int smem_bytes(int E) { return 1024 + kTableOffset + (3 * E + 1) * 4; }
+  static_assert(1024 + kTableOffset + (3 * kMaxE + 1) * 4 <= 227 * 1024, "shared memory");
+};
 
 struct Params {
   const int32_t* start;
@@ -73,6 +101,7 @@ struct Params {
   int64_t M_cap;
   void* out;             // forward [M_cap, ld_out = N..], dgrad [M_cap, Kd..], wgrad [E, N, Kd]
   int64_t ld_out;
+  int wide;              // rows of out begin on 32-byte boundaries
   int32_t* status;
 };
 
@@ -97,36 +126,218 @@ constexpr uint32_t idesc_f16(bool half, bool a_mn, bool b_mn, int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, K = 16.
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, K = 16. kCtas = 2: issued
+// by the pair's first CTA; each CTA's shared memory holds its half of A's rows
+// and of B's, each CTA's TMEM its half of D's rows.
+template <int kCtas>
 MOE_DEV void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (kCtas == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-MOE_DEV void tma_load_3d(void* dst, const CUtensorMap* tm, int32_t x, int32_t y, int32_t z,
-                         uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
+// Arrive once on `bar` (kCtas = 2: on the barrier at this place in both CTAs)
+// when the MMAs issued so far have completed.
+template <int kCtas>
+MOE_DEV void tc_commit_all(uint64_t* bar) {
+  if constexpr (kCtas == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+template <int kCtas>
+MOE_DEV void tc_commit_own(uint64_t* bar) {
+  if constexpr (kCtas == 1)
+    tc_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
 }
 
-MOE_DEV void tc_wait32(uint32_t (&v)[32]) {
+template <int kCtas>
+MOE_DEV void tmem_alloc_n(uint32_t* slot, uint32_t ncols) {
+  if constexpr (kCtas == 1) {
+    tmem_alloc(slot, ncols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(slot)),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int kCtas>
+MOE_DEV void tmem_dealloc_n(uint32_t taddr, uint32_t ncols) {
+  if constexpr (kCtas == 1)
+    tmem_dealloc(taddr, ncols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
+}
+
+// Address of the same shared-memory place in the pair's CTA of that rank.
+MOE_DEV uint32_t cta_smem(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+MOE_DEV uint32_t leader_smem(const void* p) { return cta_smem(p, 0); }
+// Arrive on a barrier of the pair's first CTA. The relaxed form is for a
+// thread whose only business with the waiter is TMEM it has read (the loads
+// are complete after tcgen05.wait::ld): a release would first wait for the
+// thread's global stores to be visible, which has nothing to do with it.
+MOE_DEV void mbar_arrive_leader(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_smem(bar))
+               : "memory");
+}
+MOE_DEV void mbar_arrive_leader_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_smem(bar))
+               : "memory");
+}
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// mbar_wait for a barrier that threads of the other CTA arrive on after
+// writing shared memory of their own that this thread's MMAs read.
+MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSleepNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort = 1;
+      set_status(status, MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// TMA loads whose bytes are counted on `bar` (a shared::cluster address): a
+// barrier of this CTA, or (kCtas = 2) of the pair's first.
+template <int kCtas>
+MOE_DEV void load_2d(void* dst, const CUtensorMap* tm, int32_t x, int32_t y, uint32_t bar) {
+  if constexpr (kCtas == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int kCtas>
+MOE_DEV void load_3d(void* dst, const CUtensorMap* tm, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  if constexpr (kCtas == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// TMA store (kAdd: addition in fp32, done by L2) of a staged 128-byte-wide
+// piece; places past the tensor are not written.
+template <bool kAdd>
+MOE_DEV void tma_store_3d(const CUtensorMap* tm, uint32_t src, int32_t x, int32_t y, int32_t z) {
+  if constexpr (kAdd)
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(src)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(src)
+        : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The staged pieces have been read (may be overwritten) / the stores are done.
+MOE_DEV void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+MOE_DEV void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A 32-byte sector of a row of D that has `left` more values (a multiple of 8
+// 16-bit values or of 8 fp32 ones; <= 0: none), `per` values a sector. wide:
+// rows begin on 32-byte boundaries, so a thread moves a whole sector at once.
+MOE_DEV void store_sector(uint8_t* a, const uint32_t* v, int left, int per, int wide) {
+  if (left >= per && wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    if (left > 0) *reinterpret_cast<uint4*>(a) = make_uint4(v[0], v[1], v[2], v[3]);
+    if (left >= per) *reinterpret_cast<uint4*>(a + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+MOE_DEV void load_sector(const uint8_t* a, uint32_t* v, int left, int per, int wide) {
+  if (left >= per && wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "l"(a)
+                 : "memory");
+  } else {
+    if (left > 0) {
+      const uint4 x = *reinterpret_cast<const uint4*>(a);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    }
+    if (left >= per) {
+      const uint4 x = *reinterpret_cast<const uint4*>(a + 16);
+      v[4] = x.x; v[5] = x.y; v[6] = x.z; v[7] = x.w;
+    }
+  }
+}
+
+// 32 TMEM lanes x 32 columns, waited for.
+MOE_DEV void tc_ld32_wait(uint32_t taddr, uint32_t (&v)[32]) {
+  tc_ld32(taddr, v);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   tc_regs_landed(v);
 }
 
-MOE_DEV void drain_wait(uint64_t* bar, uint32_t parity) {
+// Bounded wait used while draining: no abort check, only the time limit.
+MOE_DEV bool drain_wait(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
-    if (clock64() - t0 > kWaitLimitCycles) return;
+    if (clock64() - t0 > kWaitLimitCycles) return false;
   }
+  return true;
 }
 
 struct Tile {
@@ -136,63 +347,72 @@ struct Tile {
 
 // Out16: D is stored in the operands' type, else (wgrad) in fp32. Add: D is
 // added to what `out` holds.
-template <int kMode, bool Half, bool Out16, bool Add>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kMode, bool Half, bool Out16, bool Add, int kCtas>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     grouped_mm16_kernel(const __grid_constant__ CUtensorMap tmA,
-                        const __grid_constant__ CUtensorMap tmB, const Params p) {
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmD, const Params p) {
+  using C = Cfg<kMode, kCtas, Out16>;
+  constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
+  // the same offset in both CTAs of a pair: their windows begin alike
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOffset);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
   uint64_t* empty = full + kStages;
-  uint64_t* clean = empty + kStages;    // wgrad: the stage's ragged rows are zero
-  uint64_t* tfull = clean + kStages;
+  // wgrad, a tile's ragged block: it has landed in this CTA; its ragged rows
+  // are zero in every CTA of the tile
+  uint64_t* rlanded = empty + kStages;
+  uint64_t* rzeroed = rlanded + kStages;
+  uint64_t* tfull = rzeroed + kStages;
   uint64_t* tempty = tfull + kAcc;
   uint64_t* mma_done = tempty + kAcc;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOffset);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOffset + 4);
-  int* s_tp = reinterpret_cast<int*>(smem + kTableOffset);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOffset);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOffset + 4);
+  int* s_tp = reinterpret_cast<int*>(smem + C::kTableOffset);
   int* s_start = s_tp + p.E + 1;
   int* s_end = s_start + p.E;
   __shared__ int s_warp_sum[kThreads / 32];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = kCtas == 1 ? 0 : static_cast<int>(blockIdx.x % kCtas);   // in the pair
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kMode == kWgrad ? 2 : 1);   // MMA (and the zeroing warp)
-      mbar_init(&clean[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&rlanded[s], 1);
+      mbar_init(&rzeroed[s], kCtas);
     }
     for (int b = 0; b < kAcc; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], kEpiWarps);
+      mbar_init(&tempty[b], kCtas * kEpiWarps);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
+    if (C::kTmaStore) prefetch_tmap(&tmD);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_n<kCtas>(tmem_slot, kTmemCols);
   // Segments, clamped into the buffer, and (forward, dgrad) the prefix of
-  // their row tiles: thread t owns experts 4t .. 4t+3.
+  // their row tiles: thread t owns experts kPer t .. kPer t + kPer - 1.
   {
-    int mine = 0, cnt[4] = {0, 0, 0, 0};
+    constexpr int kPer = (kMaxE + kThreads - 1) / kThreads;
+    int mine = 0, cnt[kPer];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = threadIdx.x * 4 + j;
+    for (int j = 0; j < kPer; ++j) {
+      const int e = threadIdx.x * kPer + j;
+      cnt[j] = 0;
       if (e < p.E) {
         const int cap = static_cast<int>(p.M_cap);
         const int a = min(max(p.start[e], 0), cap);
         const int b = min(max(p.psum[e], a), cap);
         s_start[e] = a;
         s_end[e] = b;
-        cnt[j] = (b - a + BM - 1) / BM;
+        cnt[j] = (b - a + C::BM - 1) / C::BM;
         mine += cnt[j];
       }
     }
@@ -207,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int base = incl - mine;
     for (int w = 0; w < warp; ++w) base += s_warp_sum[w];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = threadIdx.x * 4 + j;
+    for (int j = 0; j < kPer; ++j) {
+      const int e = threadIdx.x * kPer + j;
       if (e < p.E) {
         s_tp[e] = base;
         base += cnt[j];
@@ -218,14 +438,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (kCtas > 1) cluster_sync();   // the other CTA's barriers exist, its TMEM too
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   // D's columns, its column tiles and (wgrad) row tiles
   const int cols = kMode == kForward ? p.N : p.Kd;
   const int nj = (cols + BN - 1) / BN;
-  const int ni_w = (p.N + BM - 1) / BM;
+  const int ni_w = (p.N + C::BM - 1) / C::BM;
   const int num_tiles = kMode == kWgrad ? p.E * ni_w * nj : s_tp[p.E] * nj;
+  const int first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
 
   // Tile id -> tile. Within an expert the tiles go in columns of kRaster row
   // tiles, row tile fastest, so the CTAs that run at one time share both
@@ -251,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = l / (kRaster * nj);
     const int in = l - g * kRaster * nj;
     const int gi = min(kRaster, ni - g * kRaster);
-    t.i0 = (g * kRaster + in % gi) * BM;
+    t.i0 = (g * kRaster + in % gi) * C::BM;
     t.j0 = (in / gi) * BN;
     t.row0 = s_start[t.e];
     t.rows = s_end[t.e] - t.row0;
@@ -265,56 +487,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
-    int stage = 0, issued = 0;
+    // Both CTAs' bytes are counted on the first CTA's barrier, those of a
+    // ragged block on each CTA's own, for the warp that zeroes rows there.
+    constexpr int kGroup = kCtas;
+    int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
+    for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
       const Tile t = tile_at(tile);
       const int nb = num_blocks(t);
       const int rag = ragged(t);
+      const int i0 = t.i0 + rank * BMC, j0 = t.j0 + rank * C::kBRows;
       for (int b = 0; b < nb; ++b) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-        uint8_t* sa = smem + stage * kStageBytes;
-        uint8_t* sb = sa + kABytes;
-        mbar_arrive_expect_tx(&full[stage], kStageBytes);
+        uint8_t* sa = smem + stage * C::kStageBytes;
+        uint8_t* sb = sa + C::kABytes;
+        uint32_t bar;
+        if (kMode == kWgrad && rag && b == 0) {
+          mbar_arrive_expect_tx(&rlanded[stage], C::kStageBytes);
+          bar = kCtas == 1 ? smem_u32(&rlanded[stage]) : cta_smem(&rlanded[stage], rank);
+        } else {
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], kCtas * C::kStageBytes);
+          bar = kCtas == 1 ? smem_u32(&full[stage]) : cta_smem(&full[stage], 0);
+        }
         if (kMode == kForward) {
-          tma_load_2d(sa, &tmA, b * BC, t.row0 + t.i0, &full[stage]);
-          tma_load_3d(sb, &tmB, b * BC, t.j0, t.e, &full[stage]);
+          load_2d<kGroup>(sa, &tmA, b * BC, t.row0 + i0, bar);
+          load_3d<kGroup>(sb, &tmB, b * BC, j0, t.e, bar);
         } else if (kMode == kDgrad) {
-          tma_load_2d(sa, &tmA, b * BC, t.row0 + t.i0, &full[stage]);
+          load_2d<kGroup>(sa, &tmA, b * BC, t.row0 + i0, bar);
 #pragma unroll
-          for (int q = 0; q < BN / 64; ++q)
-            tma_load_3d(sb + q * kPanel, &tmB, t.j0 + q * 64, b * BC, t.e, &full[stage]);
+          for (int q = 0; q < C::kBRows / 64; ++q)
+            load_3d<kGroup>(sb + q * kPanel, &tmB, j0 + q * 64, b * BC, t.e, bar);
         } else {
           // the ragged block first: it is the segment's last
           const int c = rag ? (b == 0 ? t.rows - rag : (b - 1) * BC) : b * BC;
 #pragma unroll
-          for (int q = 0; q < BM / 64; ++q)
-            tma_load_2d(sa + q * kPanel, &tmA, t.i0 + q * 64, t.row0 + c, &full[stage]);
+          for (int q = 0; q < BMC / 64; ++q)
+            load_2d<kGroup>(sa + q * kPanel, &tmA, i0 + q * 64, t.row0 + c, bar);
 #pragma unroll
-          for (int q = 0; q < BN / 64; ++q)
-            tma_load_2d(sb + q * kPanel, &tmB, t.j0 + q * 64, t.row0 + c, &full[stage]);
+          for (int q = 0; q < C::kBRows / 64; ++q)
+            load_2d<kGroup>(sb + q * kPanel, &tmB, j0 + q * 64, t.row0 + c, bar);
         }
-        ++issued;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
-    // Let the last loads land before the CTA can exit.
-    const int outstanding = issued < kStages ? issued : kStages;
-    for (int i = 1; i <= outstanding; ++i) {
-      int s = stage - i;
-      uint32_t ph = phase;
-      if (s < 0) { s += kStages; ph ^= 1u; }
-      drain_wait(&full[s], ph);
+    // Every load has landed before the CTA can exit: the tensor core has
+    // consumed (released) each stage once more. After a wait that gave up,
+    // this one is bounded too.
+    for (int i = 0; i < kStages; ++i) {
+      if (!drain_wait(&empty[stage], phase ^ 1u)) break;
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && lane == 0 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc = idesc_f16(Half, kMode == kWgrad, kMode != kForward, BM, BN);
+    constexpr uint32_t idesc = idesc_f16(Half, kMode == kWgrad, kMode != kForward, C::BM, BN);
     int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    uint32_t clean_phase[kStages] = {};
+    uint32_t acc_phase = 0;
+    uint32_t full_phase = 0, rag_phase = 0;   // a bit per stage: uses so far
     bool ok = true;
-    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
+    for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
       const Tile t = tile_at(tile);
       const int nb = num_blocks(t);
       if (nb == 0) continue;   // wgrad of an expert without rows: the epilogue stores zeros
@@ -322,190 +553,226 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) break;
       const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
       for (int b = 0; b < nb; ++b) {
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
-        int steps = BC / kUmmaK;
-        if (kMode == kWgrad && rag && b == 0) {
-#pragma unroll
-          for (int s = 0; s < kStages; ++s)
-            if (s == stage) {
-              ok = mbar_wait(&clean[s], clean_phase[s], abort_flag, p.status);
-              clean_phase[s] ^= 1u;
-            }
-          if (!ok) break;
-          steps = (rag + kUmmaK - 1) / kUmmaK;
-        }
+        const bool ragged_block = kMode == kWgrad && rag && b == 0;
+        uint64_t* landed = ragged_block ? &rzeroed[stage] : &full[stage];
+        uint32_t& uses = ragged_block ? rag_phase : full_phase;
+        ok = ragged_block && kCtas > 1 ? mbar_wait_cluster(landed, (uses >> stage) & 1u, abort_flag, p.status)
+                                       : mbar_wait(landed, (uses >> stage) & 1u, abort_flag, p.status);
+        if (!ok) break;
+        uses ^= 1u << stage;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + stage * kStageBytes);
-        const uint32_t sb = sa + kABytes;
-        for (int k = 0; k < steps; ++k) {
-          // 16 contracted values on: 32 bytes along a c-contiguous row, 16
-          // rows of 128 bytes otherwise
+        const uint32_t sa = smem_u32(smem + stage * C::kStageBytes);
+        const uint32_t sb = sa + C::kABytes;
+        // 16 contracted values on: 32 bytes along a c-contiguous row, 16 rows
+        // of 128 bytes otherwise
+        auto step = [&](int k) {
           const uint64_t da = kMode == kWgrad ? sw128_mnmajor_desc(sa + k * kUmmaK * 128)
                                               : sw128_kmajor_desc(sa + k * kUmmaK * 2);
           const uint64_t db = kMode != kForward ? sw128_mnmajor_desc(sb + k * kUmmaK * 128)
                                                 : sw128_kmajor_desc(sb + k * kUmmaK * 2);
-          tc_mma_f16(d, da, db, idesc, (b > 0 || k > 0) ? 1u : 0u);
+          tc_mma_f16<kCtas>(d, da, db, idesc, (b > 0 || k > 0) ? 1u : 0u);
+        };
+        if (ragged_block) {
+          for (int k = 0; k < (rag + kUmmaK - 1) / kUmmaK; ++k) step(k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < BC / kUmmaK; ++k) step(k);
         }
-        tc_commit(&empty[stage]);
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        tc_commit_all<kCtas>(&empty[stage]);
+        if (++stage == kStages) stage = 0;
       }
       if (!ok) break;
-      tc_commit(&tfull[acc]);
+      tc_commit_all<kCtas>(&tfull[acc]);
       if (++acc == kAcc) { acc = 0; acc_phase ^= 1u; }
     }
     // Every MMA issued so far must complete before TMEM is released.
-    tc_commit(mma_done);
+    tc_commit_own<kCtas>(mma_done);
     drain_wait(mma_done, 0);
   } else if (warp == 2 && kMode == kWgrad) {
     // ------------------------------------------------- ragged rows to zero
     // Only the rows up to the next multiple of 16 are read by the tensor core.
-    // The warp follows every block and has its own arrival on `empty`: a
-    // parity wait is sound only for a waiter that is never two phases away.
     int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
+    uint32_t uses = 0;   // a bit per stage
+    for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
       const Tile t = tile_at(tile);
-      const int nb = num_blocks(t);
       const int rag = ragged(t);
-      for (int b = 0; b < nb; ++b) {
-        if (!mbar_wait_warp(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
-        if (rag && b == 0) {
-          const int r1 = (rag + kUmmaK - 1) / kUmmaK * kUmmaK;
-          uint8_t* s = smem + stage * kStageBytes;
-          const int per_panel = (r1 - rag) * 8;   // 16-byte vectors
-          for (int q = 0; q < (BM + BN) / 64; ++q)
-            for (int v = lane; v < per_panel; v += 32)
-              *reinterpret_cast<uint4*>(s + q * kPanel + rag * 128 + v * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&clean[stage]);
+      if (rag) {
+        if (!mbar_wait_warp(&rlanded[stage], (uses >> stage) & 1u, abort_flag, p.status)) break;
+        uses ^= 1u << stage;
+        const int r1 = (rag + kUmmaK - 1) / kUmmaK * kUmmaK;
+        uint8_t* s = smem + stage * C::kStageBytes;
+        const int per_panel = (r1 - rag) * 8;   // 16-byte vectors
+        for (int q = 0; q < C::kStageBytes / kPanel; ++q)
+          for (int v = lane; v < per_panel; v += 32)
+            *reinterpret_cast<uint4*>(s + q * kPanel + rag * 128 + v * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 1) mbar_arrive(&rzeroed[stage]); else mbar_arrive_leader(&rzeroed[stage]);
         }
-        if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
+      stage = (stage + num_blocks(t)) % kStages;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    // A warp owns 32 rows of D (its TMEM lanes): it reads 32 or 64 columns,
-    // converts, passes them through shared memory (swizzled, so that neither
-    // side has bank conflicts) and stores whole row pieces. Where 16-bit
-    // results are added to, the pieces stay in fp32 until after the addition,
-    // so that the sum is rounded once.
+    // A thread owns one row of D (its TMEM lane) and 128 columns, in pieces of
+    // 32. A warp whose 32 rows are all D's (always in wgrad; in forward and
+    // dgrad all but a segment's last) stages a piece in shared memory
+    // (swizzled: no bank conflicts) and one TMA store takes it out; fp32
+    // results that are added to `out` are added by that store, in L2. The
+    // other rows go straight from registers, a 32-byte sector per thread, as
+    // do 16-bit results that are added to, whose sum is rounded once: their
+    // old values are asked for before the tile's products are waited for, or
+    // kAhead pieces early. Stores from registers alone slowed the products:
+    // with 1024 rows an expert and 4096 x 4096 weights wgrad took 930 cycles a
+    // block of 64 rows with them, 738 with TMA stores, 750 with no stores at all.
     const int quarter = warp & 3;
-    const uint32_t stg = smem_u32(smem + kStoreOffset + quarter * 32 * 128);
+    const int half_cols = ((warp - 4) >> 2) * (BN / 2);
     constexpr int kElem = Out16 ? 2 : 4;
-    constexpr bool kStage16 = Out16 && !Add;
-    constexpr int kCols = kStage16 ? 64 : 32;   // columns of D per staged 128-byte row piece
-    constexpr int kVec = kCols / 8;             // columns per staged 16-byte vector
+    constexpr bool kAddHere = Add && Out16;     // added in registers
+    constexpr bool kTma = C::kTmaStore && !kAddHere;
+    constexpr int kPiece = C::kPieceBytes;      // 64 or 128
+    constexpr int kWords = kPiece / 4;
+    constexpr int kCols = 32;                   // columns of D per piece
+    static_assert(kPiece == kCols * kElem, "a piece is 32 columns");
+    constexpr int kPieces = BN / 2 / kCols;
+    const uint32_t stg = smem_u32(smem + C::kStoreOffset + (warp - 4) * 32 * kPiece);
+    constexpr int kAhead = kAddHere ? 2 : 1;
+    constexpr int kSector = 32 / kElem;         // columns of a 32-byte sector
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+    for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
       const Tile t = tile_at(tile);
       const bool empty_tile = num_blocks(t) == 0;
       if (empty_tile && Add) continue;
+      const int ilim = kMode == kWgrad ? p.N : t.rows;                // rows of D that exist
+      const int iw = t.i0 + rank * BMC + quarter * 32;                // this warp's first row
+      const int j = t.j0 + half_cols;                                 // and column
+      const bool by_tma = kTma && (kMode == kWgrad || iw + 32 <= ilim);
+      const int64_t orow = (kMode == kWgrad ? static_cast<int64_t>(t.e) * p.N : t.row0) + iw + lane;
+      uint8_t* out = static_cast<uint8_t*>(p.out) + (orow * p.ld_out + j) * kElem;
+      const int ncols = iw + lane < ilim ? cols - j : 0;              // columns to store from j on
+      uint32_t old[kAhead][kWords];
+      auto fetch = [&](int piece, uint32_t (&o)[kWords]) {
+#pragma unroll
+        for (int q = 0; q < kWords / 8; ++q)
+          load_sector(out + piece * kPiece + q * 32, &o[q * 8], ncols - piece * kCols - q * kSector,
+                      kSector, p.wide);
+      };
+      if constexpr (kAddHere) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) fetch(a, old[a]);
+      }
       if (!empty_tile) {
         if (!mbar_wait_warp(&tfull[acc], acc_phase, abort_flag, p.status)) break;
         tc_fence_after();
       }
       const uint32_t tq = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                          static_cast<uint32_t>(acc * BN);
-      const int ilim = kMode == kWgrad ? p.N : t.rows;   // rows of D that exist
-      const int iw = t.i0 + quarter * 32;                // this warp's first row
-      const int64_t orow = kMode == kWgrad ? static_cast<int64_t>(t.e) * p.N : t.row0;
-      uint8_t* out = static_cast<uint8_t*>(p.out);
-      for (int c0 = 0; c0 < BN; c0 += kCols) {
-        uint32_t w[32];   // the thread's row, 128 bytes
+                          static_cast<uint32_t>(acc * BN + half_cols);
+#pragma unroll
+      for (int piece = 0; piece < kPieces; ++piece) {
+        uint32_t w[kWords];   // the thread's row of the piece
         if (empty_tile) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = 0u;
-        } else if (kStage16) {
-          uint32_t va[32], vb[32];
-          tc_ld32(tq + c0, va);
-          tc_ld32(tq + c0 + 32, vb);
-          tc_wait64(va, vb);
+          for (int k = 0; k < kWords; ++k) w[k] = 0u;
+        } else if constexpr (Out16) {
+          uint32_t a[32];
+          tc_ld32_wait(tq + piece * kCols, a);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            w[i] = pack2<Half>(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1]));
-            w[16 + i] = pack2<Half>(__uint_as_float(vb[2 * i]), __uint_as_float(vb[2 * i + 1]));
+          for (int k = 0; k < 16; ++k) {
+            float x = __uint_as_float(a[2 * k]), y = __uint_as_float(a[2 * k + 1]);
+            if constexpr (kAddHere) {
+              const float2 was = unpack2<Half>(old[piece % kAhead][k]);
+              x += was.x;
+              y += was.y;
+            }
+            w[k] = pack2<Half>(x, y);
           }
         } else {
-          tc_ld32(tq + c0, w);
-          tc_wait32(w);
+          tc_ld32_wait(tq + piece * kCols, w);
         }
-        if (!empty_tile && c0 + kCols == BN) {   // the last read has landed
+        if (!empty_tile && piece == kPieces - 1) {   // the last read has landed
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[acc]);
-        }
-        if (t.j0 + c0 >= cols || iw >= ilim) continue;   // the same for the whole warp
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           stg + lane * 128 + ((c ^ (lane & 7)) << 4)),
-                       "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
-                       : "memory");
-        __syncwarp();
-        const int c = lane & 7;
-        const bool col_ok = t.j0 + c0 + c * kVec < cols;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          uint4 v;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(stg + r * 128 + ((c ^ (r & 7)) << 4))
-                       : "memory");
-          if (iw + r < ilim && col_ok) {
-            uint8_t* dst = out + ((orow + iw + r) * p.ld_out + t.j0 + c0 + c * kVec) * kElem;
-            if (Add) {
-              float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                            __uint_as_float(v.w)};
-              if (Out16) {
-                const uint2 o = *reinterpret_cast<const uint2*>(dst);
-                const float2 lo = unpack2<Half>(o.x), hi = unpack2<Half>(o.y);
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<Half>(lo.x + f[0], lo.y + f[1]),
-                                                            pack2<Half>(hi.x + f[2], hi.y + f[3]));
-              } else {
-                const float4 o = *reinterpret_cast<const float4*>(dst);
-                *reinterpret_cast<float4*>(dst) =
-                    make_float4(o.x + f[0], o.y + f[1], o.z + f[2], o.w + f[3]);
-              }
-            } else {
-              *reinterpret_cast<uint4*>(dst) = v;
-            }
+          if (lane == 0) {
+            if (kCtas == 1) mbar_arrive(&tempty[acc]); else mbar_arrive_leader_relaxed(&tempty[acc]);
           }
         }
-        __syncwarp();
+        if (by_tma) {
+          if (j + piece * kCols >= cols || iw >= ilim) continue;   // the same for the whole warp
+          if (lane == 0) tma_store_read();   // the warp's last piece has left the buffer
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < kPiece / 16; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             stg + lane * kPiece +
+                             ((c ^ (kPiece == 128 ? lane & 7 : (lane >> 1) & 3)) << 4)),
+                         "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                         : "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0)
+            tma_store_3d<Add>(&tmD, stg, j + piece * kCols, kMode == kWgrad ? iw : t.row0 + iw,
+                              kMode == kWgrad ? t.e : 0);
+        } else {
+#pragma unroll
+          for (int q = 0; q < kWords / 8; ++q)
+            store_sector(out + piece * kPiece + q * 32, &w[q * 8], ncols - piece * kCols - q * kSector,
+                         kSector, p.wide);
+          if constexpr (kAddHere)
+            if (piece + kAhead < kPieces) fetch(piece + kAhead, old[piece % kAhead]);
+        }
       }
       if (!empty_tile && ++acc == kAcc) { acc = 0; acc_phase ^= 1u; }
     }
+    if (kTma && lane == 0) tma_store_done();
   }
 
   tc_fence_before();
   __syncthreads();
+  if (kCtas > 1) cluster_sync();   // neither CTA leaves, or frees TMEM, under the other's work
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+    tmem_dealloc_n<kCtas>(tmem_base, kTmemCols);
   }
 }
 
-template <int kMode, bool Half, bool Out16, bool Add>
-int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, int64_t max_tiles,
-           cudaStream_t s) {
-  auto* kernel = grouped_mm16_kernel<kMode, Half, Out16, Add>;
-  static bool attr_set[64] = {};
+template <int kMode, bool Half, bool Out16, bool Add, int kCtas>
+int launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const Params& p,
+           int64_t max_tiles, cudaStream_t s) {
+  using C = Cfg<kMode, kCtas, Out16>;
+  auto* kernel = grouped_mm16_kernel<kMode, Half, Out16, Add, kCtas>;
+  // clusters of the device that run at one time (a GPC may have an SM without
+  // a partner), found once per device
+  static std::atomic<int> resident[64];
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+  if (dev < 0 || dev >= 64) dev = 0;
+  int n = resident[dev].load();
+  if (n == 0) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem_bytes(kMaxE)) != cudaSuccess)
+                             C::smem_bytes(kMaxE)) != cudaSuccess)
       return check_launch("cudaFuncSetAttribute(grouped_mm16_kernel)");
-    attr_set[dev] = true;
+    n = device_sm_count();
+    if (kCtas > 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(n / kCtas * kCtas));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = C::smem_bytes(kMaxE);
+      cudaLaunchAttribute at = {};
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = kCtas;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
+        return check_launch("cudaOccupancyMaxActiveClusters(grouped_mm16_kernel)");
+      if (n < 1) n = 1;
+    }
+    resident[dev].store(n);
   }
-  int64_t grid = device_sm_count();
-  if (grid > max_tiles) grid = max_tiles;
-  kernel<<<static_cast<unsigned>(grid), kThreads, smem_bytes(p.E), s>>>(ta, tb, p);
+  const int64_t grid = n < max_tiles ? n : max_tiles;
+  kernel<<<static_cast<unsigned>(grid * kCtas), kThreads, C::smem_bytes(p.E), s>>>(ta, tb, td, p);
   return check_launch("grouped_mm16_kernel");
 }
 
@@ -514,10 +781,10 @@ int check_sizes(const char* what, int dtype, int E, int N, int Kd, int64_t M_cap
   MOE_REQUIRE(E > 0 && E <= kMaxE, "%s: E must be in [1, 1024]", what);
   MOE_REQUIRE(N > 0 && N % 8 == 0 && Kd > 0 && Kd % 8 == 0,
               "%s: N and Kd must be positive multiples of 8", what);
-  MOE_REQUIRE(M_cap >= 0 && M_cap <= INT32_MAX - BM, "%s: bad M_cap", what);
+  MOE_REQUIRE(M_cap >= 0 && M_cap <= INT32_MAX - 256, "%s: bad M_cap", what);
   // linear tile ids are 32-bit
   const int64_t nj = (N > Kd ? N : Kd) / BN + 1;
-  MOE_REQUIRE((M_cap / BM + E) * nj <= INT32_MAX && static_cast<int64_t>(E) * (N / BM + 1) * nj <= INT32_MAX,
+  MOE_REQUIRE((M_cap / BMC + E) * nj <= INT32_MAX && static_cast<int64_t>(E) * (N / BMC + 1) * nj <= INT32_MAX,
               "%s: sizes exceed 32-bit tile numbers", what);
   return MOE_OK;
 }
@@ -549,9 +816,14 @@ int rows_times_weights(const char* what, bool dgrad, const void* a, int64_t ld_a
   }
   MOE_REQUIRE_DEVICE();
   if (M_cap == 0) return MOE_OK;
-  CUtensorMap ta, tb;
-  MOE_TRY(make_tmap_rows16(&ta, a, in, M_cap, ld_a, BM));
-  MOE_TRY(make_tmap_weights16(&tb, w, Kd, N, E, dgrad ? 64 : BN));
+  CUtensorMap ta, tb, td = {};
+  // A pair of CTAs per tile once the experts have 128 rows on average; fewer,
+  // and the second CTA of most pairs would have none.
+  const bool pair = M_cap > static_cast<int64_t>(E) * BMC;
+  const int bm = pair ? 2 * BMC : BMC;
+  MOE_TRY(make_tmap_rows16(&ta, a, in, M_cap, ld_a, BMC));
+  MOE_TRY(make_tmap_weights16(&tb, w, Kd, N, E, dgrad ? 64 : (pair ? BN / 2 : BN)));
+  if (pair) MOE_TRY(make_tmap_result(&td, out, false, width, M_cap, 1, ld_out, Cfg<kForward, 2>::kPieceBytes));
   Params p;
   p.start = start;
   p.psum = psum;
@@ -561,25 +833,35 @@ int rows_times_weights(const char* what, bool dgrad, const void* a, int64_t ld_a
   p.M_cap = M_cap;
   p.out = out;
   p.ld_out = ld_out;
+  p.wide = aligned(out, 32) && ld_out % 16 == 0;
   p.status = d_status;
-  const int64_t m_tiles = M_cap / BM + (E < M_cap ? E : M_cap);
+  const int64_t m_tiles = M_cap / bm + (E < M_cap ? E : M_cap);
   const int64_t tiles = m_tiles * ((width + BN - 1) / BN);
   const bool half = dtype == MOE_F16;
-  if (dgrad)
-    return half ? launch<kDgrad, true, true, false>(ta, tb, p, tiles, s)
-                : launch<kDgrad, false, true, false>(ta, tb, p, tiles, s);
-  return half ? launch<kForward, true, true, false>(ta, tb, p, tiles, s)
-              : launch<kForward, false, true, false>(ta, tb, p, tiles, s);
+  if (dgrad) {
+    if (pair)
+      return half ? launch<kDgrad, true, true, false, 2>(ta, tb, td, p, tiles, s)
+                  : launch<kDgrad, false, true, false, 2>(ta, tb, td, p, tiles, s);
+    return half ? launch<kDgrad, true, true, false, 1>(ta, tb, td, p, tiles, s)
+                : launch<kDgrad, false, true, false, 1>(ta, tb, td, p, tiles, s);
+  }
+  if (pair)
+    return half ? launch<kForward, true, true, false, 2>(ta, tb, td, p, tiles, s)
+                : launch<kForward, false, true, false, 2>(ta, tb, td, p, tiles, s);
+  return half ? launch<kForward, true, true, false, 1>(ta, tb, td, p, tiles, s)
+              : launch<kForward, false, true, false, 1>(ta, tb, td, p, tiles, s);
 }
 
-template <bool Half>
-int launch_wgrad(const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, int64_t tiles,
+template <bool Half, int kCtas>
+int launch_wgrad(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const Params& p,
                  bool out16, bool add, cudaStream_t s) {
+  const int64_t tiles = static_cast<int64_t>(p.E) * ((p.N + kCtas * BMC - 1) / (kCtas * BMC)) *
+                        ((p.Kd + BN - 1) / BN);
   if (out16)
-    return add ? launch<kWgrad, Half, true, true>(ta, tb, p, tiles, s)
-               : launch<kWgrad, Half, true, false>(ta, tb, p, tiles, s);
-  return add ? launch<kWgrad, Half, false, true>(ta, tb, p, tiles, s)
-             : launch<kWgrad, Half, false, false>(ta, tb, p, tiles, s);
+    return add ? launch<kWgrad, Half, true, true, kCtas>(ta, tb, td, p, tiles, s)
+               : launch<kWgrad, Half, true, false, kCtas>(ta, tb, td, p, tiles, s);
+  return add ? launch<kWgrad, Half, false, true, kCtas>(ta, tb, td, p, tiles, s)
+             : launch<kWgrad, Half, false, false, kCtas>(ta, tb, td, p, tiles, s);
 }
 
 }  // namespace
@@ -623,7 +905,9 @@ extern "C" int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x
     if (cudaMemsetAsync(dw, 0, bytes, s) != cudaSuccess) return check_launch("cudaMemsetAsync(dw)");
     return MOE_OK;
   }
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb, td;
+  MOE_TRY(make_tmap_result(&td, dw, out_dtype == MOE_F32, Kd, N, E, Kd,
+                           out_dtype == MOE_F32 ? 128 : Cfg<kWgrad, 2>::kPieceBytes));
   MOE_TRY(make_tmap_rows16(&ta, dy, N, M_cap, ld_dy, BC));
   MOE_TRY(make_tmap_rows16(&tb, x, Kd, M_cap, ld_x, BC));
   Params p;
@@ -635,9 +919,12 @@ extern "C" int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x
   p.M_cap = M_cap;
   p.out = dw;
   p.ld_out = Kd;
+  p.wide = aligned(dw, 32) && (Kd % 16 == 0 || out_dtype == MOE_F32);
   p.status = d_status;
-  const int64_t tiles = static_cast<int64_t>(E) * ((N + BM - 1) / BM) * ((Kd + BN - 1) / BN);
   const bool out16 = out_dtype != MOE_F32, add = accumulate != 0;
-  return dtype == MOE_F16 ? launch_wgrad<true>(ta, tb, p, tiles, out16, add, s)
-                          : launch_wgrad<false>(ta, tb, p, tiles, out16, add, s);
+  if (N > BMC)
+    return dtype == MOE_F16 ? launch_wgrad<true, 2>(ta, tb, td, p, out16, add, s)
+                            : launch_wgrad<false, 2>(ta, tb, td, p, out16, add, s);
+  return dtype == MOE_F16 ? launch_wgrad<true, 1>(ta, tb, td, p, out16, add, s)
+                          : launch_wgrad<false, 1>(ta, tb, td, p, out16, add, s);
 }

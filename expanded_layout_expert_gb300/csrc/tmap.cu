@@ -24,18 +24,21 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 16-bit values are moved as such, whatever they stand for.
+// 16-bit values are moved as such, whatever they stand for; fp32 is named so
+// that it can be added to.
 int make_tmap16(CUtensorMap* tm, const void* base, uint32_t rank, const cuuint64_t* dims,
-                const cuuint64_t* strides, const cuuint32_t* box) {
+                const cuuint64_t* strides, const cuuint32_t* box,
+                CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) {
     set_error("cuTensorMapEncodeTiled is not available from the driver");
     return MOE_ERR_CUDA;
   }
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims,
+  const CUresult r = enc(tm, type, rank, const_cast<void*>(base), dims,
                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     set_error("cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -60,6 +63,17 @@ int make_tmap_weights16(CUtensorMap* tm, const void* base, uint64_t Kd, uint64_t
   const cuuint64_t strides[2] = {Kd * 2, N * Kd * 2};
   const cuuint32_t box[3] = {64u, box_n, 1u};
   return make_tmap16(tm, base, 3, dims, strides, box);
+}
+
+int make_tmap_result(CUtensorMap* tm, void* base, bool f32, uint64_t width, uint64_t rows, uint64_t E,
+                     uint64_t ld, uint32_t box_bytes) {
+  const uint64_t size = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {width, rows, E};
+  const cuuint64_t strides[2] = {ld * size, rows * ld * size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / size), 32u, 1u};
+  return make_tmap16(tm, base, 3, dims, strides, box,
+                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                     box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int make_tmap_k128(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
