@@ -90,6 +90,8 @@ def library_path() -> str:
 def load():
     """The loaded library; raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB

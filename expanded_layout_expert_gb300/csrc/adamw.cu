@@ -20,11 +20,10 @@
 // Bytes a value: 8 (p) + 2|4 (g) + 16 (fp32 m, v) or 4 + 16/128 (8 bits) + 2
 // (copy): bound by HBM. A warp takes 128 consecutive values, 4 per lane (16
 // bytes of each fp32 array), which is also one scale block, so its largest
-// values are two warp reductions. The tensors' table is a kernel parameter:
+// magnitudes are two warp reductions. The tensors' table is a kernel parameter:
 // nothing is copied to the device before the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <cmath>
 
@@ -122,49 +121,61 @@ MOE_DEV void store4(void* a, int type, int64_t i, int64_t n, bool vec, const flo
   }
 }
 
-MOE_DEV void load_codes(const void* a, int64_t i, int64_t n, bool vec, float scale, float (&f)[4]) {
-  const uint8_t* s = static_cast<const uint8_t*>(a) + i;
-  uint8_t c[4] = {0, 0, 0, 0};
-  if (vec) {
-    const uchar4 t = *reinterpret_cast<const uchar4*>(s);
-    c[0] = t.x; c[1] = t.y; c[2] = t.z; c[3] = t.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + j < n) c[j] = s[j];
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    __nv_fp8_e4m3 q;
-    q.__x = c[j];
-    f[j] = __fmul_rn(static_cast<float>(q), scale);
-  }
+// Four e4m3 codes (low byte first) as fp32, exactly: through fp16, which holds
+// every e4m3 value.
+MOE_DEV void decode4(uint32_t codes, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(codes)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(codes >> 16)));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+MOE_DEV uint32_t encode4(const float (&f)[4]) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// The block's values as codes (Floor: a positive value never becomes zero);
-// returns the block's scale. Warp-collective.
-template <bool Floor>
-MOE_DEV float store_codes(void* a, int64_t i, int64_t n, bool vec, const float (&f)[4]) {
-  float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+// Four codes from index i (of n); those past n are zero.
+MOE_DEV uint32_t load_codes(const void* a, int64_t i, int64_t n, bool vec) {
+  const uint8_t* s = static_cast<const uint8_t*>(a) + i;
+  if (vec) return *reinterpret_cast<const uint32_t*>(s);
+  uint32_t c = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) c |= static_cast<uint32_t>(s[j]) << (8 * j);
+  return c;
+}
+
+// The block's values as codes (Floor: a positive value never becomes zero),
+// given the block's largest magnitude; returns the block's scale.
+template <bool Floor>
+MOE_DEV float store_codes(void* a, int64_t i, int64_t n, bool vec, const float (&f)[4], float amax) {
   const bool live = amax >= kTinyAmax;
   const float inv = live ? __fmul_rn(__frcp_rn(amax), 448.0f) : 0.0f;
-  uint8_t c[4];
+  const float least = live ? 0x1p-9f : 0.0f;   // the smallest positive code
+  float q[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    c[j] = __nv_cvt_float_to_fp8(__fmul_rn(f[j], inv), __NV_SATFINITE, __NV_E4M3);
-    if (Floor && live && f[j] > 0.0f && (c[j] & 0x7f) == 0) c[j] = 1;
+    q[j] = __fmul_rn(f[j], inv);
+    if (Floor && f[j] > 0.0f && q[j] < least) q[j] = least;
   }
+  const uint32_t c = encode4(q);
   uint8_t* s = static_cast<uint8_t*>(a) + i;
   if (vec) {
-    *reinterpret_cast<uchar4*>(s) = make_uchar4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<uint32_t*>(s) = c;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (i + j < n) s[j] = c[j];
+      if (i + j < n) s[j] = static_cast<uint8_t>(c >> (8 * j));
   }
   return live ? __fmul_rn(amax, 1.0f / 448.0f) : 0.0f;
+}
+
+MOE_DEV float largest4(const float (&f)[4]) {
+  return fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
 }
 
 template <int Bits, int Max>
@@ -196,10 +207,16 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       load4(t.m, MOE_F32, i, n, vec, m);
       load4(t.v, MOE_F32, i, n, vec, v);
     } else {
-      load_codes(t.m, i, n, vec, t.ms[b / kBlock], m);
-      load_codes(t.v, i, n, vec, t.vs[b / kBlock], v);
+      const uint32_t mc = load_codes(t.m, i, n, vec), vc = load_codes(t.v, i, n, vec);
+      const float ms = t.ms[b / kBlock], vs = t.vs[b / kBlock];
+      decode4(mc, m);
+      decode4(vc, v);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], v[j]);
+      for (int j = 0; j < 4; ++j) {
+        m[j] = __fmul_rn(m[j], ms);
+        v[j] = __fmul_rn(v[j], vs);
+        v[j] = __fmul_rn(v[j], v[j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -220,8 +237,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (i + j >= n) m[j] = r[j] = 0.0f;
-      const float ms = store_codes<false>(t.m, i, n, vec, m);
-      const float vs = store_codes<true>(t.v, i, n, vec, r);
+      // The block's largest |m| and r: fp32 magnitudes compare as integers do.
+      const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(largest4(m)));
+      const uint32_t ar = __reduce_max_sync(0xffffffffu, __float_as_uint(largest4(r)));
+      const float ms = store_codes<false>(t.m, i, n, vec, m, __uint_as_float(am));
+      const float vs = store_codes<true>(t.v, i, n, vec, r, __uint_as_float(ar));
       if (lane == 0) {
         t.ms[b / kBlock] = ms;
         t.vs[b / kBlock] = vs;

@@ -19,10 +19,11 @@ constexpr int kThreads = 256;
 constexpr int kPadRowsPerBlock = 8;
 
 // Blocks [0, pad_blocks) zero the alignment gaps (first in the grid, so they
-// are never its tail); the others walk (token, 256-vector piece) items. A
-// block reads its piece of a token's row once and stores it to the token's
-// rows; a row of more than 256 16-byte vectors is several items, so that a
-// batch of few tokens still spreads over the GPU.
+// are never its tail); the warps of the others take pieces of tokens' rows, a
+// piece being 1 KB: two 16-byte vectors per lane, both read before the K pairs
+// of stores. Small pieces spread a batch of few tokens over the GPU.
+constexpr int kPieceVec = 64;
+
 __global__ void __launch_bounds__(kThreads) expand_rows_kernel(
     const uint16_t* __restrict__ x, int64_t ld_x, const float* __restrict__ topk_w,
     const int32_t* __restrict__ src2dst, const int32_t* __restrict__ psum,
@@ -50,17 +51,22 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(
     nv = *d_n_valid;
     nv = nv < 0 ? 0 : (nv > T ? T : nv);
   }
-  const int pieces = (nvec + kThreads - 1) / kThreads;
+  const int pieces = (nvec + kPieceVec - 1) / kPieceVec;
   const int64_t items = nv * pieces;
   const int lane = tid & 31;
-  for (int64_t it = blockIdx.x - pad_blocks; it < items; it += gridDim.x - pad_blocks) {
-    const int64_t t = it / pieces;
+  const int64_t step = static_cast<int64_t>(gridDim.x - pad_blocks) * (kThreads / 32);
+  for (int64_t it = static_cast<int64_t>(blockIdx.x - pad_blocks) * (kThreads / 32) + (tid >> 5);
+       it < items; it += step) {
+    const int64_t t = it <= UINT32_MAX ? static_cast<uint32_t>(it) / static_cast<uint32_t>(pieces)
+                                       : it / pieces;
     const int piece = static_cast<int>(it - t * pieces);
-    const int v = piece * kThreads + tid;
-    const bool act = v < nvec;
-    uint4 val = make_uint4(0, 0, 0, 0);
-    if (act) val = __ldcs(reinterpret_cast<const uint4*>(x + t * ld_x) + v);
-    // lane k < K of every warp holds pair k's row
+    const int v = piece * kPieceVec + lane;
+    const uint4* src = reinterpret_cast<const uint4*>(x + t * ld_x) + v;
+    const bool act0 = v < nvec, act1 = v + 32 < nvec;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (act0) a = __ldcs(src);
+    if (act1) b = __ldcs(src + 32);
+    // lane k < K holds pair k's row
     int my = -1;
     if (lane < K) {
       my = src2dst[t * K + lane];
@@ -68,11 +74,14 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(
         set_status(status, MOE_ERR_DEVICE_CHECK);
         my = -1;
       }
-      if (row_w != nullptr && piece == 0 && tid < 32 && my >= 0) row_w[my] = topk_w[t * K + lane];
+      if (row_w != nullptr && piece == 0 && my >= 0) row_w[my] = topk_w[t * K + lane];
     }
     for (int k = 0; k < K; ++k) {
       const int r = __shfl_sync(0xffffffffu, my, k);
-      if (r >= 0 && act) reinterpret_cast<uint4*>(xe + static_cast<int64_t>(r) * ld_xe)[v] = val;
+      if (r < 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(xe + static_cast<int64_t>(r) * ld_xe) + v;
+      if (act0) dst[0] = a;
+      if (act1) dst[32] = b;
     }
   }
 }
@@ -118,9 +127,12 @@ extern "C" int moe_expand_rows(const uint16_t* x, int64_t ld_x, const float* top
   const int64_t pad_per_expert =
       (align - 1 + moe::kPadRowsPerBlock - 1) / moe::kPadRowsPerBlock;
   const int64_t pad = pad_per_expert * E;
-  const int64_t items = T * ((nvec + moe::kThreads - 1) / moe::kThreads);
-  int64_t blocks = static_cast<int64_t>(moe::device_sm_count()) * (2048 / moe::kThreads);
-  if (blocks > items) blocks = items;
+  // up to eight times the blocks that fit at once, so that the hardware evens
+  // out what they have to do
+  const int64_t items = T * ((nvec + moe::kPieceVec - 1) / moe::kPieceVec);
+  const int64_t need = (items + moe::kThreads / 32 - 1) / (moe::kThreads / 32);
+  int64_t blocks = static_cast<int64_t>(moe::device_sm_count()) * (2048 / moe::kThreads) * 8;
+  if (blocks > need) blocks = need;
   if (pad + blocks == 0) return MOE_OK;
   MOE_REQUIRE(pad + blocks < (1ll << 31), "moe_expand_rows: grid too large");
   moe::expand_rows_kernel<<<static_cast<unsigned>(pad + blocks), moe::kThreads, 0,

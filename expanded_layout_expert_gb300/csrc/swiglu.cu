@@ -6,8 +6,10 @@
 // once to the 16-bit type, dw stays fp32.
 //
 // Bytes a row: 6I + 4 forward, 10I + 8 backward, so both are bound by HBM. A
-// warp takes a row: the backward needs the row's sum, and a lane's 16-byte
-// vectors of g, u (and dh) are one contiguous 512-byte run per instruction.
+// group of kGroup lanes takes a row (the backward needs the row's sum): a
+// warp, whose 16-byte vectors of g, u (and dh) are one contiguous 512-byte run
+// per instruction, or, for rows of few vectors, the 8 or 16 lanes that leave
+// the fewest idle.
 // e^x is the hardware's base-2 exponential, the quotient its reciprocal
 // (about 2 ulp each, far below the 16-bit rounding): with correctly rounded
 // ones the arithmetic, not HBM, would set the time of the backward.
@@ -18,25 +20,25 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
 MOE_DEV float sigmoid_fast(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-template <bool Half>
+template <bool Half, int kGroup>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(
     const uint16_t* __restrict__ gu, int64_t ld_gu, int nvec, const float* __restrict__ row_w,
     const int32_t* __restrict__ d_total, int64_t M_cap, uint16_t* __restrict__ h, int64_t ld_h) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x % kGroup;
   int64_t total = *d_total;
   if (total > M_cap) total = M_cap;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < total;
-       r += nwarps) {
+  constexpr int kRows = kThreads / kGroup;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup; r < total;
+       r += step) {
     const uint4* g4 = reinterpret_cast<const uint4*>(gu + r * ld_gu);
     const uint4* u4 = g4 + nvec;
     uint4* h4 = reinterpret_cast<uint4*>(h + r * ld_h);
     const float w = row_w != nullptr ? row_w[r] : 1.0f;
-    for (int v = lane; v < nvec; v += 32) {
+    for (int v = lane; v < nvec; v += kGroup) {
       float g[8], u[8];
       unpack8<Half>(__ldcs(g4 + v), g);
       unpack8<Half>(__ldcs(u4 + v), u);
@@ -50,23 +52,24 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(
 // dgu may be gu itself: a lane reads its vectors of g and u before it writes
 // the same places, and no other lane touches them (so no __restrict__ or
 // read-only loads on gu here).
-template <bool Half>
+template <bool Half, int kGroup>
 __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(
     const uint16_t* __restrict__ dh, int64_t ld_dh, const uint16_t* gu, int64_t ld_gu, int nvec,
     const float* __restrict__ row_w, const int32_t* __restrict__ d_total, int64_t M_cap,
     uint16_t* dgu, int64_t ld_dgu, float* __restrict__ drow_w) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x % kGroup;
   int64_t total = *d_total;
   if (total > M_cap) total = M_cap;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < total;
-       r += nwarps) {
+  constexpr int kRows = kThreads / kGroup;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup; r < total;
+       r += step) {
     const uint4* g4 = reinterpret_cast<const uint4*>(gu + r * ld_gu);
     const uint4* d4 = reinterpret_cast<const uint4*>(dh + r * ld_dh);
     uint4* o4 = reinterpret_cast<uint4*>(dgu + r * ld_dgu);
     const float w = row_w != nullptr ? row_w[r] : 1.0f;
     float sum = 0.0f;
-    for (int v = lane; v < nvec; v += 32) {
+    for (int v = lane; v < nvec; v += kGroup) {
       float g[8], u[8], d[8];
       unpack8<Half>(g4[v], g);
       unpack8<Half>(g4[nvec + v], u);
@@ -84,17 +87,52 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(
       o4[nvec + v] = pack8<Half>(u);
     }
     if (drow_w != nullptr) {
+      // the row's own lanes: rows of one warp may end their loops apart
+      const uint32_t lanes = kGroup == 32 ? 0xffffffffu
+                                          : ((1u << (kGroup % 32)) - 1u) << (threadIdx.x % 32 / kGroup * kGroup);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int o = kGroup / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
       if (lane == 0) drow_w[r] = sum;
     }
   }
 }
 
-unsigned grid_for(int64_t rows) {
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * (2048 / kThreads);
-  const int64_t need = (rows + kWarps - 1) / kWarps;
+// Lanes per row: the group that idles least, the widest of equals.
+int group_for(int nvec) {
+  int best = 32, least = (nvec + 31) / 32 * 32;
+  for (int g = 16; g >= 8; g /= 2) {
+    const int n = (nvec + g - 1) / g * g;
+    if (n < least * 15 / 16) {   // a narrower run per row has to gain something
+      best = g;
+      least = n;
+    }
+  }
+  return best;
+}
+
+// Up to eight times the blocks that fit at once: the hardware hands out rows
+// as blocks finish, and rows of a large buffer past `total` cost little.
+unsigned grid_for(int64_t rows, int group) {
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * (2048 / kThreads) * 8;
+  const int64_t per = kThreads / group;
+  const int64_t need = (rows + per - 1) / per;
   return static_cast<unsigned>(need < most ? need : most);
+}
+
+template <int kGroup>
+void launch_forward(bool half, const uint16_t* gu, int64_t ld_gu, int nvec, const float* row_w,
+                    const int32_t* d_total, int64_t M_cap, uint16_t* h, int64_t ld_h, cudaStream_t s) {
+  auto* kernel = half ? swiglu_kernel<true, kGroup> : swiglu_kernel<false, kGroup>;
+  kernel<<<grid_for(M_cap, kGroup), kThreads, 0, s>>>(gu, ld_gu, nvec, row_w, d_total, M_cap, h, ld_h);
+}
+
+template <int kGroup>
+void launch_backward(bool half, const uint16_t* dh, int64_t ld_dh, const uint16_t* gu, int64_t ld_gu,
+                     int nvec, const float* row_w, const int32_t* d_total, int64_t M_cap,
+                     uint16_t* dgu, int64_t ld_dgu, float* drow_w, cudaStream_t s) {
+  auto* kernel = half ? swiglu_backward_kernel<true, kGroup> : swiglu_backward_kernel<false, kGroup>;
+  kernel<<<grid_for(M_cap, kGroup), kThreads, 0, s>>>(dh, ld_dh, gu, ld_gu, nvec, row_w, d_total, M_cap,
+                                                      dgu, ld_dgu, drow_w);
 }
 
 }  // namespace
@@ -113,10 +151,11 @@ extern "C" int moe_swiglu(const void* gu, int64_t ld_gu, int dtype, int I, const
   MOE_REQUIRE_DEVICE();
   if (M_cap == 0) return MOE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto kernel = dtype == MOE_F16 ? moe::swiglu_kernel<true> : moe::swiglu_kernel<false>;
-  kernel<<<moe::grid_for(M_cap), moe::kThreads, 0, s>>>(
-      static_cast<const uint16_t*>(gu), ld_gu, I / 8, row_w, d_total, M_cap,
-      static_cast<uint16_t*>(h), ld_h);
+  const int group = moe::group_for(I / 8);
+  auto launch = group == 32 ? moe::launch_forward<32>
+                            : (group == 16 ? moe::launch_forward<16> : moe::launch_forward<8>);
+  launch(dtype == MOE_F16, static_cast<const uint16_t*>(gu), ld_gu, I / 8, row_w, d_total, M_cap,
+         static_cast<uint16_t*>(h), ld_h, s);
   return moe::check_launch("swiglu_kernel");
 }
 
@@ -139,9 +178,10 @@ extern "C" int moe_swiglu_backward(const void* dh, int64_t ld_dh, const void* gu
   MOE_REQUIRE_DEVICE();
   if (M_cap == 0) return MOE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto kernel = dtype == MOE_F16 ? moe::swiglu_backward_kernel<true> : moe::swiglu_backward_kernel<false>;
-  kernel<<<moe::grid_for(M_cap), moe::kThreads, 0, s>>>(
-      static_cast<const uint16_t*>(dh), ld_dh, static_cast<const uint16_t*>(gu), ld_gu, I / 8, row_w,
-      d_total, M_cap, static_cast<uint16_t*>(dgu), ld_dgu, drow_w);
+  const int group = moe::group_for(I / 8);
+  auto launch = group == 32 ? moe::launch_backward<32>
+                            : (group == 16 ? moe::launch_backward<16> : moe::launch_backward<8>);
+  launch(dtype == MOE_F16, static_cast<const uint16_t*>(dh), ld_dh, static_cast<const uint16_t*>(gu),
+         ld_gu, I / 8, row_w, d_total, M_cap, static_cast<uint16_t*>(dgu), ld_dgu, drow_w, s);
   return moe::check_launch("swiglu_backward_kernel");
 }

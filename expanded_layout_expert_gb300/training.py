@@ -9,9 +9,9 @@ larger than the row (a multiple of 8 values); rows outside the segments
 """
 from __future__ import annotations
 
-import ctypes as C
 from typing import List, Optional, Sequence
 
+import numpy as np
 import torch
 
 from ._capi import MOE_BF16, MOE_F16, MOE_F32, check, load
@@ -23,8 +23,12 @@ TYPE_CODE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MO
 STATE_BLOCK = 128   # values that share a scale in an 8-bit AdamW state
 
 
-def _stream(stream=None):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _stream(stream, device_of: torch.Tensor):
+    """The given stream's handle, or that of the current stream of the
+    tensor's device (without building a stream object for it)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device_of.get_device())
 
 
 def _code16(t: torch.Tensor, name: str) -> int:
@@ -97,7 +101,7 @@ def expand_rows(x: torch.Tensor, lay, topk_w: Optional[torch.Tensor] = None,
         _whole(lay.psum, "lay.psum", (lay.E,), torch.int32), _word(n_valid, "n_valid"), T, H, K,
         lay.E, lay.align, lay.M_cap, op, ld_o,
         _whole(row_w, "row_w", (lay.M_cap,), torch.float32), _word(status, "status"),
-        _stream(stream))
+        _stream(stream, x))
     check(rc, "moe_expand_rows")
     return out if topk_w is None else (out, row_w)
 
@@ -112,7 +116,7 @@ def collect_row_grads(rows: torch.Tensor, lay, n_valid: Optional[torch.Tensor] =
     rc = load().moe_collect_row_grads(
         _whole(rows, "rows", (lay.M_cap,), torch.float32),
         _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32), _word(n_valid, "n_valid"), T, K,
-        lay.M_cap, _whole(out, "out", (T, K), torch.float32), _stream(stream))
+        lay.M_cap, _whole(out, "out", (T, K), torch.float32), _stream(stream, rows))
     check(rc, "moe_collect_row_grads")
     return out
 
@@ -130,7 +134,7 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, lay, out: Optional[torch.Te
     xp, ld_x = _rows(x, "x", M, Kd, x.dtype)
     op, ld_o = _rows(out, "out", M, N, x.dtype)
     rc = load().moe_grouped_mm(xp, ld_x, _whole(w, "w", (E, N, Kd), x.dtype), start, psum, dt, E, N,
-                               Kd, M, op, ld_o, _word(status, "status"), _stream(stream))
+                               Kd, M, op, ld_o, _word(status, "status"), _stream(stream, x))
     check(rc, "moe_grouped_mm")
     return out
 
@@ -148,7 +152,7 @@ def grouped_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, lay, out: Optional[t
     dp, ld_d = _rows(dy, "dy", M, N, dy.dtype)
     op, ld_o = _rows(out, "out", M, Kd, dy.dtype)
     rc = load().moe_grouped_mm_dgrad(dp, ld_d, _whole(w, "w", (E, N, Kd), dy.dtype), start, psum, dt,
-                                     E, N, Kd, M, op, ld_o, _word(status, "status"), _stream(stream))
+                                     E, N, Kd, M, op, ld_o, _word(status, "status"), _stream(stream, dy))
     check(rc, "moe_grouped_mm_dgrad")
     return out
 
@@ -175,7 +179,7 @@ def grouped_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, lay, out: Optional[t
     xp, ld_x = _rows(x, "x", M, Kd, dy.dtype)
     rc = load().moe_grouped_mm_wgrad(dp, ld_d, xp, ld_x, start, psum, dt, E, N, Kd, M,
                                      _whole(out, "out", (E, N, Kd), out.dtype), TYPE_CODE[out.dtype],
-                                     int(accumulate), _word(status, "status"), _stream(stream))
+                                     int(accumulate), _word(status, "status"), _stream(stream, dy))
     check(rc, "moe_grouped_mm_wgrad")
     return out
 
@@ -193,7 +197,7 @@ def swiglu(gu: torch.Tensor, lay, row_w: Optional[torch.Tensor] = None,
     gp, ld_g = _rows(gu, "gu", M, two, gu.dtype)
     op, ld_o = _rows(out, "out", M, two // 2, gu.dtype)
     rc = load().moe_swiglu(gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32),
-                           _word(lay.total, "lay.total"), M, op, ld_o, _stream(stream))
+                           _word(lay.total, "lay.total"), M, op, ld_o, _stream(stream, gu))
     check(rc, "moe_swiglu")
     return out
 
@@ -217,16 +221,16 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, lay, row_w: Optional[tor
     rc = load().moe_swiglu_backward(
         hp, ld_h, gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32),
         _word(lay.total, "lay.total"), M, op, ld_o, _whole(drow_w, "drow_w", (M,), torch.float32),
-        _stream(stream))
+        _stream(stream, gu))
     check(rc, "moe_swiglu_backward")
     return dgu, drow_w
 
 
-class _AdamWTensor(C.Structure):
-    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("copy", C.c_void_p), ("m", C.c_void_p),
-                ("v", C.c_void_p), ("m_scale", C.c_void_p), ("v_scale", C.c_void_p),
-                ("n", C.c_int64), ("p_type", C.c_int32), ("g_type", C.c_int32),
-                ("copy_type", C.c_int32), ("reserved", C.c_int32)]
+# moe_adamw_tensor of include/moe_expand.h
+_ADAMW_TENSOR = np.dtype([("p", np.uint64), ("g", np.uint64), ("copy", np.uint64), ("m", np.uint64),
+                          ("v", np.uint64), ("m_scale", np.uint64), ("v_scale", np.uint64),
+                          ("n", np.int64), ("p_type", np.int32), ("g_type", np.int32),
+                          ("copy_type", np.int32), ("reserved", np.int32)])
 
 
 class AdamW:
@@ -302,44 +306,59 @@ class AdamW:
             if exp_avg_scale is not None or exp_avg_sq_scale is not None:
                 raise ValueError("scales belong to 8-bit states")
             self.exp_avg_scale = self.exp_avg_sq_scale = ()
-        self._table = (_AdamWTensor * max(n, 1))()
-        for i, p in enumerate(self.params):
-            d, c = self._table[i], self.copies[i]
-            d.m, d.v = self.exp_avg[i].data_ptr(), self.exp_avg_sq[i].data_ptr()
-            if state_bits == 8:
-                d.m_scale = self.exp_avg_scale[i].data_ptr()
-                d.v_scale = self.exp_avg_sq_scale[i].data_ptr()
-            d.n, d.p_type = p.numel(), TYPE_CODE[p.dtype]
-            d.copy_type = 0 if c is None else TYPE_CODE[c.dtype]
+        self._table = np.zeros(n, dtype=_ADAMW_TENSOR)
+        self._sizes = [p.numel() for p in self.params]
+        self._table["n"] = self._sizes
+        self._table["m"] = [t.data_ptr() for t in self.exp_avg]
+        self._table["v"] = [t.data_ptr() for t in self.exp_avg_sq]
+        if state_bits == 8:
+            self._table["m_scale"] = [t.data_ptr() for t in self.exp_avg_scale]
+            self._table["v_scale"] = [t.data_ptr() for t in self.exp_avg_sq_scale]
+        self._devices = [p.get_device() for p in self.params]
+        self._types = [p.dtype for p in self.params], [None if c is None else c.dtype for c in self.copies]
+        self._table["p_type"] = [TYPE_CODE[t] for t in self._types[0]]
+        self._table["copy_type"] = [0 if t is None else TYPE_CODE[t] for t in self._types[1]]
+        self._where = None   # (parameters', copies') addresses in the table
+
+    def _locate(self, where) -> None:
+        for name, tensors, types in (("parameter", self.params, self._types[0]),
+                                     ("copy", self.copies, self._types[1])):
+            for i, (t, n, ty, d) in enumerate(zip(tensors, self._sizes, types, self._devices)):
+                if t is not None and (t.numel() != n or t.dtype is not ty or not t.is_contiguous()
+                                      or t.get_device() != d):
+                    raise ValueError(f"{name} {i} has changed its size, type, layout or device since "
+                                     "this optimizer was made")
+        self._table["p"], self._table["copy"] = where
+        self._where = where
 
     def step(self, grads: Sequence[torch.Tensor], *, grad_scale: Optional[torch.Tensor] = None,
              lr: Optional[float] = None, stream=None) -> None:
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        # parameters, copies and gradients are looked up anew at every step: a
-        # caller may have given them other storage since the last one
-        for d, p, c, g in zip(self._table, self.params, self.copies, grads):
-            code = TYPE_CODE.get(g.dtype)
-            if code is None or g.numel() != d.n or not g.is_cuda or not g.is_contiguous():
-                raise ValueError("a gradient must be a contiguous float32, bfloat16 or float16 GPU "
-                                 f"tensor of its parameter's {d.n} values, got {g.dtype} {tuple(g.shape)}")
-            if p.numel() != d.n or TYPE_CODE.get(p.dtype) != d.p_type or not p.is_contiguous():
-                raise ValueError("a parameter has changed its size, type or layout since this "
-                                 "optimizer was made")
-            d.p, d.g, d.g_type = p.data_ptr(), g.data_ptr(), code
-            if c is not None:
-                if c.numel() != d.n or TYPE_CODE.get(c.dtype) != d.copy_type or not c.is_contiguous():
-                    raise ValueError("a copy has changed its size, type or layout since this "
-                                     "optimizer was made")
-                d.copy = c.data_ptr()
+        if not self.params:
+            self.steps += 1
+            return
+        # Every gradient is checked at every step; parameters and copies are
+        # looked up anew, and checked when they have been given other storage.
+        table, sizes, T = self._table, self._sizes, torch.Tensor
+        types = [g.dtype for g in grads]
+        if list(map(T.numel, grads)) != sizes or not all(map(T.is_contiguous, grads)) \
+                or list(map(T.get_device, grads)) != self._devices or not set(types) <= TYPE_CODE.keys():
+            raise ValueError("every gradient must be a contiguous float32, bfloat16 or float16 tensor of "
+                             "its parameter's size on its device")
+        where = list(map(T.data_ptr, self.params)), [0 if c is None else c.data_ptr() for c in self.copies]
+        if where != self._where:
+            self._locate(where)
+        table["g"] = list(map(T.data_ptr, grads))
+        table["g_type"] = TYPE_CODE[types[0]] if len(set(types)) == 1 else [TYPE_CODE[t] for t in types]
         if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1
                                        or not grad_scale.is_cuda):
             raise ValueError("grad_scale must be a float32 GPU tensor of one element")
-        rc = load().moe_adamw_step(C.cast(self._table, C.c_void_p), len(self.params), self.state_bits,
+        rc = load().moe_adamw_step(table.ctypes.data, len(self.params), self.state_bits,
                                    self.lr if lr is None else lr, self.betas[0], self.betas[1],
                                    self.eps, self.weight_decay, self.steps + 1,
                                    None if grad_scale is None else grad_scale.data_ptr(),
-                                   _stream(stream))
+                                   _stream(stream, self.params[0]))
         check(rc, "moe_adamw_step")
         self.steps += 1
 

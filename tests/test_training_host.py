@@ -115,13 +115,17 @@ def test_swiglu_refuses(capi, p):
 
 
 def test_adamw_refuses(capi, p):
-    from expanded_layout_expert_gb300.training import _AdamWTensor
+    import numpy as np
+    from expanded_layout_expert_gb300.training import _ADAMW_TENSOR
+    assert _ADAMW_TENSOR.itemsize == 80
     f = capi.load().moe_adamw_step
 
     def call(bits=32, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, wd=0.0, step=1, count=1, **kw):
-        t = (_AdamWTensor * 1)(_AdamWTensor(**dict(dict(p=p, g=p, m=p, v=p, m_scale=p, v_scale=p, n=4,
-                                                        p_type=2, g_type=2), **kw)))
-        return f(ctypes.cast(t, ctypes.c_void_p), count, bits, lr, b1, b2, eps, wd, step, None, None)
+        t = np.zeros(1, dtype=_ADAMW_TENSOR)
+        for k, v in dict(dict(p=p, g=p, m=p, v=p, m_scale=p, v_scale=p, n=4, p_type=2, g_type=2),
+                         **kw).items():
+            t[k] = 0 if v is None else v
+        return f(t.ctypes.data, count, bits, lr, b1, b2, eps, wd, step, None, None)
 
     _refused(capi, call(bits=16), "state_bits")
     _refused(capi, call(step=0), "step")
