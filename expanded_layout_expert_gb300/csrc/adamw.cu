@@ -18,7 +18,12 @@
 // and v before they are rounded.
 //
 // Bytes a value: 8 (p) + 2|4 (g) + 16 (fp32 m, v) or 4 + 16/128 (8 bits) + 2
-// (copy): bound by HBM. A warp takes 128 consecutive values, 4 per lane (16
+// (copy): bound by HBM with 32-bit states (6.97 TB/s on 134 M values). With 8-bit
+// states the time hardly depends on the gradients' bytes (417 us in fp32, 402
+// in bf16, 5.8 and 5.4 TB/s): there the instructions of the exactly rounded
+// root, quotient and codes set it, and many small blocks keep them flowing
+// (128 threads, 1024 values, 14 blocks an SM; with 256 threads, 4096 values
+// and five blocks it took 549 us). A warp takes 128 consecutive values, 4 per lane (16
 // bytes of each fp32 array), which is also one scale block, so its largest
 // magnitudes are two warp reductions. The tensors' table is a kernel parameter:
 // nothing is copied to the device before the launch.
@@ -33,9 +38,10 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kBlocksPerSm = 14;            // 36 registers a thread
 constexpr int kBlock = 128;                 // values that share a scale = values of a warp
-constexpr int kChunk = 4096;                // values of a block: 4 scale blocks per warp
+constexpr int kChunk = 1024;                // values of a block: two scale blocks per warp
 constexpr float kTinyAmax = 1e-30f;
 
 struct Tensor {
@@ -178,8 +184,13 @@ MOE_DEV float largest4(const float (&f)[4]) {
   return fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
 }
 
-template <int Bits, int Max>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<Max> tab,
+// What the tensors of a launch have in common, so that the kernel need not ask:
+// their gradients' type and whether they have a bf16 copy (kAny: they differ,
+// or p is not fp32).
+enum { kAny = -1, kNone = -2 };
+
+template <int Bits, int Max, int G, int Copy>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __grid_constant__ Table<Max> tab,
                                                          const Hyper h) {
   const int chunk = blockIdx.x;
   int lo = 0, hi = tab.count - 1;   // first tensor whose chunk_end is past this chunk
@@ -193,28 +204,45 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const int64_t base = static_cast<int64_t>(chunk - first) * kChunk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float scale = h.scale != nullptr ? *h.scale : 1.0f;
+  const int p_type = G == kAny ? t.p_type : MOE_F32;
+  const int g_type = G == kAny ? t.g_type : G;
+  const int copy_type = Copy == kAny ? t.copy_type : Copy;
+  const bool has_copy = Copy == kAny ? t.copy != nullptr : Copy != kNone;
   constexpr int kIter = kChunk / kBlock / (kThreads / 32);
-#pragma unroll 2
-  for (int it = 0; it < kIter; ++it) {
-    const int64_t b = base + (it * (kThreads / 32) + warp) * kBlock;
-    if (b >= n) break;   // the whole warp
+  struct In {
+    float p[4], g[4];
+    float m[4], v[4];       // 32-bit states
+    uint32_t mc, vc;        // 8-bit states
+    float ms, vs;
+  };
+  auto block_at = [&](int it) { return base + (it * (kThreads / 32) + warp) * kBlock; };
+  auto load = [&](int64_t b, In& x) {
     const int64_t i = b + lane * 4;
     const bool vec = t.vec && i + 4 <= n;
-    float p[4], g[4], m[4], v[4], r[4];
-    load4(t.g, t.g_type, i, n, vec, g);
-    load4(t.p, t.p_type, i, n, vec, p);
+    load4(t.g, g_type, i, n, vec, x.g);
+    load4(t.p, p_type, i, n, vec, x.p);
     if (Bits == 32) {
-      load4(t.m, MOE_F32, i, n, vec, m);
-      load4(t.v, MOE_F32, i, n, vec, v);
+      load4(t.m, MOE_F32, i, n, vec, x.m);
+      load4(t.v, MOE_F32, i, n, vec, x.v);
     } else {
-      const uint32_t mc = load_codes(t.m, i, n, vec), vc = load_codes(t.v, i, n, vec);
-      const float ms = t.ms[b / kBlock], vs = t.vs[b / kBlock];
-      decode4(mc, m);
-      decode4(vc, v);
+      x.mc = load_codes(t.m, i, n, vec);
+      x.vc = load_codes(t.v, i, n, vec);
+      x.ms = t.ms[b / kBlock];
+      x.vs = t.vs[b / kBlock];
+    }
+  };
+  auto step = [&](int64_t b, In& x) {
+    const int64_t i = b + lane * 4;
+    const bool vec = t.vec && i + 4 <= n;
+    float (&p)[4] = x.p, (&g)[4] = x.g, (&m)[4] = x.m, (&v)[4] = x.v;
+    float r[4];
+    if (Bits == 8) {
+      decode4(x.mc, m);
+      decode4(x.vc, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        m[j] = __fmul_rn(m[j], ms);
-        v[j] = __fmul_rn(v[j], vs);
+        m[j] = __fmul_rn(m[j], x.ms);
+        v[j] = __fmul_rn(v[j], x.vs);
         v[j] = __fmul_rn(v[j], v[j]);
       }
     }
@@ -227,8 +255,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       const float d = __fadd_rn(__fmul_rn(r[j], h.root), h.eps);
       p[j] = __fsub_rn(__fmul_rn(p[j], h.decay), __fdiv_rn(__fmul_rn(m[j], h.step_size), d));
     }
-    store4(t.p, t.p_type, i, n, vec, p);
-    if (t.copy != nullptr) store4(t.copy, t.copy_type, i, n, vec, p);
+    store4(t.p, p_type, i, n, vec, p);
+    if (has_copy) store4(t.copy, copy_type, i, n, vec, p);
     if (Bits == 32) {
       store4(t.m, MOE_F32, i, n, vec, m);
       store4(t.v, MOE_F32, i, n, vec, v);
@@ -247,6 +275,14 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         t.vs[b / kBlock] = vs;
       }
     }
+  };
+#pragma unroll 1
+  for (int it = 0; it < kIter; ++it) {
+    const int64_t b = block_at(it);
+    if (b >= n) break;   // the whole warp
+    In x;
+    load(b, x);
+    step(b, x);
   }
 }
 
@@ -255,25 +291,44 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 constexpr int kMaxTensors = 400;
 constexpr int kFewTensors = 16;
 
-template <int Bits, int Max>
+template <int Bits, int Max, int G, int Copy>
 int launch(const Table<kMaxTensors>& all, int chunks, const Hyper& h, cudaStream_t s) {
   if constexpr (Max == kMaxTensors) {
-    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(all, h);
+    adamw_kernel<Bits, Max, G, Copy><<<chunks, kThreads, 0, s>>>(all, h);
   } else {
     Table<Max> few;
     for (int i = 0; i < all.count; ++i) few.t[i] = all.t[i];
     few.count = all.count;
-    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(few, h);
+    adamw_kernel<Bits, Max, G, Copy><<<chunks, kThreads, 0, s>>>(few, h);
   }
   return check_launch("adamw_kernel");
 }
 
+template <int Bits, int Max>
+int launch_types(const Table<kMaxTensors>& tab, int chunks, const Hyper& h, cudaStream_t s) {
+  bool same = true;
+  for (int i = 0; i < tab.count; ++i) {
+    const Tensor& t = tab.t[i];
+    same = same && t.p_type == MOE_F32 && t.g_type == tab.t[0].g_type &&
+           (t.copy != nullptr) == (tab.t[0].copy != nullptr) && (!t.copy || t.copy_type == MOE_BF16);
+  }
+  const int g = same ? tab.t[0].g_type : kAny;
+  const bool copy = tab.t[0].copy != nullptr;
+  if (g == MOE_F32)
+    return copy ? launch<Bits, Max, MOE_F32, MOE_BF16>(tab, chunks, h, s)
+                : launch<Bits, Max, MOE_F32, kNone>(tab, chunks, h, s);
+  if (g == MOE_BF16)
+    return copy ? launch<Bits, Max, MOE_BF16, MOE_BF16>(tab, chunks, h, s)
+                : launch<Bits, Max, MOE_BF16, kNone>(tab, chunks, h, s);
+  return launch<Bits, Max, kAny, kAny>(tab, chunks, h, s);
+}
+
 int launch_all(const Table<kMaxTensors>& tab, int bits, int chunks, const Hyper& h, cudaStream_t s) {
   if (bits == 32)
-    return tab.count <= kFewTensors ? launch<32, kFewTensors>(tab, chunks, h, s)
-                                    : launch<32, kMaxTensors>(tab, chunks, h, s);
-  return tab.count <= kFewTensors ? launch<8, kFewTensors>(tab, chunks, h, s)
-                                  : launch<8, kMaxTensors>(tab, chunks, h, s);
+    return tab.count <= kFewTensors ? launch_types<32, kFewTensors>(tab, chunks, h, s)
+                                    : launch_types<32, kMaxTensors>(tab, chunks, h, s);
+  return tab.count <= kFewTensors ? launch_types<8, kFewTensors>(tab, chunks, h, s)
+                                  : launch_types<8, kMaxTensors>(tab, chunks, h, s);
 }
 
 }  // namespace
