@@ -35,8 +35,9 @@
 // (cta_group::2): each loads half of both operands, so a 64-deep block costs an
 // SM 32 KB instead of 48. With one CTA per 128 x 256 tile a block took 705
 // cycles (1024 rows an expert, 4096 x 4096, forward), with pairs 558; the
-// tensor core's own time is 512. Experts with few rows take the single-CTA
-// form, whose tile wastes less on them.
+// tensor core's own time is 512. A segment's last tile, if it has at most 128
+// rows, is done with 64 rows per CTA in half the time. Experts with few rows
+// take the single-CTA form, which spreads their weights over more tiles.
 //
 // What bounds it: power. Forward and dgrad run at 1.6 PFLOP/s with the SM clock
 // held near 1.4 GHz by the power limit, 92-97 % of what the library's product
@@ -343,6 +344,7 @@ MOE_DEV bool drain_wait(uint64_t* bar, uint32_t parity) {
 struct Tile {
   int e, i0, j0;   // expert; first row (forward, dgrad: within the segment) and column of D
   int row0, rows;  // the expert's segment
+  bool light;      // a pair's tile with at most 128 rows, 64 of them per CTA
 };
 
 // Out16: D is stored in the operands' type, else (wgrad) in fp32. Add: D is
@@ -477,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     t.j0 = (in / gi) * BN;
     t.row0 = s_start[t.e];
     t.rows = s_end[t.e] - t.row0;
+    t.light = kCtas == 2 && kMode != kWgrad && t.rows - t.i0 <= BMC;
     return t;
   };
   // blocks of BC along the contracted axis
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       const Tile t = tile_at(tile);
       const int nb = num_blocks(t);
       const int rag = ragged(t);
-      const int i0 = t.i0 + rank * BMC, j0 = t.j0 + rank * C::kBRows;
+      const int i0 = t.i0 + rank * (t.light ? BMC / 2 : BMC), j0 = t.j0 + rank * C::kBRows;
       for (int b = 0; b < nb; ++b) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
         uint8_t* sa = smem + stage * C::kStageBytes;
@@ -540,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc = idesc_f16(Half, kMode == kWgrad, kMode != kForward, C::BM, BN);
+    constexpr uint32_t idesc_whole = idesc_f16(Half, kMode == kWgrad, kMode != kForward, C::BM, BN);
+    constexpr uint32_t idesc_light = idesc_f16(Half, kMode == kWgrad, kMode != kForward, BMC, BN);
     int stage = 0, acc = 0;
     uint32_t acc_phase = 0;
     uint32_t full_phase = 0, rag_phase = 0;   // a bit per stage: uses so far
@@ -552,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       const int rag = ragged(t);
       if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) break;
       const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+      const uint32_t idesc = t.light ? idesc_light : idesc_whole;
       for (int b = 0; b < nb; ++b) {
         const bool ragged_block = kMode == kWgrad && rag && b == 0;
         uint64_t* landed = ragged_block ? &rzeroed[stage] : &full[stage];
@@ -646,8 +651,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       const bool empty_tile = num_blocks(t) == 0;
       if (empty_tile && Add) continue;
       const int ilim = kMode == kWgrad ? p.N : t.rows;                // rows of D that exist
-      const int iw = t.i0 + rank * BMC + quarter * 32;                // this warp's first row
-      const int j = t.j0 + half_cols;                                 // and column
+      // this warp's first row and column of D, and of the accumulator; a light
+      // tile's 64 rows lie in lanes 0-63 with D's columns 0-127 and in lanes
+      // 64-127 with its columns 128-255, in accumulator columns 0-127
+      const int iw = t.i0 + (t.light ? rank * (BMC / 2) + (quarter & 1) * 32 : rank * BMC + quarter * 32);
+      const int acol = t.light ? half_cols / 2 : half_cols;
+      const int j = t.j0 + (t.light ? (quarter >> 1) * (BN / 2) : 0) + acol;
+      const int pieces = t.light ? kPieces / 2 : kPieces;
       const bool by_tma = kTma && (kMode == kWgrad || iw + 32 <= ilim);
       const int64_t orow = (kMode == kWgrad ? static_cast<int64_t>(t.e) * p.N : t.row0) + iw + lane;
       uint8_t* out = static_cast<uint8_t*>(p.out) + (orow * p.ld_out + j) * kElem;
@@ -668,9 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
         tc_fence_after();
       }
       const uint32_t tq = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                          static_cast<uint32_t>(acc * BN + half_cols);
+                          static_cast<uint32_t>(acc * BN + acol);
 #pragma unroll
       for (int piece = 0; piece < kPieces; ++piece) {
+        if (kCtas == 2 && kMode != kWgrad && piece >= pieces) break;
         uint32_t w[kWords];   // the thread's row of the piece
         if (empty_tile) {
 #pragma unroll
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
         } else {
           tc_ld32_wait(tq + piece * kCols, w);
         }
-        if (!empty_tile && piece == kPieces - 1) {   // the last read has landed
+        if (!empty_tile && piece == pieces - 1) {   // the last read has landed
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
