@@ -584,3 +584,18 @@ def test_python_refusals(mx):
     with pytest.raises(ValueError):
         opt.step([x], grad_scale=torch.zeros(2, device="cuda"))
     assert opt.steps == 0
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_example_learns(mx, bits):
+    """The example's layer approaches its teacher: the loss falls to under half."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_experts.py")
+    spec = importlib.util.spec_from_file_location("train_experts", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses = m.main(["--steps", "80", "--state-bits", str(bits)])
+    assert all(np.isfinite(losses))
+    assert np.mean(losses[-5:]) < 0.5 * np.mean(losses[:5]), (losses[:5], losses[-5:])
