@@ -67,8 +67,8 @@ SIGNATURES = {
     "moe_masked_slab_to_expand": (I32, [P, I64, P, P, P, P, I32, I32, I64, P, P]),
     "moe_expand_rows": (I32, [P, I64, P, P, P, P, I64, I32, I32, I32, I32, I64, P, I64, P, P, P]),
     "moe_collect_row_grads": (I32, [P, P, P, I64, I32, I64, P, P]),
-    "moe_grouped_mm": (I32, [P, I64, P, P, P, I32, I32, I32, I32, I64, P, I64, P, P]),
-    "moe_grouped_mm_dgrad": (I32, [P, I64, P, P, P, I32, I32, I32, I32, I64, P, I64, P, P]),
+    "moe_grouped_mm": (I32, [P, I64, P, P, P, I32, I32, I32, I32, I64, I64, P, I64, P, P]),
+    "moe_grouped_mm_dgrad": (I32, [P, I64, P, P, P, I32, I32, I32, I32, I64, I64, P, I64, P, P]),
     "moe_grouped_mm_wgrad": (I32, [P, I64, P, I64, P, P, I32, I32, I32, I32, I64, P, I32, I32, P, P]),
     "moe_swiglu": (I32, [P, I64, I32, I32, P, P, I64, P, I64, P]),
     "moe_swiglu_backward": (I32, [P, I64, P, I64, I32, I32, P, P, I64, P, I64, P, P]),

@@ -52,6 +52,14 @@ struct MxGemmArgs {
   int64_t ld_ds = 0;
 };
 
+// Forward (dgrad) product for experts with few rows each, arguments already
+// validated: out = a times the weights. max_rows: rows of all segments
+// together, at most.
+int launch_grouped_mm16_few(bool dgrad, bool half, const void* a, int64_t ld_a, const void* w,
+                            const int32_t* start, const int32_t* psum, int E, int N, int Kd,
+                            int64_t M_cap, int64_t max_rows, uint16_t* out, int64_t ld_out,
+                            int32_t* status, cudaStream_t s);
+
 // Launches the tcgen05 block-scaled kernel (N % 256 == 0).
 int launch_grouped_gemm_mx(const MxGemmArgs& a, cudaStream_t s);
 

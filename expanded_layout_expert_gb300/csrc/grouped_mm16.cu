@@ -36,24 +36,26 @@
 // SM 32 KB instead of 48. With one CTA per 128 x 256 tile a block took 705
 // cycles (1024 rows an expert, 4096 x 4096, forward), with pairs 558; the
 // tensor core's own time is 512. A segment's last tile, if it has at most 128
-// rows, is done with 64 rows per CTA in half the time. Experts with few rows
-// take the single-CTA form, which spreads their weights over more tiles.
+// rows, is done with 64 rows per CTA (300 rows an expert: 331 instead of 367
+// us). wgrad with N <= 128 has single-CTA tiles; forward and dgrad of experts
+// with few rows are grouped_mm16_few.cu's.
 //
 // What bounds it: power. Forward and dgrad run at 1.6 PFLOP/s with the SM clock
 // held near 1.4 GHz by the power limit, 92-97 % of what the library's product
 // of the same rows and weights reaches there. wgrad (both operands i/j-contiguous)
 // is bound by the rate at which the tensor core reads such an A: 668 cycles a
 // block on long segments, against 531 for the others.
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
 #include "dtype16.cuh"
 #include "gemm_host.h"
 #include "host_util.h"
+#include "mm16.cuh"
 
 namespace moe {
 namespace {
-
 
 enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
@@ -61,7 +63,7 @@ constexpr int BMC = 128;         // rows of D per CTA
 constexpr int BN = 256;          // columns of D per tile
 constexpr int BC = 64;           // contracted per stage: one 128-byte swizzle row of 16-bit values
 constexpr int kUmmaK = 16;       // contracted per tcgen05.mma
-constexpr int kPanel = 64 * 128; // 64 rows of 128 bytes: one TMA box of an i/j-contiguous operand
+constexpr int kPanel = kMm16Panel;
 constexpr int kAcc = 2;
 constexpr int kTmemCols = kAcc * BN;
 constexpr int kEpiWarps = 8;     // two per TMEM lane quarter
@@ -72,9 +74,6 @@ constexpr int kRaster = 8;       // row tiles in a column of the raster (see til
 // kCtas CTAs work on one tile of kCtas * 128 x 256.
 template <int kMode, int kCtas, bool Out16 = true>
 struct Cfg {
-  // Results leave through shared memory and TMA, except for the single-CTA
-  // forward and dgrad, which serve experts with few rows (see the epilogue).
-  static constexpr bool kTmaStore = kCtas == 2 || kMode == kWgrad;
   static constexpr int BM = kCtas * BMC;
   static constexpr int kBRows = BN / kCtas;             // columns of D whose operand this CTA loads
   static constexpr int kABytes = BMC * BC * 2;
@@ -85,9 +84,9 @@ struct Cfg {
   // block so, 785 with five stages and 128 bytes; forward 558 and 577). fp32
   // rows take 128, so that a piece is 32 columns in either type.
   static constexpr int kPieceBytes = Out16 ? 64 : 128;
-  static constexpr int kStages = kCtas == 2 ? (Out16 ? 6 : 5) : (kTmaStore ? 3 : 4);
+  static constexpr int kStages = kCtas == 2 ? (Out16 ? 6 : 5) : 3;
   static constexpr int kStoreOffset = kStages * kStageBytes;   // per epilogue warp: 32 rows of a piece
-  static constexpr int kBarOffset = kStoreOffset + (kTmaStore ? kEpiWarps * 32 * kPieceBytes : 0);
+  static constexpr int kBarOffset = kStoreOffset + kEpiWarps * 32 * kPieceBytes;
   static constexpr int kNumBars = 4 * kStages + 2 * kAcc + 1;
   static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;          // tmem slot, abort flag
   static constexpr int kTableOffset = (kMiscOffset + 8 + 15) / 16 * 16;  // prefix [E+1], start, end [E]
@@ -105,49 +104,6 @@ struct Params {
   int wide;              // rows of out begin on 32-byte boundaries
   int32_t* status;
 };
-
-// Tensor-core operand whose contiguous axis is i/j, not c: panels of 64 c rows
-// x 128 bytes (64 values), 128-byte swizzle. Groups of 8 c rows are 1024 bytes
-// apart (stride byte offset), panels kPanel apart (leading byte offset).
-MOE_DEV uint64_t sw128_mnmajor_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kPanel >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// Instruction descriptor: dense, D = f32, A and B both fp16 or both bf16;
-// a_mn / b_mn: the operand's contiguous axis is i / j.
-constexpr uint32_t idesc_f16(bool half, bool a_mn, bool b_mn, int M, int N) {
-  return (1u << 4) | ((half ? 0u : 1u) << 7) | ((half ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
-         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, K = 16. kCtas = 2: issued
-// by the pair's first CTA; each CTA's shared memory holds its half of A's rows
-// and of B's, each CTA's TMEM its half of D's rows.
-template <int kCtas>
-MOE_DEV void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                        uint32_t accumulate) {
-  if constexpr (kCtas == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 
 // Arrive once on `bar` (kCtas = 2: on the barrier at this place in both CTAs)
 // when the MMAs issued so far have completed.
@@ -194,12 +150,6 @@ MOE_DEV void tmem_dealloc_n(uint32_t taddr, uint32_t ncols) {
                  : "memory");
 }
 
-// Address of the same shared-memory place in the pair's CTA of that rank.
-MOE_DEV uint32_t cta_smem(const void* p, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
 MOE_DEV uint32_t leader_smem(const void* p) { return cta_smem(p, 0); }
 // Arrive on a barrier of the pair's first CTA. The relaxed form is for a
 // thread whose only business with the waiter is TMEM it has read (the loads
@@ -212,10 +162,6 @@ MOE_DEV void mbar_arrive_leader(uint64_t* bar) {
 MOE_DEV void mbar_arrive_leader_relaxed(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_smem(bar))
                : "memory");
-}
-MOE_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // mbar_wait for a barrier that threads of the other CTA arrive on after
 // writing shared memory of their own that this thread's MMAs read.
@@ -238,39 +184,6 @@ MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abo
       return false;
     }
   }
-}
-
-// TMA loads whose bytes are counted on `bar` (a shared::cluster address): a
-// barrier of this CTA, or (kCtas = 2) of the pair's first.
-template <int kCtas>
-MOE_DEV void load_2d(void* dst, const CUtensorMap* tm, int32_t x, int32_t y, uint32_t bar) {
-  if constexpr (kCtas == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-template <int kCtas>
-MOE_DEV void load_3d(void* dst, const CUtensorMap* tm, int32_t x, int32_t y, int32_t z, uint32_t bar) {
-  if constexpr (kCtas == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
 }
 
 // TMA store (kAdd: addition in fp32, done by L2) of a staged 128-byte-wide
@@ -323,22 +236,6 @@ MOE_DEV void load_sector(const uint8_t* a, uint32_t* v, int left, int per, int w
       v[4] = x.x; v[5] = x.y; v[6] = x.z; v[7] = x.w;
     }
   }
-}
-
-// 32 TMEM lanes x 32 columns, waited for.
-MOE_DEV void tc_ld32_wait(uint32_t taddr, uint32_t (&v)[32]) {
-  tc_ld32(taddr, v);
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  tc_regs_landed(v);
-}
-
-// Bounded wait used while draining: no abort check, only the time limit.
-MOE_DEV bool drain_wait(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
-    if (clock64() - t0 > kWaitLimitCycles) return false;
-  }
-  return true;
 }
 
 struct Tile {
@@ -396,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     fence_mbar_init();
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
-    if (C::kTmaStore) prefetch_tmap(&tmD);
+    prefetch_tmap(&tmD);
   }
   if (warp == 1) tmem_alloc_n<kCtas>(tmem_slot, kTmemCols);
   // Segments, clamped into the buffer, and (forward, dgrad) the prefix of
@@ -635,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     const int half_cols = ((warp - 4) >> 2) * (BN / 2);
     constexpr int kElem = Out16 ? 2 : 4;
     constexpr bool kAddHere = Add && Out16;     // added in registers
-    constexpr bool kTma = C::kTmaStore && !kAddHere;
+    constexpr bool kTma = !kAddHere;
     constexpr int kPiece = C::kPieceBytes;      // 64 or 128
     constexpr int kWords = kPiece / 4;
     constexpr int kCols = 32;                   // columns of D per piece
@@ -813,12 +710,20 @@ int check_rows(const char* what, const char* name, const void* a, int64_t ld, in
     if (rc_ != MOE_OK) return rc_;     \
   } while (0)
 
+// Rows per expert, on average, up to which the few-rows form is taken. With 24
+// rows it takes 171 us and the pairs 176 (32 experts of 4096 x 4096, forward;
+// dgrad 166 and 166), with 48 rows 183 and 178 (180 and 169); with 32 rows of
+// 64 experts of 4096 x 7168 it takes 551 and the pairs 587.
+constexpr int kFewRows = 40;
+
 // Forward and dgrad: rows [M_cap, in] times weights -> rows [M_cap, out].
 int rows_times_weights(const char* what, bool dgrad, const void* a, int64_t ld_a, const void* w,
                        const int32_t* start, const int32_t* psum, int dtype, int E, int N, int Kd,
-                       int64_t M_cap, void* out, int64_t ld_out, int32_t* d_status, cudaStream_t s) {
+                       int64_t M_cap, int64_t max_rows, void* out, int64_t ld_out, int32_t* d_status,
+                       cudaStream_t s) {
   MOE_TRY(check_sizes(what, dtype, E, N, Kd, M_cap));
   const int in = dgrad ? N : Kd, width = dgrad ? Kd : N;
+  MOE_REQUIRE(max_rows >= 0 && max_rows <= M_cap, "%s: max_rows must be in [0, M_cap]", what);
   if (M_cap > 0) {
     MOE_REQUIRE(start && psum, "%s: null segments", what);
     MOE_TRY(check_rows(what, dgrad ? "dy" : "x", a, ld_a, in));
@@ -826,15 +731,15 @@ int rows_times_weights(const char* what, bool dgrad, const void* a, int64_t ld_a
     MOE_TRY(check_rows(what, dgrad ? "dx" : "out", out, ld_out, width));
   }
   MOE_REQUIRE_DEVICE();
-  if (M_cap == 0) return MOE_OK;
-  CUtensorMap ta, tb, td = {};
-  // A pair of CTAs per tile once the experts have 128 rows on average; fewer,
-  // and the second CTA of most pairs would have none.
-  const bool pair = M_cap > static_cast<int64_t>(E) * BMC;
-  const int bm = pair ? 2 * BMC : BMC;
+  if (max_rows == 0) return MOE_OK;
+  const bool half = dtype == MOE_F16;
+  if (max_rows <= static_cast<int64_t>(E) * kFewRows)
+    return launch_grouped_mm16_few(dgrad, half, a, ld_a, w, start, psum, E, N, Kd, M_cap, max_rows,
+                                   static_cast<uint16_t*>(out), ld_out, d_status, s);
+  CUtensorMap ta, tb, td;
   MOE_TRY(make_tmap_rows16(&ta, a, in, M_cap, ld_a, BMC));
-  MOE_TRY(make_tmap_weights16(&tb, w, Kd, N, E, dgrad ? 64 : (pair ? BN / 2 : BN)));
-  if (pair) MOE_TRY(make_tmap_result(&td, out, false, width, M_cap, 1, ld_out, Cfg<kForward, 2>::kPieceBytes));
+  MOE_TRY(make_tmap_weights16(&tb, w, Kd, N, E, dgrad ? 64 : BN / 2));
+  MOE_TRY(make_tmap_result(&td, out, false, width, M_cap, 1, ld_out, Cfg<kForward, 2>::kPieceBytes));
   Params p;
   p.start = start;
   p.psum = psum;
@@ -846,21 +751,13 @@ int rows_times_weights(const char* what, bool dgrad, const void* a, int64_t ld_a
   p.ld_out = ld_out;
   p.wide = aligned(out, 32) && ld_out % 16 == 0;
   p.status = d_status;
-  const int64_t m_tiles = M_cap / bm + (E < M_cap ? E : M_cap);
+  const int64_t m_tiles = max_rows / (2 * BMC) + std::min<int64_t>(E, max_rows);
   const int64_t tiles = m_tiles * ((width + BN - 1) / BN);
-  const bool half = dtype == MOE_F16;
-  if (dgrad) {
-    if (pair)
-      return half ? launch<kDgrad, true, true, false, 2>(ta, tb, td, p, tiles, s)
-                  : launch<kDgrad, false, true, false, 2>(ta, tb, td, p, tiles, s);
-    return half ? launch<kDgrad, true, true, false, 1>(ta, tb, td, p, tiles, s)
-                : launch<kDgrad, false, true, false, 1>(ta, tb, td, p, tiles, s);
-  }
-  if (pair)
-    return half ? launch<kForward, true, true, false, 2>(ta, tb, td, p, tiles, s)
-                : launch<kForward, false, true, false, 2>(ta, tb, td, p, tiles, s);
-  return half ? launch<kForward, true, true, false, 1>(ta, tb, td, p, tiles, s)
-              : launch<kForward, false, true, false, 1>(ta, tb, td, p, tiles, s);
+  if (dgrad)
+    return half ? launch<kDgrad, true, true, false, 2>(ta, tb, td, p, tiles, s)
+                : launch<kDgrad, false, true, false, 2>(ta, tb, td, p, tiles, s);
+  return half ? launch<kForward, true, true, false, 2>(ta, tb, td, p, tiles, s)
+              : launch<kForward, false, true, false, 2>(ta, tb, td, p, tiles, s);
 }
 
 template <bool Half, int kCtas>
@@ -880,17 +777,18 @@ int launch_wgrad(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap
 
 extern "C" int moe_grouped_mm(const void* x, int64_t ld_x, const void* w, const int32_t* start,
                               const int32_t* psum, int dtype, int E, int N, int Kd, int64_t M_cap,
-                              void* out, int64_t ld_out, int32_t* d_status, moe_stream_t stream) {
+                              int64_t max_rows, void* out, int64_t ld_out, int32_t* d_status,
+                              moe_stream_t stream) {
   return moe::rows_times_weights("moe_grouped_mm", false, x, ld_x, w, start, psum, dtype, E, N, Kd,
-                                 M_cap, out, ld_out, d_status, reinterpret_cast<cudaStream_t>(stream));
+                                 M_cap, max_rows, out, ld_out, d_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_grouped_mm_dgrad(const void* dy, int64_t ld_dy, const void* w,
                                     const int32_t* start, const int32_t* psum, int dtype, int E,
-                                    int N, int Kd, int64_t M_cap, void* dx, int64_t ld_dx,
-                                    int32_t* d_status, moe_stream_t stream) {
+                                    int N, int Kd, int64_t M_cap, int64_t max_rows, void* dx,
+                                    int64_t ld_dx, int32_t* d_status, moe_stream_t stream) {
   return moe::rows_times_weights("moe_grouped_mm_dgrad", true, dy, ld_dy, w, start, psum, dtype, E, N,
-                                 Kd, M_cap, dx, ld_dx, d_status, reinterpret_cast<cudaStream_t>(stream));
+                                 Kd, M_cap, max_rows, dx, ld_dx, d_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,

@@ -77,6 +77,13 @@ def _segments(lay) -> tuple:
         _whole(lay.psum, "lay.psum", (E,), torch.int32), E
 
 
+def _most_rows(lay, M: int) -> int:
+    """Rows of all segments together, at most: one per pair of the layout (a
+    layout without pairs of its own may fill the buffer)."""
+    pairs = lay.src2dst.numel()
+    return min(pairs, M) if pairs else M
+
+
 def expand_rows(x: torch.Tensor, lay, topk_w: Optional[torch.Tensor] = None,
                 n_valid: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                 row_w: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
@@ -134,7 +141,8 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, lay, out: Optional[torch.Te
     xp, ld_x = _rows(x, "x", M, Kd, x.dtype)
     op, ld_o = _rows(out, "out", M, N, x.dtype)
     rc = load().moe_grouped_mm(xp, ld_x, _whole(w, "w", (E, N, Kd), x.dtype), start, psum, dt, E, N,
-                               Kd, M, op, ld_o, _word(status, "status"), _stream(stream, x))
+                               Kd, M, _most_rows(lay, M), op, ld_o, _word(status, "status"),
+                               _stream(stream, x))
     check(rc, "moe_grouped_mm")
     return out
 
@@ -152,7 +160,8 @@ def grouped_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, lay, out: Optional[t
     dp, ld_d = _rows(dy, "dy", M, N, dy.dtype)
     op, ld_o = _rows(out, "out", M, Kd, dy.dtype)
     rc = load().moe_grouped_mm_dgrad(dp, ld_d, _whole(w, "w", (E, N, Kd), dy.dtype), start, psum, dt,
-                                     E, N, Kd, M, op, ld_o, _word(status, "status"), _stream(stream, dy))
+                                     E, N, Kd, M, _most_rows(lay, M), op, ld_o,
+                                     _word(status, "status"), _stream(stream, dy))
     check(rc, "moe_grouped_mm_dgrad")
     return out
 

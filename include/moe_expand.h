@@ -398,15 +398,20 @@ int moe_collect_row_grads(const float* rows, const int32_t* src2dst, const int32
  *   dw       [E, N, Kd] contiguous, out_dtype = dtype or MOE_F32; accumulate:
  *            added to what it holds (an expert without rows is left as it is),
  *            else overwritten (zeros for an expert without rows)
+ *   max_rows at most this many rows in all segments together (T*K of the
+ *            layout, or M_cap where nothing better is known). It chooses the
+ *            kernel's form and bounds its grid: rows past it are not computed
  * N, Kd and the row strides are multiples of 8, pointers 16-byte aligned,
  * E <= 1024. M_cap = 0 is allowed (row pointers may then be NULL).
  */
 int moe_grouped_mm(const void* x, int64_t ld_x, const void* w, const int32_t* start,
-                   const int32_t* psum, int dtype, int E, int N, int Kd, int64_t M_cap, void* out,
-                   int64_t ld_out, int32_t* d_status, moe_stream_t stream);
+                   const int32_t* psum, int dtype, int E, int N, int Kd, int64_t M_cap,
+                   int64_t max_rows, void* out, int64_t ld_out, int32_t* d_status,
+                   moe_stream_t stream);
 int moe_grouped_mm_dgrad(const void* dy, int64_t ld_dy, const void* w, const int32_t* start,
                          const int32_t* psum, int dtype, int E, int N, int Kd, int64_t M_cap,
-                         void* dx, int64_t ld_dx, int32_t* d_status, moe_stream_t stream);
+                         int64_t max_rows, void* dx, int64_t ld_dx, int32_t* d_status,
+                         moe_stream_t stream);
 int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
                          const int32_t* start, const int32_t* psum, int dtype, int E, int N, int Kd,
                          int64_t M_cap, void* dw, int out_dtype, int accumulate, int32_t* d_status,

@@ -119,6 +119,51 @@ def test_products(mx, seg, N, Kd, dtype):
             close(got[e], r, tol, f"wgrad {out} {acc}")
 
 
+FEW = {
+    "single tokens": [1, 0, 1, 1, 0, 0, 1, 0],
+    "a few": [3, 9, 0, 17, 30, 0, 1, 5],
+    "one crowded": [0] * 20 + [260] + [0] * 10 + [2],
+    "forty": [40, 33, 41, 0, 64, 65, 20, 37],
+}
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("N,Kd", [(136, 4104), (1000, 776), (72, 64), (4104, 136)])
+@pytest.mark.parametrize("seg", FEW)
+def test_few_rows(mx, seg, N, Kd, dtype):
+    """Few rows per expert: one and several chunks of rows, contractions whole
+    and split over the CTAs of a cluster, in a buffer (align 128) with far more
+    rows than pairs."""
+    counts = FEW[seg]
+    lay, bounds = layout_of(mx, counts, align=128, slack=5)
+    lay.src2dst = torch.zeros(sum(counts), 1, dtype=torch.int32, device="cuda")   # one pair per row
+    E, M = lay.E, lay.M_cap
+    g = gen(N + Kd)
+    x, dy = normal(g, M, Kd, dtype=dtype), normal(g, M, N, dtype=dtype)
+    w = normal(g, E, N, Kd, dtype=dtype, std=0.1)
+    inside = torch.zeros(M, dtype=torch.bool, device="cuda")
+    for a, b in bounds:
+        inside[a:b] = True
+    x[~inside] = float("nan")
+    dy[~inside] = float("nan")
+    y = torch.full((M, N), 7.0, dtype=dtype, device="cuda")
+    dx = torch.full((M, Kd), 7.0, dtype=dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mx.grouped_matmul(x, w, lay, out=y, status=status)
+    mx.grouped_matmul_dgrad(dy, w, lay, out=dx, status=status)
+    again = mx.grouped_matmul(x, w, lay, out=torch.full_like(y, 7.0))
+    torch.cuda.synchronize()
+    assert status.item() == 0 and torch.equal(again, y)
+    assert (y[~inside] == 7).all() and (dx[~inside] == 7).all()
+    for e, (a, b) in enumerate(bounds):
+        if b > a:
+            X, DY, W = x[a:b].double(), dy[a:b].double(), w[e].double()
+            r = X @ W.T
+            close(y[a:b], r, product_bound(X, W, r, dtype), "forward")
+            r = DY @ W
+            close(dx[a:b], r, product_bound(DY, W.T, r, dtype), "dgrad")
+
+
 def test_weights_of_other_experts_do_not_leak(mx):
     """N and Kd that end inside a tile: the neighbour's infinite and NaN
     weights lie right behind them in memory."""

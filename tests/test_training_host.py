@@ -55,8 +55,12 @@ def test_collect_row_grads_refuses(capi, p):
 def test_grouped_mm_refuses(capi, p, which):
     f = getattr(capi.load(), which)
 
-    def call(x=p, ld_x=64, w=p, start=p, psum=p, dt=capi.MOE_BF16, E=2, N=64, K=64, M=8, out=p, ld=64):
-        return f(x, ld_x, w, start, psum, dt, E, N, K, M, out, ld, None, None)
+    def call(x=p, ld_x=64, w=p, start=p, psum=p, dt=capi.MOE_BF16, E=2, N=64, K=64, M=8, most=None,
+             out=p, ld=64):
+        return f(x, ld_x, w, start, psum, dt, E, N, K, M, M if most is None else most, out, ld, None, None)
+
+    _refused(capi, call(most=9), "max_rows")
+    _refused(capi, call(most=-1), "max_rows")
 
     _refused(capi, call(x=None), "non-null")
     _refused(capi, call(w=None), "non-null")
