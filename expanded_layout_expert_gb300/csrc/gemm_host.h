@@ -23,9 +23,9 @@ int make_tmap_rows16(CUtensorMap* tm, const void* base, uint64_t width, uint64_t
 int make_tmap_weights16(CUtensorMap* tm, const void* base, uint64_t Kd, uint64_t N, uint64_t E,
                         uint32_t box_n);
 // Results [E, rows, width] with a row stride of `ld` values, 16-bit or fp32,
-// stored in boxes of 32 rows x 64 or 128 bytes, swizzled over that width.
+// stored in boxes of 32 rows x 64 bytes (64-byte swizzling).
 int make_tmap_result(CUtensorMap* tm, void* base, bool f32, uint64_t width, uint64_t rows, uint64_t E,
-                     uint64_t ld, uint32_t box_bytes);
+                     uint64_t ld);
 
 // Arguments of the block-scaled (ue8m0) grouped GEMM, already validated.
 struct MxGemmArgs {

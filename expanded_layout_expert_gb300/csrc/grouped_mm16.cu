@@ -25,8 +25,14 @@
 // comes first in the tile, so that this is done while the tensor core still
 // works on the tile before.
 //
-// Accumulation is in fp32 in tensor memory over the whole contraction; each
-// result is rounded once.
+// Accumulation is in fp32 and each result is rounded once. The tensor core
+// truncates where it adds, so its sums drift towards zero by about 1e-6 of
+// their size per 1024 contracted values (measured: 1.0e-6 at 1024 rows, 1.9e-5
+// at 16384, 8.7e-5 at 65536 against 1e-7 to 5e-7 of fp32 products). In
+// forward and dgrad that is far below the rounding to 16 bits. wgrad contracts
+// over as many rows as an expert has, so its sums leave tensor memory after at
+// most 896 rows (fp32 results; 4096 for 16-bit ones) and are added up, rounding to
+// nearest, in the epilogue's registers.
 //
 // Persistent CTAs, one per SM, warp-specialised as in grouped_gemm.cu: warp 0
 // TMA producer, warp 1 tcgen05.mma issuer, warp 2 zeroes ragged rows (wgrad),
@@ -69,22 +75,35 @@ constexpr int kTmemCols = kAcc * BN;
 constexpr int kEpiWarps = 8;     // two per TMEM lane quarter
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kMaxE = 1024;
-constexpr int kRaster = 8;       // row tiles in a column of the raster (see tile_at)
+// wgrad: blocks of BC summed in tensor memory at a time, at most. Short chunks
+// make the tensor core wait for an epilogue that is still storing the tile
+// before: with 8 blocks 16-bit results of 1024 rows an expert (4096 x 4096) take
+// 844 us, with up to 64 804, those of the Zipf batch (7168 x 2048) 2.08 and 1.97 ms;
+// fp32 results with 8 and 14 take 899 and 893 us.
+constexpr int max_chunk(bool out16) { return out16 ? 64 : 14; }
+// wgrad: warps 0-3 hand registers to the epilogue, whose threads hold 128 sums
+// (40 * 128 + 232 * 256 = 168 * 384, the registers the block is launched with).
+constexpr int kRegsLow = 40;
+constexpr int kRegsHigh = 232;
+// Row tiles in a column of the raster (see tile_at). Forward takes 3.52 ms with 8,
+// 3.62 with 4, 3.53 with 16 (Zipf rows, 4096 x 7168); wgrad added to fp32 1.07, 1.03
+// and 1.11 ms (1024 rows an expert, 4096 x 4096).
+constexpr int raster(int mode) { return mode == kWgrad ? 4 : 8; }
 
 // kCtas CTAs work on one tile of kCtas * 128 x 256.
-template <int kMode, int kCtas, bool Out16 = true>
+template <int kCtas>
 struct Cfg {
   static constexpr int BM = kCtas * BMC;
   static constexpr int kBRows = BN / kCtas;             // columns of D whose operand this CTA loads
   static constexpr int kABytes = BMC * BC * 2;
   static constexpr int kBBytes = kBRows * BC * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  // Of a row of D, staged at a time: 64 bytes leave room for six stages (at
+  // Of a row of D, staged at a time: 64 bytes leave room for six stages (with
   // 1024 ragged rows an expert and 4096 x 4096 weights wgrad took 767 cycles a
-  // block so, 785 with five stages and 128 bytes; forward 558 and 577). fp32
-  // rows take 128, so that a piece is 32 columns in either type.
-  static constexpr int kPieceBytes = Out16 ? 64 : 128;
-  static constexpr int kStages = kCtas == 2 ? (Out16 ? 6 : 5) : 3;
+  // block so, 785 with 128 bytes and five stages, forward 558 and 577, wgrad
+  // added to fp32 1.00 and 1.07 ms).
+  static constexpr int kPieceBytes = 64;
+  static constexpr int kStages = kCtas == 2 ? 6 : 3;
   static constexpr int kStoreOffset = kStages * kStageBytes;   // per epilogue warp: 32 rows of a piece
   static constexpr int kBarOffset = kStoreOffset + kEpiWarps * 32 * kPieceBytes;
   static constexpr int kNumBars = 4 * kStages + 2 * kAcc + 1;
@@ -186,8 +205,8 @@ MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abo
   }
 }
 
-// TMA store (kAdd: addition in fp32, done by L2) of a staged 128-byte-wide
-// piece; places past the tensor are not written.
+// TMA store (kAdd: addition in fp32, done by L2) of a staged piece of 32
+// rows; places past the tensor are not written.
 template <bool kAdd>
 MOE_DEV void tma_store_3d(const CUtensorMap* tm, uint32_t src, int32_t x, int32_t y, int32_t z) {
   if constexpr (kAdd)
@@ -251,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     grouped_mm16_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmD, const Params p) {
-  using C = Cfg<kMode, kCtas, Out16>;
+  using C = Cfg<kCtas>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   // the same offset in both CTAs of a pair: their windows begin alike
@@ -348,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
   const int num_tiles = kMode == kWgrad ? p.E * ni_w * nj : s_tp[p.E] * nj;
   const int first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
 
+  constexpr int kRaster = raster(kMode);
   // Tile id -> tile. Within an expert the tiles go in columns of kRaster row
   // tiles, row tile fastest, so the CTAs that run at one time share both
   // operands' panels in L2.
@@ -382,150 +402,166 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
   // blocks of BC along the contracted axis
   const int blocks_fd = ((kMode == kForward ? p.Kd : p.N) + BC - 1) / BC;
   auto num_blocks = [&](const Tile& t) { return kMode == kWgrad ? (t.rows + BC - 1) / BC : blocks_fd; };
+  // wgrad: blocks of a chunk, chunks being as equal as they can be
+  constexpr int kMaxChunk = max_chunk(Out16);
+  auto chunk_blocks = [&](int nb) {
+    const int chunks = (nb + kMaxChunk - 1) / kMaxChunk;
+    return (nb + chunks - 1) / chunks;
+  };
   // wgrad: rows of the ragged block (the tile's first), 0 if all are whole
   auto ragged = [&](const Tile& t) { return kMode == kWgrad ? t.rows % BC : 0; };
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------ producer
-    // Both CTAs' bytes are counted on the first CTA's barrier, those of a
-    // ragged block on each CTA's own, for the warp that zeroes rows there.
-    constexpr int kGroup = kCtas;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
-      const Tile t = tile_at(tile);
-      const int nb = num_blocks(t);
-      const int rag = ragged(t);
-      const int i0 = t.i0 + rank * (t.light ? BMC / 2 : BMC), j0 = t.j0 + rank * C::kBRows;
-      for (int b = 0; b < nb; ++b) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-        uint8_t* sa = smem + stage * C::kStageBytes;
-        uint8_t* sb = sa + C::kABytes;
-        uint32_t bar;
-        if (kMode == kWgrad && rag && b == 0) {
-          mbar_arrive_expect_tx(&rlanded[stage], C::kStageBytes);
-          bar = kCtas == 1 ? smem_u32(&rlanded[stage]) : cta_smem(&rlanded[stage], rank);
-        } else {
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], kCtas * C::kStageBytes);
-          bar = kCtas == 1 ? smem_u32(&full[stage]) : cta_smem(&full[stage], 0);
+  if (warp < 4) {
+    if constexpr (kMode == kWgrad) regs_release<kRegsLow>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ producer
+      // Both CTAs' bytes are counted on the first CTA's barrier, those of a
+      // ragged block on each CTA's own, for the warp that zeroes rows there.
+      constexpr int kGroup = kCtas;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+        const Tile t = tile_at(tile);
+        const int nb = num_blocks(t);
+        const int rag = ragged(t);
+        const int i0 = t.i0 + rank * (t.light ? BMC / 2 : BMC), j0 = t.j0 + rank * C::kBRows;
+        for (int b = 0; b < nb; ++b) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          uint8_t* sa = smem + stage * C::kStageBytes;
+          uint8_t* sb = sa + C::kABytes;
+          uint32_t bar;
+          if (kMode == kWgrad && rag && b == 0) {
+            mbar_arrive_expect_tx(&rlanded[stage], C::kStageBytes);
+            bar = kCtas == 1 ? smem_u32(&rlanded[stage]) : cta_smem(&rlanded[stage], rank);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], kCtas * C::kStageBytes);
+            bar = kCtas == 1 ? smem_u32(&full[stage]) : cta_smem(&full[stage], 0);
+          }
+          if (kMode == kForward) {
+            load_2d<kGroup>(sa, &tmA, b * BC, t.row0 + i0, bar);
+            load_3d<kGroup>(sb, &tmB, b * BC, j0, t.e, bar);
+          } else if (kMode == kDgrad) {
+            load_2d<kGroup>(sa, &tmA, b * BC, t.row0 + i0, bar);
+#pragma unroll
+            for (int q = 0; q < C::kBRows / 64; ++q)
+              load_3d<kGroup>(sb + q * kPanel, &tmB, j0 + q * 64, b * BC, t.e, bar);
+          } else {
+            // the ragged block first: it is the segment's last
+            const int c = rag ? (b == 0 ? t.rows - rag : (b - 1) * BC) : b * BC;
+#pragma unroll
+            for (int q = 0; q < BMC / 64; ++q)
+              load_2d<kGroup>(sa + q * kPanel, &tmA, i0 + q * 64, t.row0 + c, bar);
+#pragma unroll
+            for (int q = 0; q < C::kBRows / 64; ++q)
+              load_2d<kGroup>(sb + q * kPanel, &tmB, j0 + q * 64, t.row0 + c, bar);
+          }
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
-        if (kMode == kForward) {
-          load_2d<kGroup>(sa, &tmA, b * BC, t.row0 + i0, bar);
-          load_3d<kGroup>(sb, &tmB, b * BC, j0, t.e, bar);
-        } else if (kMode == kDgrad) {
-          load_2d<kGroup>(sa, &tmA, b * BC, t.row0 + i0, bar);
-#pragma unroll
-          for (int q = 0; q < C::kBRows / 64; ++q)
-            load_3d<kGroup>(sb + q * kPanel, &tmB, j0 + q * 64, b * BC, t.e, bar);
-        } else {
-          // the ragged block first: it is the segment's last
-          const int c = rag ? (b == 0 ? t.rows - rag : (b - 1) * BC) : b * BC;
-#pragma unroll
-          for (int q = 0; q < BMC / 64; ++q)
-            load_2d<kGroup>(sa + q * kPanel, &tmA, i0 + q * 64, t.row0 + c, bar);
-#pragma unroll
-          for (int q = 0; q < C::kBRows / 64; ++q)
-            load_2d<kGroup>(sb + q * kPanel, &tmB, j0 + q * 64, t.row0 + c, bar);
-        }
+      }
+      // Every load has landed before the CTA can exit: the tensor core has
+      // consumed (released) each stage once more. After a wait that gave up,
+      // this one is bounded too.
+      for (int i = 0; i < kStages; ++i) {
+        if (!drain_wait(&empty[stage], phase ^ 1u)) break;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
-    }
-    // Every load has landed before the CTA can exit: the tensor core has
-    // consumed (released) each stage once more. After a wait that gave up,
-    // this one is bounded too.
-    for (int i = 0; i < kStages; ++i) {
-      if (!drain_wait(&empty[stage], phase ^ 1u)) break;
-      if (++stage == kStages) { stage = 0; phase ^= 1u; }
-    }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_whole = idesc_f16(Half, kMode == kWgrad, kMode != kForward, C::BM, BN);
-    constexpr uint32_t idesc_light = idesc_f16(Half, kMode == kWgrad, kMode != kForward, BMC, BN);
-    int stage = 0, acc = 0;
-    uint32_t acc_phase = 0;
-    uint32_t full_phase = 0, rag_phase = 0;   // a bit per stage: uses so far
-    bool ok = true;
-    for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
-      const Tile t = tile_at(tile);
-      const int nb = num_blocks(t);
-      if (nb == 0) continue;   // wgrad of an expert without rows: the epilogue stores zeros
-      const int rag = ragged(t);
-      if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) break;
-      const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
-      const uint32_t idesc = t.light ? idesc_light : idesc_whole;
-      for (int b = 0; b < nb; ++b) {
-        const bool ragged_block = kMode == kWgrad && rag && b == 0;
-        uint64_t* landed = ragged_block ? &rzeroed[stage] : &full[stage];
-        uint32_t& uses = ragged_block ? rag_phase : full_phase;
-        ok = ragged_block && kCtas > 1 ? mbar_wait_cluster(landed, (uses >> stage) & 1u, abort_flag, p.status)
-                                       : mbar_wait(landed, (uses >> stage) & 1u, abort_flag, p.status);
-        if (!ok) break;
-        uses ^= 1u << stage;
-        tc_fence_after();
-        const uint32_t sa = smem_u32(smem + stage * C::kStageBytes);
-        const uint32_t sb = sa + C::kABytes;
-        // 16 contracted values on: 32 bytes along a c-contiguous row, 16 rows
-        // of 128 bytes otherwise
-        auto step = [&](int k) {
-          const uint64_t da = kMode == kWgrad ? sw128_mnmajor_desc(sa + k * kUmmaK * 128)
-                                              : sw128_kmajor_desc(sa + k * kUmmaK * 2);
-          const uint64_t db = kMode != kForward ? sw128_mnmajor_desc(sb + k * kUmmaK * 128)
-                                                : sw128_kmajor_desc(sb + k * kUmmaK * 2);
-          tc_mma_f16<kCtas>(d, da, db, idesc, (b > 0 || k > 0) ? 1u : 0u);
-        };
-        if (ragged_block) {
-          for (int k = 0; k < (rag + kUmmaK - 1) / kUmmaK; ++k) step(k);
-        } else {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc_whole = idesc_f16(Half, kMode == kWgrad, kMode != kForward, C::BM, BN);
+      constexpr uint32_t idesc_light = idesc_f16(Half, kMode == kWgrad, kMode != kForward, BMC, BN);
+      int stage = 0, acc = 0;
+      uint32_t acc_phase = 0;
+      uint32_t full_phase = 0, rag_phase = 0;   // a bit per stage: uses so far
+      bool ok = true;
+      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+        const Tile t = tile_at(tile);
+        const int nb = num_blocks(t);
+        if (nb == 0) continue;   // wgrad of an expert without rows: the epilogue stores zeros
+        const int rag = ragged(t);
+        const uint32_t idesc = t.light ? idesc_light : idesc_whole;
+        const int chunk = kMode == kWgrad ? chunk_blocks(nb) : nb;
+        for (int b0 = 0; b0 < nb && ok; b0 += chunk) {
+          if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+          const int b1 = min(b0 + chunk, nb);
+          for (int b = b0; b < b1; ++b) {
+            const bool ragged_block = kMode == kWgrad && rag && b == 0;
+            if (ragged_block) {
+              ok = kCtas > 1 ? mbar_wait_cluster(&rzeroed[stage], (rag_phase >> stage) & 1u, abort_flag, p.status)
+                             : mbar_wait(&rzeroed[stage], (rag_phase >> stage) & 1u, abort_flag, p.status);
+              rag_phase ^= 1u << stage;
+            } else {
+              ok = mbar_wait(&full[stage], (full_phase >> stage) & 1u, abort_flag, p.status);
+              full_phase ^= 1u << stage;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * C::kStageBytes);
+            const uint32_t sb = sa + C::kABytes;
+            // 16 contracted values on: 32 bytes along a c-contiguous row, 16
+            // rows of 128 bytes otherwise
+            auto step = [&](int k) {
+              const uint64_t da = kMode == kWgrad ? sw128_mnmajor_desc(sa + k * kUmmaK * 128)
+                                                  : sw128_kmajor_desc(sa + k * kUmmaK * 2);
+              const uint64_t db = kMode != kForward ? sw128_mnmajor_desc(sb + k * kUmmaK * 128)
+                                                    : sw128_kmajor_desc(sb + k * kUmmaK * 2);
+              tc_mma_f16<kCtas>(d, da, db, idesc, (b > b0 || k > 0) ? 1u : 0u);
+            };
+            if (ragged_block) {
+              for (int k = 0; k < (rag + kUmmaK - 1) / kUmmaK; ++k) step(k);
+            } else {
 #pragma unroll
-          for (int k = 0; k < BC / kUmmaK; ++k) step(k);
-        }
-        tc_commit_all<kCtas>(&empty[stage]);
-        if (++stage == kStages) stage = 0;
-      }
-      if (!ok) break;
-      tc_commit_all<kCtas>(&tfull[acc]);
-      if (++acc == kAcc) { acc = 0; acc_phase ^= 1u; }
-    }
-    // Every MMA issued so far must complete before TMEM is released.
-    tc_commit_own<kCtas>(mma_done);
-    drain_wait(mma_done, 0);
-  } else if (warp == 2 && kMode == kWgrad) {
-    // ------------------------------------------------- ragged rows to zero
-    // Only the rows up to the next multiple of 16 are read by the tensor core.
-    int stage = 0;
-    uint32_t uses = 0;   // a bit per stage
-    for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
-      const Tile t = tile_at(tile);
-      const int rag = ragged(t);
-      if (rag) {
-        if (!mbar_wait_warp(&rlanded[stage], (uses >> stage) & 1u, abort_flag, p.status)) break;
-        uses ^= 1u << stage;
-        const int r1 = (rag + kUmmaK - 1) / kUmmaK * kUmmaK;
-        uint8_t* s = smem + stage * C::kStageBytes;
-        const int per_panel = (r1 - rag) * 8;   // 16-byte vectors
-        for (int q = 0; q < C::kStageBytes / kPanel; ++q)
-          for (int v = lane; v < per_panel; v += 32)
-            *reinterpret_cast<uint4*>(s + q * kPanel + rag * 128 + v * 16) = make_uint4(0, 0, 0, 0);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (kCtas == 1) mbar_arrive(&rzeroed[stage]); else mbar_arrive_leader(&rzeroed[stage]);
+              for (int k = 0; k < BC / kUmmaK; ++k) step(k);
+            }
+            tc_commit_all<kCtas>(&empty[stage]);
+            if (++stage == kStages) stage = 0;
+          }
+          if (!ok) break;
+          tc_commit_all<kCtas>(&tfull[acc]);
+          if (++acc == kAcc) { acc = 0; acc_phase ^= 1u; }
         }
       }
-      stage = (stage + num_blocks(t)) % kStages;
+      // Every MMA issued so far must complete before TMEM is released.
+      tc_commit_own<kCtas>(mma_done);
+      drain_wait(mma_done, 0);
+    } else if (warp == 2 && kMode == kWgrad) {
+      // ------------------------------------------------- ragged rows to zero
+      // Only the rows up to the next multiple of 16 are read by the tensor core.
+      int stage = 0;
+      uint32_t uses = 0;   // a bit per stage
+      for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
+        const Tile t = tile_at(tile);
+        const int rag = ragged(t);
+        if (rag) {
+          if (!mbar_wait_warp(&rlanded[stage], (uses >> stage) & 1u, abort_flag, p.status)) break;
+          uses ^= 1u << stage;
+          const int r1 = (rag + kUmmaK - 1) / kUmmaK * kUmmaK;
+          uint8_t* s = smem + stage * C::kStageBytes;
+          const int per_panel = (r1 - rag) * 8;   // 16-byte vectors
+          for (int q = 0; q < C::kStageBytes / kPanel; ++q)
+            for (int v = lane; v < per_panel; v += 32)
+              *reinterpret_cast<uint4*>(s + q * kPanel + rag * 128 + v * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (kCtas == 1) mbar_arrive(&rzeroed[stage]); else mbar_arrive_leader(&rzeroed[stage]);
+          }
+        }
+        stage = (stage + num_blocks(t)) % kStages;
+      }
     }
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (kMode == kWgrad) regs_claim<kRegsHigh>();
     // ------------------------------------------------------------ epilogue
     // A thread owns one row of D (its TMEM lane) and 128 columns, in pieces of
-    // 32. A warp whose 32 rows are all D's (always in wgrad; in forward and
+    // 64 bytes. A warp whose 32 rows are all D's (always in wgrad; in forward and
     // dgrad all but a segment's last) stages a piece in shared memory
     // (swizzled: no bank conflicts) and one TMA store takes it out; fp32
     // results that are added to `out` are added by that store, in L2. The
     // other rows go straight from registers, a 32-byte sector per thread, as
     // do 16-bit results that are added to, whose sum is rounded once: their
-    // old values are asked for before the tile's products are waited for, or
-    // kAhead pieces early. Stores from registers alone slowed the products:
+    // old values are asked for kAhead pieces early. Stores from registers alone slowed the products:
     // with 1024 rows an expert and 4096 x 4096 weights wgrad took 930 cycles a
     // block of 64 rows with them, 738 with TMA stores, 750 with no stores at all.
     const int quarter = warp & 3;
@@ -533,10 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     constexpr int kElem = Out16 ? 2 : 4;
     constexpr bool kAddHere = Add && Out16;     // added in registers
     constexpr bool kTma = !kAddHere;
-    constexpr int kPiece = C::kPieceBytes;      // 64 or 128
+    constexpr int kPiece = C::kPieceBytes;
     constexpr int kWords = kPiece / 4;
-    constexpr int kCols = 32;                   // columns of D per piece
-    static_assert(kPiece == kCols * kElem, "a piece is 32 columns");
+    constexpr int kCols = kPiece / kElem;       // columns of D per piece: 32 or 16
     constexpr int kPieces = BN / 2 / kCols;
     const uint32_t stg = smem_u32(smem + C::kStoreOffset + (warp - 4) * 32 * kPiece);
     constexpr int kAhead = kAddHere ? 2 : 1;
@@ -545,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
     uint32_t acc_phase = 0;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
       const Tile t = tile_at(tile);
-      const bool empty_tile = num_blocks(t) == 0;
-      if (empty_tile && Add) continue;
+      if (Add && num_blocks(t) == 0) continue;   // an expert without rows adds nothing
       const int ilim = kMode == kWgrad ? p.N : t.rows;                // rows of D that exist
       // this warp's first row and column of D, and of the accumulator; a light
       // tile's 64 rows lie in lanes 0-63 with D's columns 0-127 and in lanes
@@ -566,44 +600,94 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
           load_sector(out + piece * kPiece + q * 32, &o[q * 8], ncols - piece * kCols - q * kSector,
                       kSector, p.wide);
       };
+      auto accumulator = [&]() {
+        return tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+               static_cast<uint32_t>(acc * BN + acol);
+      };
+      auto release = [&]() {   // its last read has landed
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 1) mbar_arrive(&tempty[acc]); else mbar_arrive_leader_relaxed(&tempty[acc]);
+        }
+        if (++acc == kAcc) { acc = 0; acc_phase ^= 1u; }
+      };
+      // wgrad: the thread's 128 results, the tile's chunks added up
+      float sum[kMode == kWgrad ? BN / 2 : 1];
+      uint32_t tq = 0;
+      bool ok = true;
+      if constexpr (kMode == kWgrad) {
+        const int nb = num_blocks(t);
+        const int chunk = nb > 0 ? chunk_blocks(nb) : 1;
+        if (nb == 0) {
+#pragma unroll
+          for (int k = 0; k < BN / 2; ++k) sum[k] = 0.0f;
+        } else {
+          ok = mbar_wait_warp(&tfull[acc], acc_phase, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ta = accumulator();
+#pragma unroll
+          for (int q = 0; q < BN / 32; ++q) {
+            uint32_t a[16];
+            tc_ld16_wait(ta + q * 16, a);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum[q * 16 + k] = __uint_as_float(a[k]);
+          }
+          release();
+        }
+#pragma unroll 1
+        for (int c = chunk; c < nb; c += chunk) {
+          ok = mbar_wait_warp(&tfull[acc], acc_phase, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ta = accumulator();
+#pragma unroll
+          for (int q = 0; q < BN / 32; ++q) {
+            uint32_t a[16];
+            tc_ld16_wait(ta + q * 16, a);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum[q * 16 + k] += __uint_as_float(a[k]);
+          }
+          release();
+        }
+      } else {
+        ok = mbar_wait_warp(&tfull[acc], acc_phase, abort_flag, p.status);
+        tc_fence_after();
+        tq = accumulator();
+      }
+      if (!ok) break;
       if constexpr (kAddHere) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) fetch(a, old[a]);
       }
-      if (!empty_tile) {
-        if (!mbar_wait_warp(&tfull[acc], acc_phase, abort_flag, p.status)) break;
-        tc_fence_after();
-      }
-      const uint32_t tq = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                          static_cast<uint32_t>(acc * BN + acol);
 #pragma unroll
       for (int piece = 0; piece < kPieces; ++piece) {
         if (kCtas == 2 && kMode != kWgrad && piece >= pieces) break;
         uint32_t w[kWords];   // the thread's row of the piece
-        if (empty_tile) {
+        float f[kCols];
+        if constexpr (kMode == kWgrad) {
 #pragma unroll
-          for (int k = 0; k < kWords; ++k) w[k] = 0u;
-        } else if constexpr (Out16) {
+          for (int k = 0; k < kCols; ++k) f[k] = sum[piece * kCols + k];
+        } else {
           uint32_t a[32];
           tc_ld32_wait(tq + piece * kCols, a);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x = __uint_as_float(a[2 * k]), y = __uint_as_float(a[2 * k + 1]);
+          for (int k = 0; k < kCols; ++k) f[k] = __uint_as_float(a[k]);
+          if (piece == pieces - 1) release();
+        }
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          if constexpr (Out16) {
+            float x = f[2 * k], y = f[2 * k + 1];
             if constexpr (kAddHere) {
               const float2 was = unpack2<Half>(old[piece % kAhead][k]);
               x += was.x;
               y += was.y;
             }
             w[k] = pack2<Half>(x, y);
-          }
-        } else {
-          tc_ld32_wait(tq + piece * kCols, w);
-        }
-        if (!empty_tile && piece == pieces - 1) {   // the last read has landed
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (kCtas == 1) mbar_arrive(&tempty[acc]); else mbar_arrive_leader_relaxed(&tempty[acc]);
+          } else {
+            w[k] = __float_as_uint(f[k]);
           }
         }
         if (by_tma) {
@@ -614,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
           for (int c = 0; c < kPiece / 16; ++c)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                              stg + lane * kPiece +
-                             ((c ^ (kPiece == 128 ? lane & 7 : (lane >> 1) & 3)) << 4)),
+                             ((c ^ ((lane >> 1) & 3)) << 4)),
                          "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                          : "memory");
           fence_async_smem();
@@ -631,7 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
             if (piece + kAhead < kPieces) fetch(piece + kAhead, old[piece % kAhead]);
         }
       }
-      if (!empty_tile && ++acc == kAcc) { acc = 0; acc_phase ^= 1u; }
     }
     if (kTma && lane == 0) tma_store_done();
   }
@@ -648,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
 template <int kMode, bool Half, bool Out16, bool Add, int kCtas>
 int launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const Params& p,
            int64_t max_tiles, cudaStream_t s) {
-  using C = Cfg<kMode, kCtas, Out16>;
+  using C = Cfg<kCtas>;
   auto* kernel = grouped_mm16_kernel<kMode, Half, Out16, Add, kCtas>;
   // clusters of the device that run at one time (a GPC may have an SM without
   // a partner), found once per device
@@ -739,7 +822,7 @@ int rows_times_weights(const char* what, bool dgrad, const void* a, int64_t ld_a
   CUtensorMap ta, tb, td;
   MOE_TRY(make_tmap_rows16(&ta, a, in, M_cap, ld_a, BMC));
   MOE_TRY(make_tmap_weights16(&tb, w, Kd, N, E, dgrad ? 64 : BN / 2));
-  MOE_TRY(make_tmap_result(&td, out, false, width, M_cap, 1, ld_out, Cfg<kForward, 2>::kPieceBytes));
+  MOE_TRY(make_tmap_result(&td, out, false, width, M_cap, 1, ld_out));
   Params p;
   p.start = start;
   p.psum = psum;
@@ -815,8 +898,7 @@ extern "C" int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x
     return MOE_OK;
   }
   CUtensorMap ta, tb, td;
-  MOE_TRY(make_tmap_result(&td, dw, out_dtype == MOE_F32, Kd, N, E, Kd,
-                           out_dtype == MOE_F32 ? 128 : Cfg<kWgrad, 2>::kPieceBytes));
+  MOE_TRY(make_tmap_result(&td, dw, out_dtype == MOE_F32, Kd, N, E, Kd));
   MOE_TRY(make_tmap_rows16(&ta, dy, N, M_cap, ld_dy, BC));
   MOE_TRY(make_tmap_rows16(&tb, x, Kd, M_cap, ld_x, BC));
   Params p;

@@ -104,6 +104,19 @@ MOE_DEV void tc_ld32_wait(uint32_t taddr, uint32_t (&v)[32]) {
   tc_regs_landed(v);
 }
 
+// 32 TMEM lanes x 16 columns, waited for.
+MOE_DEV void tc_ld16_wait(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Bounded wait used while draining: no abort check, only the time limit.
 MOE_DEV bool drain_wait(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();

@@ -66,14 +66,14 @@ int make_tmap_weights16(CUtensorMap* tm, const void* base, uint64_t Kd, uint64_t
 }
 
 int make_tmap_result(CUtensorMap* tm, void* base, bool f32, uint64_t width, uint64_t rows, uint64_t E,
-                     uint64_t ld, uint32_t box_bytes) {
+                     uint64_t ld) {
   const uint64_t size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {width, rows, E};
   const cuuint64_t strides[2] = {ld * size, rows * ld * size};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / size), 32u, 1u};
+  const cuuint32_t box[3] = {f32 ? 16u : 32u, 32u, 1u};
   return make_tmap16(tm, base, 3, dims, strides, box,
                      f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-                     box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                     CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int make_tmap_k128(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,

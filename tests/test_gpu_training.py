@@ -232,6 +232,27 @@ def test_products_of_many_tiles(mx, N, Kd, rows):
         close(dw[e], r, product_bound(DY.T, X.T, r, BF16) if b > a else torch.zeros_like(r), "wgrad")
 
 
+@pytest.mark.parametrize("mean", [0.0, 0.5])
+def test_long_sums_do_not_drift(mx, mean):
+    """wgrad over many rows, stored in fp32. The tensor core truncates its
+    sums: at most 56 additions (896 rows) of 2^-24 of their size before they
+    are added up rounding to nearest. Left alone for all 16384 rows they drift
+    by 1.9e-5."""
+    g = gen(6)
+    lay, bounds = layout_of(mx, [16384, 897, 0, 1793])
+    x = (normal(g, lay.M_cap, 264) + mean).to(BF16)
+    dy = (normal(g, lay.M_cap, 136) + mean).to(BF16)
+    base = normal(g, 4, 136, 264)
+    dw = mx.grouped_matmul_wgrad(dy, x, lay, out_dtype=F32)
+    added = mx.grouped_matmul_wgrad(dy, x, lay, out=base.clone(), accumulate=True)
+    for e, (a, b) in enumerate(bounds):
+        r = dy[a:b].double().T @ x[a:b].double()
+        bound = 60 * 2.0 ** -24
+        assert float((dw[e].double() - r).norm()) <= bound * float(r.norm())
+        r = r + base[e].double()
+        assert float((added[e].double() - r).norm()) <= bound * float(r.norm())
+
+
 def test_products_are_repeatable(mx):
     lay, _ = layout_of(mx, [200, 0, 77, 513])
     g = gen(4)
