@@ -45,7 +45,7 @@ def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype) -> tuple:
         raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    ld = t.stride(0) if rows > 1 else max(width, t.stride(0))
+    ld = t.stride(0) if rows > 1 else width   # one row has no stride to speak of
     if (t.stride(1) != 1 and width > 1) or ld < width:
         raise ValueError(f"{name} must have contiguous, non-overlapping rows")
     if not t.is_cuda:

@@ -593,6 +593,62 @@ def test_layer_against_autograd(mx, T, K, E, H, I, align, nv):
         layer.backward(dy)
 
 
+def test_nothing_to_do(mx):
+    """No tokens, no rows, no parameters; a single row with any stride."""
+    lay, _ = layout_of(mx, [0, 0])
+    lay.M_cap = 0
+    w = normal(gen(1), 2, 64, 72, dtype=BF16)
+    x, dy = w.new_zeros(0, 72), w.new_zeros(0, 64)
+    assert mx.grouped_matmul(x, w, lay).shape == (0, 64)
+    assert mx.grouped_matmul_dgrad(dy, w, lay).shape == (0, 72)
+    assert (mx.grouped_matmul_wgrad(dy, x, lay, out=torch.ones(2, 64, 72, device="cuda")) == 0).all()
+    kept = mx.grouped_matmul_wgrad(dy, x, lay, out=torch.ones(2, 64, 72, device="cuda"), accumulate=True)
+    assert (kept == 1).all()
+    assert mx.swiglu(dy, lay).shape == (0, 32)
+    dgu, dr = mx.swiglu_backward(dy[:, :32], dy, lay)
+    assert dgu.shape == (0, 64) and dr.shape == (0,)
+    lay.src2dst = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    assert mx.expand_rows(x, lay).shape == (0, 72)
+    assert mx.collect_row_grads(torch.zeros(0, device="cuda"), lay).shape == (0, 2)
+    opt = mx.AdamW([])
+    opt.step([])
+    assert opt.steps == 1
+    lay, _ = layout_of(mx, [0, 1])
+    row = normal(gen(2), 1, 75, dtype=BF16)[:, :72]
+    r = row.double() @ w[1].double().T
+    close(mx.grouped_matmul(row, w, lay), r, product_bound(row.double(), w[1].double(), r, BF16), "one row")
+    torch.cuda.synchronize()
+
+
+def test_capture(mx):
+    """A forward, backward and step recorded into a CUDA graph and replayed."""
+    g = gen(9)
+    T, K, E, H, I = 64, 2, 4, 128, 64
+    layer = mx.TrainableExperts(normal(g, E, 2 * I, H, dtype=BF16, std=0.1),
+                                normal(g, E, H, I, dtype=BF16, std=0.1), K=K, max_tokens=T)
+    x, dy = normal(g, T, H, dtype=BF16), normal(g, T, H, dtype=BF16)
+    w, ids = torch.rand(T, E, generator=g, device="cuda").topk(K, dim=1)
+    ids, w = ids.to(torch.int32).contiguous(), w.contiguous()
+
+    def step(stream=None):
+        y = layer.forward(x, ids, w, stream=stream)
+        dx, dw = layer.backward(dy, stream=stream)
+        return y, dx, dw, *layer.gradients
+
+    want = [t.clone() for t in step()]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            got = step(side)
+    for t in got:
+        t.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_other_stream(mx):
     """Calls queued on a stream of their own, behind work that makes their
     inputs there."""

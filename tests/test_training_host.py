@@ -145,3 +145,23 @@ def test_adamw_refuses(capi, p):
     _refused(capi, call(p=p + 2), "aligned")
     assert f(None, 0, 32, 1e-3, 0.9, 0.99, 1e-8, 0.0, 1, None, None) in (
         capi.MOE_OK, capi.MOE_ERR_UNSUPPORTED)   # nothing to do
+
+
+def test_grouped_product_kernels_keep_their_registers():
+    """wgrad's warps trade registers (setmaxnreg): 40 * 128 + 232 * 256 must be
+    exactly what the block of 384 threads is launched with, or the claim would
+    wait for registers that never come. Spills: at most twelve words, once a
+    tile; none in the kernels without a trade."""
+    from expanded_layout_expert_gb300 import build
+    wgrad = 0
+    for name, v in build.ptxas_usage("grouped_mm16.cu").items():
+        if "grouped_mm16_kernelILi2E" in name:
+            wgrad += 1
+            assert v["registers"] * 384 == 40 * 128 + 232 * 256, (name, v)
+            assert v["spill_st"] <= 48, (name, v)
+        else:
+            assert v["spill_st"] == 0 and v["stack"] == 0, (name, v)
+    assert wgrad == 16   # type x result type x added or not x CTAs a tile
+    for src in ("grouped_mm16_few.cu", "adamw.cu", "swiglu.cu", "expand_rows.cu"):
+        for name, v in build.ptxas_usage(src).items():
+            assert v["spill_st"] == 0, (name, v)
