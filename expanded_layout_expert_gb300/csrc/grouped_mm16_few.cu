@@ -129,6 +129,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       base += c;
     }
+    // more chunks than the grid has: the caller's bound on the rows was wrong
+    if (blockIdx.x == 0 && threadIdx.x == kThreads - 1 &&
+        static_cast<int64_t>(base) * ni * splits > static_cast<int64_t>(gridDim.x))
+      set_status(p.status, MOE_ERR_DEVICE_CHECK);
   }
   tc_fence_before();
   __syncthreads();
@@ -296,7 +300,10 @@ int launch_grouped_mm16_few(bool dgrad, bool half, const void* a, int64_t ld_a, 
   p.out = out;
   p.ld_out = ld_out;
   p.status = status;
-  // Experts that can have rows, and rows for about twice their mean.
+  // Experts that can have rows, and rows for about twice their mean: one token
+  // of 8 out of 64 experts of 4096 x 7168 takes 76 us with 16 rows a tile, 112
+  // with 128; 16 rows each of 32 experts of 4096 x 4096 164 us with 32, 172 with
+  // 128.
   const int64_t live = std::min<int64_t>(E, max_rows);
   const int64_t mean = (max_rows + live - 1) / live;
   p.rows = mean <= 8 ? 16 : (mean <= 20 ? 32 : (mean <= 48 ? 64 : 128));

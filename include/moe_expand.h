@@ -400,7 +400,8 @@ int moe_collect_row_grads(const float* rows, const int32_t* src2dst, const int32
  *            else overwritten (zeros for an expert without rows)
  *   max_rows at most this many rows in all segments together (T*K of the
  *            layout, or M_cap where nothing better is known). It chooses the
- *            kernel's form and bounds its grid: rows past it are not computed
+ *            kernel's form and bounds its grid: if the segments hold more,
+ *            some rows may be left out, with MOE_ERR_DEVICE_CHECK
  * N, Kd and the row strides are multiples of 8, pointers 16-byte aligned,
  * E <= 1024. M_cap = 0 is allowed (row pointers may then be NULL).
  */

@@ -593,6 +593,17 @@ def test_layer_against_autograd(mx, T, K, E, H, I, align, nv):
         layer.backward(dy)
 
 
+def test_wrong_bound_on_rows_is_flagged(mx):
+    """A layout that says it has three pairs, with segments of 200 rows: the
+    rows the few-rows form leaves out are not left out silently."""
+    lay, _ = layout_of(mx, [200, 0, 0, 0])
+    lay.src2dst = torch.zeros(3, 1, dtype=torch.int32, device="cuda")
+    w, x = normal(gen(1), 4, 64, 64, dtype=BF16), normal(gen(2), lay.M_cap, 64, dtype=BF16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mx.grouped_matmul(x, w, lay, status=status)
+    assert status.item() == -5   # MOE_ERR_DEVICE_CHECK
+
+
 def test_nothing_to_do(mx):
     """No tokens, no rows, no parameters; a single row with any stride."""
     lay, _ = layout_of(mx, [0, 0])
