@@ -41,12 +41,14 @@ def _code16(t: torch.Tensor, name: str) -> int:
 
 def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype) -> tuple:
     """(pointer, row stride) of a [rows, width] tensor with contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+    if t.shape != (rows, width):
         raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    ld = t.stride(0) if rows > 1 else width   # one row has no stride to speak of
-    if (t.stride(1) != 1 and width > 1) or ld < width:
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = width   # one row has no stride to speak of
+    if (one != 1 and width > 1) or ld < width:
         raise ValueError(f"{name} must have contiguous, non-overlapping rows")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
