@@ -82,9 +82,10 @@ constexpr int kMaxE = 1024;
 // fp32 results with 8 and 14 take 899 and 893 us.
 constexpr int max_chunk(bool out16) { return out16 ? 64 : 14; }
 // wgrad: warps 0-3 hand registers to the epilogue, whose threads hold 128 sums
-// (40 * 128 + 232 * 256 = 168 * 384, the registers the block is launched with).
-constexpr int kRegsLow = 40;
-constexpr int kRegsHigh = 232;
+// (56 * 128 + 224 * 256 = 168 * 384, the registers the block is launched with).
+constexpr int kRegsLow = 56;
+constexpr int kRegsHigh = 224;
+static_assert(kRegsLow * 128 + kRegsHigh * 256 == 168 * kThreads, "register split");
 // Row tiles in a column of the raster (see tile_at). Forward takes 3.52 ms with 8,
 // 3.62 with 4, 3.53 with 16 (Zipf rows, 4096 x 7168); wgrad added to fp32 1.07, 1.03
 // and 1.11 ms (1024 rows an expert, 4096 x 4096).
@@ -474,6 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       uint32_t acc_phase = 0;
       uint32_t full_phase = 0, rag_phase = 0;   // a bit per stage: uses so far
       bool ok = true;
+      const uint32_t ring = smem_u32(smem);
+      const uint64_t desc_a = kMode == kWgrad ? sw128_mnmajor_desc(ring) : sw128_kmajor_desc(ring);
+      const uint64_t desc_b = kMode != kForward ? sw128_mnmajor_desc(ring + C::kABytes)
+                                                : sw128_kmajor_desc(ring + C::kABytes);
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         const Tile t = tile_at(tile);
         const int nb = num_blocks(t);
@@ -497,16 +502,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
             }
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = smem_u32(smem + stage * C::kStageBytes);
-            const uint32_t sb = sa + C::kABytes;
-            // 16 contracted values on: 32 bytes along a c-contiguous row, 16
-            // rows of 128 bytes otherwise
+            // the descriptors' addresses are in 16-byte units; 16 contracted
+            // values on are 32 bytes along a c-contiguous row, 16 rows of 128
+            // bytes otherwise
+            const uint32_t at = static_cast<uint32_t>(stage * (C::kStageBytes >> 4));
+            const uint64_t da0 = desc_a + at, db0 = desc_b + at;
             auto step = [&](int k) {
-              const uint64_t da = kMode == kWgrad ? sw128_mnmajor_desc(sa + k * kUmmaK * 128)
-                                                  : sw128_kmajor_desc(sa + k * kUmmaK * 2);
-              const uint64_t db = kMode != kForward ? sw128_mnmajor_desc(sb + k * kUmmaK * 128)
-                                                    : sw128_kmajor_desc(sb + k * kUmmaK * 2);
-              tc_mma_f16<kCtas>(d, da, db, idesc, (b > b0 || k > 0) ? 1u : 0u);
+              constexpr int kAlong = kUmmaK * 2 / 16, kAcross = kUmmaK * 128 / 16;
+              tc_mma_f16<kCtas>(d, da0 + k * (kMode == kWgrad ? kAcross : kAlong),
+                                db0 + k * (kMode != kForward ? kAcross : kAlong), idesc,
+                                (b > b0 || k > 0) ? 1u : 0u);
             };
             if (ragged_block) {
               for (int k = 0; k < (rag + kUmmaK - 1) / kUmmaK; ++k) step(k);
