@@ -122,6 +122,7 @@ struct Params {
   void* out;             // forward [M_cap, ld_out = N..], dgrad [M_cap, Kd..], wgrad [E, N, Kd]
   int64_t ld_out;
   int wide;              // rows of out begin on 32-byte boundaries
+  int splits;            // CTAs of a cluster that share a tile's contraction (single-CTA wgrad)
   int32_t* status;
 };
 
@@ -267,7 +268,7 @@ struct Tile {
 // Out16: D is stored in the operands' type, else (wgrad) in fp32. Add: D is
 // added to what `out` holds.
 template <int kMode, bool Half, bool Out16, bool Add, int kCtas>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     grouped_mm16_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmD, const Params p) {
@@ -366,7 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
   const int nj = (cols + BN - 1) / BN;
   const int ni_w = (p.N + C::BM - 1) / C::BM;
   const int num_tiles = kMode == kWgrad ? p.E * ni_w * nj : s_tp[p.E] * nj;
-  const int first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
+  constexpr bool kCanSplit = kMode == kWgrad && kCtas == 1;
+  const int splits = kCanSplit ? p.splits : 1;
+  const int split = kCanSplit ? static_cast<int>(blockIdx.x) % splits : 0;
+  const int first_tile = blockIdx.x / (kCtas * splits), tile_step = gridDim.x / (kCtas * splits);
 
   constexpr int kRaster = raster(kMode);
   // Tile id -> tile. Within an expert the tiles go in columns of kRaster row
@@ -403,6 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
   // blocks of BC along the contracted axis
   const int blocks_fd = ((kMode == kForward ? p.Kd : p.N) + BC - 1) / BC;
   auto num_blocks = [&](const Tile& t) { return kMode == kWgrad ? (t.rows + BC - 1) / BC : blocks_fd; };
+  // this CTA's share of them: [first_block, end_block)
+  auto first_block = [&](const Tile& t) { return kCanSplit ? num_blocks(t) * split / splits : 0; };
+  auto end_block = [&](const Tile& t) {
+    return kCanSplit ? num_blocks(t) * (split + 1) / splits : num_blocks(t);
+  };
   // wgrad: blocks of a chunk, chunks being as equal as they can be
   constexpr int kMaxChunk = max_chunk(Out16);
   auto chunk_blocks = [&](int nb) {
@@ -424,10 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       bool ok = true;
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         const Tile t = tile_at(tile);
-        const int nb = num_blocks(t);
+        const int nb = end_block(t);
         const int rag = ragged(t);
         const int i0 = t.i0 + rank * (t.light ? BMC / 2 : BMC), j0 = t.j0 + rank * C::kBRows;
-        for (int b = 0; b < nb; ++b) {
+        for (int b = first_block(t); b < nb; ++b) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
           uint8_t* sa = smem + stage * C::kStageBytes;
           uint8_t* sb = sa + C::kABytes;
@@ -481,12 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
                                                 : sw128_kmajor_desc(ring + C::kABytes);
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         const Tile t = tile_at(tile);
-        const int nb = num_blocks(t);
-        if (nb == 0) continue;   // wgrad of an expert without rows: the epilogue stores zeros
+        const int bf = first_block(t), nb = end_block(t);
+        if (nb == bf) continue;   // wgrad of an expert without rows: the epilogue stores zeros
         const int rag = ragged(t);
         const uint32_t idesc = t.light ? idesc_light : idesc_whole;
-        const int chunk = kMode == kWgrad ? chunk_blocks(nb) : nb;
-        for (int b0 = 0; b0 < nb && ok; b0 += chunk) {
+        const int chunk = kMode == kWgrad ? chunk_blocks(nb - bf) : nb;
+        for (int b0 = bf; b0 < nb && ok; b0 += chunk) {
           if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
           const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
           const int b1 = min(b0 + chunk, nb);
@@ -537,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       uint32_t uses = 0;   // a bit per stage
       for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
         const Tile t = tile_at(tile);
-        const int rag = ragged(t);
+        const int rag = first_block(t) == 0 && end_block(t) > 0 ? ragged(t) : 0;
         if (rag) {
           if (!mbar_wait_warp(&rlanded[stage], (uses >> stage) & 1u, abort_flag, p.status)) break;
           uses ^= 1u << stage;
@@ -553,8 +562,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
             if (kCtas == 1) mbar_arrive(&rzeroed[stage]); else mbar_arrive_leader(&rzeroed[stage]);
           }
         }
-        stage = (stage + num_blocks(t)) % kStages;
+        stage = (stage + end_block(t) - first_block(t)) % kStages;
       }
+    }
+    if (kCanSplit && splits > 1) {   // the epilogue's two meetings
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
     }
   } else {
     if constexpr (kMode == kWgrad) regs_claim<kRegsHigh>();
@@ -622,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       uint32_t tq = 0;
       bool ok = true;
       if constexpr (kMode == kWgrad) {
-        const int nb = num_blocks(t);
+        const int nb = end_block(t) - first_block(t);
         const int chunk = nb > 0 ? chunk_blocks(nb) : 1;
         if (nb == 0) {
 #pragma unroll
@@ -662,6 +676,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
         tq = accumulator();
       }
       if (!ok) break;
+      if constexpr (kCanSplit) {
+        if (splits > 1) {
+          // The ring is free: every MMA of this CTA, its only tile's, is done.
+          float* part = reinterpret_cast<float*>(smem) + half_cols * BMC + quarter * 32 + lane;
+#pragma unroll
+          for (int k = 0; k < BN / 2; ++k) part[k * BMC] = sum[k];   // [column][row]
+          break;
+        }
+      }
       if constexpr (kAddHere) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) fetch(a, old[a]);
@@ -722,6 +745,61 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
       }
     }
     if (kTma && lane == 0) tma_store_done();
+    if constexpr (kCanSplit) {
+      if (splits > 1) {
+        // The partial sums of the cluster's CTAs, each CTA for its share of the
+        // columns, always in the same order. A lane takes four rows, so that a
+        // warp reads the 512 bytes of a column at once (distributed shared
+        // memory is slow where a warp's accesses are scattered: lanes that read
+        // 16 bytes of a row each made this step three times as long).
+        cluster_sync();
+        const Tile t = tile_at(first_tile);
+        const int i = t.i0 + lane * 4;
+        const int cw = BN / kEpiWarps / splits;   // columns of a warp: 16, 8 or 4
+        const int c0 = (split * kEpiWarps + (warp - 4)) * cw;
+        const bool skip = (Add && num_blocks(t) == 0) || *abort_flag;
+        for (int c = c0; c < c0 + cw && !skip; c += 4) {
+          float f[4][4] = {};   // [row][column]
+          for (int s = 0; s < splits; ++s) {
+            const uint32_t from = cta_smem(smem, s) + static_cast<uint32_t>((c * BMC + lane * 4) * 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float4 x;
+              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                           : "r"(from + k * BMC * 4));
+              f[0][k] += x.x;
+              f[1][k] += x.y;
+              f[2][k] += x.z;
+              f[3][k] += x.w;
+            }
+          }
+          if (t.j0 + c >= cols) continue;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (i + r >= p.N) break;
+            uint8_t* out = static_cast<uint8_t*>(p.out) +
+                           ((static_cast<int64_t>(t.e) * p.N + i + r) * p.ld_out + t.j0 + c) * kElem;
+            if constexpr (Out16) {
+              if (Add) {
+                const uint2 o = *reinterpret_cast<const uint2*>(out);
+                const float2 lo = unpack2<Half>(o.x), hi = unpack2<Half>(o.y);
+                f[r][0] += lo.x; f[r][1] += lo.y; f[r][2] += hi.x; f[r][3] += hi.y;
+              }
+              *reinterpret_cast<uint2*>(out) =
+                  make_uint2(pack2<Half>(f[r][0], f[r][1]), pack2<Half>(f[r][2], f[r][3]));
+            } else {
+              if (Add) {
+                const float4 o = *reinterpret_cast<const float4*>(out);
+                f[r][0] += o.x; f[r][1] += o.y; f[r][2] += o.z; f[r][3] += o.w;
+              }
+              *reinterpret_cast<float4*>(out) = make_float4(f[r][0], f[r][1], f[r][2], f[r][3]);
+            }
+          }
+        }
+        cluster_sync();   // no CTA leaves while its partial sums are read
+      }
+    }
   }
 
   tc_fence_before();
@@ -733,42 +811,66 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
   }
 }
 
+// Clusters of `size` CTAs of the kernel that the current device runs at one time
+// (a GPC's SMs need not be a multiple of it), found once per device, and the
+// kernel's shared memory allowed. 0 on an error (message set).
+template <int kMode, bool Half, bool Out16, bool Add, int kCtas>
+int resident_clusters(int size) {
+  using C = Cfg<kCtas>;
+  auto* kernel = grouped_mm16_kernel<kMode, Half, Out16, Add, kCtas>;
+  static std::atomic<int> found[64][4];   // size 1, 2, 4, 8
+  const int slot = size == 1 ? 0 : (size == 2 ? 1 : (size == 4 ? 2 : 3));
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  int n = found[dev][slot].load();
+  if (n != 0) return n;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::smem_bytes(kMaxE)) != cudaSuccess) {
+    check_launch("cudaFuncSetAttribute(grouped_mm16_kernel)");
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / size * size));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::smem_bytes(kMaxE);
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(size);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    check_launch("cudaOccupancyMaxActiveClusters(grouped_mm16_kernel)");
+    return 0;
+  }
+  if (n < 1) n = 1;
+  found[dev][slot].store(n);
+  return n;
+}
+
 template <int kMode, bool Half, bool Out16, bool Add, int kCtas>
 int launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const Params& p,
            int64_t max_tiles, cudaStream_t s) {
   using C = Cfg<kCtas>;
   auto* kernel = grouped_mm16_kernel<kMode, Half, Out16, Add, kCtas>;
-  // clusters of the device that run at one time (a GPC may have an SM without
-  // a partner), found once per device
-  static std::atomic<int> resident[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) dev = 0;
-  int n = resident[dev].load();
-  if (n == 0) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::smem_bytes(kMaxE)) != cudaSuccess)
-      return check_launch("cudaFuncSetAttribute(grouped_mm16_kernel)");
-    n = device_sm_count();
-    if (kCtas > 1) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(n / kCtas * kCtas));
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = C::smem_bytes(kMaxE);
-      cudaLaunchAttribute at = {};
-      at.id = cudaLaunchAttributeClusterDimension;
-      at.val.clusterDim.x = kCtas;
-      at.val.clusterDim.y = at.val.clusterDim.z = 1;
-      cfg.attrs = &at;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
-        return check_launch("cudaOccupancyMaxActiveClusters(grouped_mm16_kernel)");
-      if (n < 1) n = 1;
-    }
-    resident[dev].store(n);
-  }
-  const int64_t grid = n < max_tiles ? n : max_tiles;
-  kernel<<<static_cast<unsigned>(grid * kCtas), kThreads, C::smem_bytes(p.E), s>>>(ta, tb, td, p);
+  const int cluster = kCtas * p.splits;
+  const int n = resident_clusters<kMode, Half, Out16, Add, kCtas>(cluster);
+  if (n == 0) return MOE_ERR_CUDA;
+  // a split tile's cluster does that tile only
+  const int64_t grid = p.splits > 1 || max_tiles < n ? max_tiles : n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::smem_bytes(p.E);
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(cluster);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, ta, tb, td, p);
   return check_launch("grouped_mm16_kernel");
 }
 
@@ -838,6 +940,7 @@ int rows_times_weights(const char* what, bool dgrad, const void* a, int64_t ld_a
   p.out = out;
   p.ld_out = ld_out;
   p.wide = aligned(out, 32) && ld_out % 16 == 0;
+  p.splits = 1;
   p.status = d_status;
   const int64_t m_tiles = max_rows / (2 * BMC) + std::min<int64_t>(E, max_rows);
   const int64_t tiles = m_tiles * ((width + BN - 1) / BN);
@@ -918,9 +1021,20 @@ extern "C" int moe_grouped_mm_wgrad(const void* dy, int64_t ld_dy, const void* x
   p.wide = aligned(dw, 32) && (Kd % 16 == 0 || out_dtype == MOE_F32);
   p.status = d_status;
   const bool out16 = out_dtype != MOE_F32, add = accumulate != 0;
-  // One CTA a tile where a pair's second one would have no rows of D: 128 rows
-  // for each of 32 experts, N = 64, Kd = 4096 take 11.2 us, by pairs 16.9.
-  if (N > BMC)
+  // One CTA a tile where a pair's second one would have no rows of D (128 rows
+  // for each of 32 experts, N = 64, Kd = 4096 take 11.2 us, by pairs 16.9), and
+  // where there are so few such tiles that the rows can be shared by the CTAs of
+  // a cluster: all clusters run at once, each CTA has 12 blocks on average. One
+  // expert of 512 x 512 and 32768 rows takes 41 us in eight parts, 176 whole;
+  // eight of 4096 rows 28.7 in two, 29.7 whole; with 8 blocks a CTA (eight of 1024
+  // rows) parts cost 16.4 instead of 14.3; 16 tiles in eight parts, of which 15
+  // clusters run at once, 36 instead of 25 in four.
+  const int64_t tiles = static_cast<int64_t>(E) * ((N + BMC - 1) / BMC) * ((Kd + BN - 1) / BN);
+  const int64_t blocks = (M_cap / E + BC - 1) / BC;
+  p.splits = 1;
+  for (int k = 8; k > 1 && p.splits == 1; k /= 2)
+    if (blocks / k >= 12 && tiles <= resident_clusters<kWgrad, false, true, false, 1>(k)) p.splits = k;
+  if (N > BMC && p.splits == 1)
     return dtype == MOE_F16 ? launch_wgrad<true, 2>(ta, tb, td, p, out16, add, s)
                             : launch_wgrad<false, 2>(ta, tb, td, p, out16, add, s);
   return dtype == MOE_F16 ? launch_wgrad<true, 1>(ta, tb, td, p, out16, add, s)

@@ -732,3 +732,52 @@ def test_example_learns(mx, bits):
     losses = m.main(["--steps", "80", "--state-bits", str(bits)])
     assert all(np.isfinite(losses))
     assert np.mean(losses[-5:]) < 0.5 * np.mean(losses[:5]), (losses[:5], losses[-5:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("N,Kd", [(64, 72), (200, 520), (512, 512)])
+@pytest.mark.parametrize("counts", [[2000], [777, 0, 1, 5003], [64 * 40, 64 * 8 + 1]],
+                         ids=["one", "uneven", "whole blocks"])
+def test_wgrad_of_few_tiles_over_many_rows(mx, counts, N, Kd, dtype):
+    """Few tiles, long sums: the rows are shared by the CTAs of a cluster, some
+    of which have none for a small expert."""
+    lay, bounds = layout_of(mx, counts, slack=2)
+    M, E = lay.M_cap, lay.E
+    g = gen(N + Kd)
+    x, dy = normal(g, M, Kd + 8, dtype=dtype)[:, :Kd], normal(g, M, N, dtype=dtype)
+    x[bounds[-1][1]:] = float("nan")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for out in (dtype, F32):
+        for acc in (False, True):
+            base = normal(gen(3), E, N, Kd, dtype=out)
+            got = mx.grouped_matmul_wgrad(dy, x, lay, out=base.clone(), accumulate=acc, status=status)
+            again = mx.grouped_matmul_wgrad(dy, x, lay, out=base.clone(), accumulate=acc)
+            assert torch.equal(got, again)
+            for e, (a, b) in enumerate(bounds):
+                X, DY = x[a:b].double(), dy[a:b].double()
+                r = DY.T @ X + (base[e].double() if acc else 0)
+                tol = product_bound(DY.T, X.T, r, out) if b > a else torch.zeros_like(r)
+                if acc:
+                    tol = tol + 2.0 ** -24 * r.abs()
+                close(got[e], r, tol, f"wgrad {out} {acc}")
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("counts", [[50000], [9000, 3, 0, 40, 6000]], ids=["eight parts", "four parts"])
+def test_wgrad_in_parts(mx, counts):
+    """More parts than the smaller experts have blocks of rows."""
+    lay, bounds = layout_of(mx, counts)
+    g = gen(12)
+    x, dy = normal(g, lay.M_cap, 200, dtype=BF16), normal(g, lay.M_cap, 136, dtype=BF16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for out in (BF16, F32):
+        for acc in (False, True):
+            base = normal(gen(3), lay.E, 136, 200, dtype=out)
+            got = mx.grouped_matmul_wgrad(dy, x, lay, out=base.clone(), accumulate=acc, status=status)
+            for e, (a, b) in enumerate(bounds):
+                r = dy[a:b].double().T @ x[a:b].double() + (base[e].double() if acc else 0)
+                # chunks of 896 rows, or 4096 for 16-bit results, then the parts
+                drift = (60 if out is F32 else 260) * 2.0 ** -24
+                bound = (drift + (U[out] if out is BF16 else 0)) * float(r.norm())
+                assert float((got[e].double() - r).norm()) <= bound, (out, acc, e)
+    assert status.item() == 0
