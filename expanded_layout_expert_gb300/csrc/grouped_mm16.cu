@@ -43,8 +43,9 @@
 // cycles (1024 rows an expert, 4096 x 4096, forward), with pairs 558; the
 // tensor core's own time is 512. A segment's last tile, if it has at most 128
 // rows, is done with 64 rows per CTA (300 rows an expert: 331 instead of 367
-// us). wgrad with N <= 128 has single-CTA tiles; forward and dgrad of experts
-// with few rows are grouped_mm16_few.cu's.
+// us). wgrad has single-CTA tiles where N <= 128, and where tiles are so few that
+// their rows are shared by a cluster; forward and dgrad of experts with few rows
+// are grouped_mm16_few.cu's.
 //
 // What bounds it: power. Forward and dgrad run at 1.6 PFLOP/s with the SM clock
 // held near 1.4 GHz by the power limit, 92-97 % of what the library's product
@@ -580,9 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // results that are added to `out` are added by that store, in L2. The
     // other rows go straight from registers, a 32-byte sector per thread, as
     // do 16-bit results that are added to, whose sum is rounded once: their
-    // old values are asked for kAhead pieces early. Stores from registers alone slowed the products:
-    // with 1024 rows an expert and 4096 x 4096 weights wgrad took 930 cycles a
-    // block of 64 rows with them, 738 with TMA stores, 750 with no stores at all.
+    // old values are asked for kAhead pieces early. Stores from registers alone
+    // slowed the products: with 1024 rows an expert and 4096 x 4096 weights wgrad
+    // took 930 cycles a block of 64 rows with them, 738 with TMA stores, 750 with
+    // no stores at all.
     const int quarter = warp & 3;
     const int half_cols = ((warp - 4) >> 2) * (BN / 2);
     constexpr int kElem = Out16 ? 2 : 4;
