@@ -15,8 +15,8 @@
 // loads in flight each; a CTA does one tile, so that the hardware evens out
 // the work and one CTA's start and end hide under the other's loads.
 // Measured (in a graph): a decode batch of 32 rows for each of 64 experts of
-// 4096 x 7168, 551 us, 6.8 TB/s of weights; one token of 8 of those experts, 76
-// us (6.2 TB/s), where tiles of 256 weight rows by CTA pairs took 104; 18 experts
+// 4096 x 7168, 551 us, 6.8 TB/s of weights; one token of 8 of those experts, 73
+// us (6.4 TB/s), where tiles of 256 weight rows by CTA pairs took 104; 18 experts
 // of 96 x 4032 with a row each, 7.6 us (22 by pairs).
 #include <algorithm>
 #include <atomic>
@@ -301,7 +301,7 @@ int launch_grouped_mm16_few(bool dgrad, bool half, const void* a, int64_t ld_a, 
   p.ld_out = ld_out;
   p.status = status;
   // Experts that can have rows, and rows for about twice their mean: one token
-  // of 8 out of 64 experts of 4096 x 7168 takes 76 us with 16 rows a tile, 112
+  // of 8 out of 64 experts of 4096 x 7168 takes 73 us with 16 rows a tile, 112
   // with 128; 16 rows each of 32 experts of 4096 x 4096 164 us with 32, 172 with
   // 128.
   const int64_t live = std::min<int64_t>(E, max_rows);
@@ -309,12 +309,13 @@ int launch_grouped_mm16_few(bool dgrad, bool half, const void* a, int64_t ld_a, 
   p.rows = mean <= 8 ? 16 : (mean <= 20 ? 32 : (mean <= 48 ? 64 : 128));
   p.stages = stages_for(p.rows);
   const int64_t ni = (p.width + kI - 1) / kI;
-  // Splits: until every SM has two CTAs, none with less than six blocks. More
-  // (up to four or eight CTAs an SM) cost more in their starts than they even
-  // out: 82 and 95 us instead of 76 for one token of 8 out of 64 experts of
-  // 4096 x 7168. Two experts' 96 x 4032 take 7.6 us in eight parts, 9.4 in
-  // four; 512 x 512 takes 6.6 us whole, 7.5 in two.
-  const int64_t want = 2 * static_cast<int64_t>(device_sm_count());
+  // Splits: until every SM has a CTA, none with less than six blocks. More cost
+  // more in their starts than they even out: one token of 8 out of 64 experts of
+  // 4096 x 7168 takes 73 us whole (256 tiles), 76, 82 and 95 in two, four and
+  // eight parts; six experts of 3416 x 6344 48 whole, 59 in two. Two experts' 96 x
+  // 4032 take 7.6 us in eight parts, 9.4 in four; 512 x 512 takes 6.6 whole, 7.5 in
+  // two.
+  const int64_t want = device_sm_count();
   p.splits = 1;
   while (p.splits < 8 && live * ni * p.splits < want && p.blocks / (2 * p.splits) >= 6) p.splits *= 2;
   const int64_t tiles = (max_rows / p.rows + live) * ni;
