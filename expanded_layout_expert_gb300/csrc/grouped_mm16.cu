@@ -165,6 +165,7 @@ MOE_DEV void tmem_alloc_n(uint32_t* slot, uint32_t ncols) {
 }
 template <int kCtas>
 MOE_DEV void tmem_dealloc_n(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();   // lane 0 comes from a role of its own
   if constexpr (kCtas == 1)
     tmem_dealloc(taddr, ncols);
   else
@@ -567,7 +568,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (kCanSplit && splits > 1) {   // the epilogue's two meetings
-      __syncwarp();
       cluster_sync();
       cluster_sync();
     }
@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kCols; ++k) f[k] = sum[piece * kCols + k];
         } else {
           uint32_t a[32];
+          __syncwarp();   // the stores of the piece before differ from lane to lane
           tc_ld32_wait(tq + piece * kCols, a);
 #pragma unroll
           for (int k = 0; k < kCols; ++k) f[k] = __uint_as_float(a[k]);

@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       float* part = reinterpret_cast<float*>(smem);   // the ring is free: every MMA is done
       for (int r0 = 0; r0 < rows && got; r0 += 32) {
         uint32_t v[32];
+        __syncwarp();   // lanes past the last weight row stored nothing
         tc_ld32_wait(tmem + (static_cast<uint32_t>(warp * 32) << 16) + r0, v);
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
@@ -212,7 +213,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    __syncwarp();
     if (splits > 1) {
       cluster_sync();
       if (warp < 4) {
@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   if (warp == 5) {
     tc_fence_after();
+    __syncwarp();   // lane 0 comes from the issuer's role
     tmem_dealloc(tmem, tmem_cols);
   }
 }

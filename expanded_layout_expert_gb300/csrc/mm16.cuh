@@ -59,7 +59,10 @@ MOE_DEV uint32_t cta_smem(const void* p, int rank) {
   return r;
 }
 
+// The .aligned forms want the whole warp at the instruction, so the lanes meet
+// first, wherever the branches before it have left them.
 MOE_DEV void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
