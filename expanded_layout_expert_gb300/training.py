@@ -5,7 +5,8 @@ together.
 Each function marshals torch tensors and the current CUDA stream into one C
 call, as the package's other functions do. Row tensors may have a row stride
 larger than the row (a multiple of 8 values); rows outside the segments
-[start[e], psum[e]) of the layout are neither used nor written.
+[start[e], psum[e]) of the layout are neither used nor written. A result that a
+call makes itself is made on the stream the call is queued on.
 """
 from __future__ import annotations
 
@@ -29,6 +30,16 @@ def _stream(stream, device_of: torch.Tensor):
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device_of.get_device())
+
+
+def _new(make, shape: tuple, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A result tensor, made by torch.zeros or torch.empty on the stream that
+    fills it: zeroed on another one it could be wiped after the kernel, and
+    its memory given away while the kernel still writes."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
 
 
 def _code16(t: torch.Tensor, name: str) -> int:
@@ -97,9 +108,9 @@ def expand_rows(x: torch.Tensor, lay, topk_w: Optional[torch.Tensor] = None,
     K = lay.src2dst.shape[1]
     _code16(x, "x")
     if out is None:
-        out = torch.zeros(lay.M_cap, H, dtype=x.dtype, device=x.device)
+        out = _new(torch.zeros, (lay.M_cap, H), x.dtype, x, stream)
     if topk_w is not None and row_w is None:
-        row_w = torch.zeros(lay.M_cap, dtype=torch.float32, device=x.device)
+        row_w = _new(torch.zeros, (lay.M_cap,), torch.float32, x, stream)
     if topk_w is None and row_w is not None:
         raise ValueError("row_w needs topk_w")
     xp, ld_x = _rows(x, "x", T, H, x.dtype)
@@ -121,7 +132,7 @@ def collect_row_grads(rows: torch.Tensor, lay, n_valid: Optional[torch.Tensor] =
     where there is no pair (the gradient of the top-k weights)."""
     T, K = lay.src2dst.shape
     if out is None:
-        out = torch.zeros(T, K, dtype=torch.float32, device=rows.device)
+        out = _new(torch.zeros, (T, K), torch.float32, rows, stream)
     rc = load().moe_collect_row_grads(
         _whole(rows, "rows", (lay.M_cap,), torch.float32),
         _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32), _word(n_valid, "n_valid"), T, K,
@@ -139,7 +150,7 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, lay, out: Optional[torch.Te
     M, Kd = x.shape
     N = w.shape[1]
     if out is None:
-        out = torch.zeros(M, N, dtype=x.dtype, device=x.device)
+        out = _new(torch.zeros, (M, N), x.dtype, x, stream)
     xp, ld_x = _rows(x, "x", M, Kd, x.dtype)
     op, ld_o = _rows(out, "out", M, N, x.dtype)
     rc = load().moe_grouped_mm(xp, ld_x, _whole(w, "w", (E, N, Kd), x.dtype), start, psum, dt, E, N,
@@ -158,7 +169,7 @@ def grouped_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, lay, out: Optional[t
     M, N = dy.shape
     Kd = w.shape[2]
     if out is None:
-        out = torch.zeros(M, Kd, dtype=dy.dtype, device=dy.device)
+        out = _new(torch.zeros, (M, Kd), dy.dtype, dy, stream)
     dp, ld_d = _rows(dy, "dy", M, N, dy.dtype)
     op, ld_o = _rows(out, "out", M, Kd, dy.dtype)
     rc = load().moe_grouped_mm_dgrad(dp, ld_d, _whole(w, "w", (E, N, Kd), dy.dtype), start, psum, dt,
@@ -181,7 +192,7 @@ def grouped_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, lay, out: Optional[t
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(E, N, Kd, dtype=out_dtype or dy.dtype, device=dy.device)
+        out = _new(torch.empty, (E, N, Kd), out_dtype or dy.dtype, dy, stream)
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
     if out.dtype is not dy.dtype and out.dtype is not torch.float32:
@@ -204,7 +215,7 @@ def swiglu(gu: torch.Tensor, lay, row_w: Optional[torch.Tensor] = None,
     if two % 2:
         raise ValueError("gu must have an even number of columns")
     if out is None:
-        out = torch.zeros(M, two // 2, dtype=gu.dtype, device=gu.device)
+        out = _new(torch.zeros, (M, two // 2), gu.dtype, gu, stream)
     gp, ld_g = _rows(gu, "gu", M, two, gu.dtype)
     op, ld_o = _rows(out, "out", M, two // 2, gu.dtype)
     rc = load().moe_swiglu(gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32),
@@ -223,9 +234,9 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, lay, row_w: Optional[tor
     if two % 2:
         raise ValueError("gu must have an even number of columns")
     if dgu is None:
-        dgu = torch.zeros(M, two, dtype=gu.dtype, device=gu.device)
+        dgu = _new(torch.zeros, (M, two), gu.dtype, gu, stream)
     if drow_w is None:
-        drow_w = torch.zeros(M, dtype=torch.float32, device=gu.device)
+        drow_w = _new(torch.zeros, (M,), torch.float32, gu, stream)
     gp, ld_g = _rows(gu, "gu", M, two, gu.dtype)
     hp, ld_h = _rows(dh, "dh", M, two // 2, gu.dtype)
     op, ld_o = _rows(dgu, "dgu", M, two, gu.dtype)
