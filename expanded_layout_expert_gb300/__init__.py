@@ -3,9 +3,10 @@
 A thin binding over libmoe_expand.so (include/moe_expand.h): each function
 marshals torch tensors (device memory, owned by the caller) and the current
 CUDA stream into one C call; every step of the layer runs in the library's
-CUDA kernels. ``ExpandedMoELayer`` strings the calls together with buffers
-allocated once. The experts' training in 16 bits over the same layout is in
-``training.py``: grouped products with both gradients, SwiGLU, AdamW, and
+CUDA kernels. Results and workspaces that a call makes itself are made on the
+stream it is queued on. ``ExpandedMoELayer`` strings the calls together with
+buffers allocated once. The experts' training in 16 bits over the same layout
+is in ``training.py``: grouped products with both gradients, SwiGLU, AdamW, and
 ``TrainableExperts``, which strings those together.
 """
 from __future__ import annotations
@@ -93,16 +94,18 @@ def expand_layout(topk_ids: torch.Tensor, E: int, align: int, M_cap: int,
                   stream=None) -> Layout:
     T, K = topk_ids.shape
     dev = topk_ids.device
-    if out is None:
-        out = Layout(psum=torch.empty(E, dtype=torch.int32, device=dev),
-                     start=torch.empty(E, dtype=torch.int32, device=dev),
-                     total=torch.empty(1, dtype=torch.int32, device=dev),
-                     m_indices=torch.empty(M_cap, dtype=torch.int32, device=dev),
-                     src2dst=torch.empty(T, K, dtype=torch.int32, device=dev),
-                     tile_prefix=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                     E=E, align=align, M_cap=M_cap)
-    if ws is None:
-        ws = torch.zeros(workspace_size(T, K, E), dtype=torch.uint8, device=dev)
+    if out is None or ws is None:
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = Layout(psum=torch.empty(E, dtype=torch.int32, device=dev),
+                             start=torch.empty(E, dtype=torch.int32, device=dev),
+                             total=torch.empty(1, dtype=torch.int32, device=dev),
+                             m_indices=torch.empty(M_cap, dtype=torch.int32, device=dev),
+                             src2dst=torch.empty(T, K, dtype=torch.int32, device=dev),
+                             tile_prefix=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                             E=E, align=align, M_cap=M_cap)
+            if ws is None:
+                ws = torch.zeros(workspace_size(T, K, E), dtype=torch.uint8, device=dev)
     rc = load().moe_expand_layout(_ptr(topk_ids), T, K, E, align, _ptr(n_valid), M_cap,
                                   _ptr(out.psum), _ptr(out.start), _ptr(out.total),
                                   _ptr(out.m_indices), _ptr(out.src2dst), _ptr(out.tile_prefix),
@@ -119,12 +122,14 @@ def expand_scatter(x_q: torch.Tensor, x_scale: torch.Tensor, scale_layout: int,
     T, H = x_q.shape
     K = topk_w.shape[1]
     dev = x_q.device
-    if xe is None:
-        xe = torch.zeros(lay.M_cap, H, dtype=torch.uint8, device=dev)
-    if xe_scale is None:
-        xe_scale = new_scale(lay.M_cap, H // 128, scale_layout, dev)
-    if row_w is None:
-        row_w = torch.zeros(lay.M_cap, dtype=torch.float32, device=dev)
+    if xe is None or xe_scale is None or row_w is None:
+        with torch.cuda.stream(stream):
+            if xe is None:
+                xe = torch.zeros(lay.M_cap, H, dtype=torch.uint8, device=dev)
+            if xe_scale is None:
+                xe_scale = new_scale(lay.M_cap, H // 128, scale_layout, dev)
+            if row_w is None:
+                row_w = torch.zeros(lay.M_cap, dtype=torch.float32, device=dev)
     rc = load().moe_expand_scatter(_ptr(x_q), _ptr(x_scale), scale_layout, x_scale.shape[1],
                                    _ptr(topk_w), _ptr(lay.src2dst), _ptr(lay.psum),
                                    _ptr(lay.start), _ptr(n_valid), T, H, K, lay.E, lay.align,
@@ -148,22 +153,24 @@ def expand_layout_scatter(x_q: torch.Tensor, x_scale: torch.Tensor, scale_layout
     T, H = x_q.shape
     K = topk_ids.shape[1]
     dev = x_q.device
-    if out is None:
-        out = Layout(psum=torch.empty(E, dtype=torch.int32, device=dev),
-                     start=torch.empty(E, dtype=torch.int32, device=dev),
-                     total=torch.empty(1, dtype=torch.int32, device=dev),
-                     m_indices=torch.empty(M_cap, dtype=torch.int32, device=dev),
-                     src2dst=torch.empty(T, K, dtype=torch.int32, device=dev),
-                     tile_prefix=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                     E=E, align=align, M_cap=M_cap)
-    if ws is None:
-        ws = torch.zeros(workspace_size(T, K, E), dtype=torch.uint8, device=dev)
-    if xe is None:
-        xe = torch.zeros(M_cap, H, dtype=torch.uint8, device=dev)
-    if xe_scale is None:
-        xe_scale = new_scale(M_cap, H // 128, scale_layout, dev)
-    if row_w is None:
-        row_w = torch.zeros(M_cap, dtype=torch.float32, device=dev)
+    if out is None or ws is None or xe is None or xe_scale is None or row_w is None:
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = Layout(psum=torch.empty(E, dtype=torch.int32, device=dev),
+                             start=torch.empty(E, dtype=torch.int32, device=dev),
+                             total=torch.empty(1, dtype=torch.int32, device=dev),
+                             m_indices=torch.empty(M_cap, dtype=torch.int32, device=dev),
+                             src2dst=torch.empty(T, K, dtype=torch.int32, device=dev),
+                             tile_prefix=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                             E=E, align=align, M_cap=M_cap)
+            if ws is None:
+                ws = torch.zeros(workspace_size(T, K, E), dtype=torch.uint8, device=dev)
+            if xe is None:
+                xe = torch.zeros(M_cap, H, dtype=torch.uint8, device=dev)
+            if xe_scale is None:
+                xe_scale = new_scale(M_cap, H // 128, scale_layout, dev)
+            if row_w is None:
+                row_w = torch.zeros(M_cap, dtype=torch.float32, device=dev)
     rc = load().moe_expand_layout_scatter(
         _ptr(topk_ids), _ptr(topk_w), _ptr(x_q), _ptr(x_scale), scale_layout, x_scale.shape[1], T,
         H, K, E, align, _ptr(n_valid), M_cap, _ptr(out.psum), _ptr(out.start), _ptr(out.total),
@@ -180,7 +187,8 @@ def grouped_gemm(A: torch.Tensor, A_scale: torch.Tensor, scale_layout: int, lay:
     M_cap, Kd = A.shape
     E, N, _ = W.shape
     if out is None:
-        out = torch.zeros(M_cap, N, dtype=torch.bfloat16, device=A.device)
+        with torch.cuda.stream(stream):
+            out = torch.zeros(M_cap, N, dtype=torch.bfloat16, device=A.device)
     rc = load().moe_grouped_gemm(_ptr(A), _ptr(A_scale), scale_layout, A_scale.shape[1],
                                  _ptr(lay.start), _ptr(lay.tile_prefix), _ptr(lay.total),
                                  _ptr(W), _ptr(W_scale), _ptr(row_w), flags, E, N, Kd, M_cap,
@@ -195,10 +203,12 @@ def act_quant(gu: torch.Tensor, row_w: Optional[torch.Tensor], flags: int, scale
               stream=None):
     M_cap, twoI = gu.shape
     I = twoI // 2
-    if di is None:
-        di = torch.zeros(M_cap, I, dtype=torch.uint8, device=gu.device)
-    if di_scale is None:
-        di_scale = new_scale(M_cap, I // 128, scale_layout, gu.device)
+    if di is None or di_scale is None:
+        with torch.cuda.stream(stream):
+            if di is None:
+                di = torch.zeros(M_cap, I, dtype=torch.uint8, device=gu.device)
+            if di_scale is None:
+                di_scale = new_scale(M_cap, I // 128, scale_layout, gu.device)
     rc = load().moe_act_quant(_ptr(gu), I, _ptr(row_w), flags, scale_layout, _ptr(total), M_cap,
                               _ptr(di), _ptr(di_scale), di_scale.shape[1], _ptr(status),
                               _stream(stream))
@@ -216,10 +226,12 @@ def grouped_gemm_act_quant(A: torch.Tensor, A_scale: torch.Tensor, scale_layout:
     M_cap, H = A.shape
     E, twoI, _ = W13.shape
     I = twoI // 2
-    if di is None:
-        di = torch.zeros(M_cap, I, dtype=torch.uint8, device=A.device)
-    if di_scale is None:
-        di_scale = new_scale(M_cap, I // 128, scale_layout, A.device)
+    if di is None or di_scale is None:
+        with torch.cuda.stream(stream):
+            if di is None:
+                di = torch.zeros(M_cap, I, dtype=torch.uint8, device=A.device)
+            if di_scale is None:
+                di_scale = new_scale(M_cap, I // 128, scale_layout, A.device)
     rc = load().moe_grouped_gemm_act_quant(_ptr(A), _ptr(A_scale), scale_layout, A_scale.shape[1],
                                            _ptr(lay.start), _ptr(lay.tile_prefix), _ptr(lay.total),
                                            _ptr(W13), _ptr(W13_scale), _ptr(row_w), flags, E, I, H, M_cap,
@@ -236,14 +248,16 @@ def grouped_ffn(xe, xe_scale, scale_layout: int, lay: Layout, w13, s13, w2, s2, 
     E, twoI, _ = w13.shape
     I = twoI // 2
     dev = xe.device
-    if gateup is None:
-        gateup = torch.zeros(M_cap, twoI, dtype=torch.bfloat16, device=dev)
-    if down_in is None:
-        down_in = torch.zeros(M_cap, I, dtype=torch.uint8, device=dev)
-    if down_in_scale is None:
-        down_in_scale = new_scale(M_cap, I // 128, scale_layout, dev)
-    if down_out is None:
-        down_out = torch.zeros(M_cap, H, dtype=torch.bfloat16, device=dev)
+    if gateup is None or down_in is None or down_in_scale is None or down_out is None:
+        with torch.cuda.stream(stream):
+            if gateup is None:
+                gateup = torch.zeros(M_cap, twoI, dtype=torch.bfloat16, device=dev)
+            if down_in is None:
+                down_in = torch.zeros(M_cap, I, dtype=torch.uint8, device=dev)
+            if down_in_scale is None:
+                down_in_scale = new_scale(M_cap, I // 128, scale_layout, dev)
+            if down_out is None:
+                down_out = torch.zeros(M_cap, H, dtype=torch.bfloat16, device=dev)
     rc = load().moe_grouped_ffn(_ptr(xe), _ptr(xe_scale), xe_scale.shape[1], scale_layout,
                                 _ptr(lay.start), _ptr(lay.tile_prefix), _ptr(lay.total),
                                 _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(row_w), flags,

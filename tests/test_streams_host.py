@@ -6,6 +6,7 @@ import contextlib
 import pytest
 import torch
 
+import expanded_layout_expert_gb300 as mx
 from expanded_layout_expert_gb300 import Layout, training
 
 
@@ -39,6 +40,9 @@ def made(monkeypatch):
     monkeypatch.setattr(training, "_rows", lambda t, *a: (0, t.shape[1]))
     for name in ("_whole", "_word", "_stream", "_device"):
         monkeypatch.setattr(training, name, lambda *a: 0, raising=False)
+    monkeypatch.setattr(mx, "load", Library)
+    monkeypatch.setattr(mx, "_stream", lambda *a: 0)
+    monkeypatch.setattr(mx, "workspace_size", lambda *a: 16)
     return seen
 
 
@@ -63,6 +67,26 @@ CALLS = {
     "swiglu": lambda s: training.swiglu(bf16(8, 32), layout(), stream=s),
     "swiglu_backward": lambda s: training.swiglu_backward(bf16(8, 16), bf16(8, 32), layout(), stream=s),
 }
+
+
+def u8(*s):
+    return torch.ones(*s).to(torch.uint8)
+
+
+IDS, SCALE = torch.ones(4, 2, dtype=torch.int32), torch.ones(4, 1)
+CALLS.update({
+    "expand_layout": lambda s: mx.expand_layout(IDS, 2, 1, 8, stream=s),
+    "expand_scatter": lambda s: mx.expand_scatter(u8(4, 128), SCALE, 0, torch.ones(4, 2), layout(), stream=s),
+    "expand_layout_scatter": lambda s: mx.expand_layout_scatter(u8(4, 128), SCALE, 0, IDS, torch.ones(4, 2), 2, 1,
+                                                                8, stream=s),
+    "grouped_gemm": lambda s: mx.grouped_gemm(u8(8, 128), torch.ones(8, 1), 0, layout(), u8(2, 128, 128), SCALE,
+                                              stream=s),
+    "act_quant": lambda s: mx.act_quant(bf16(8, 256), None, 0, 1, torch.ones(1), stream=s),
+    "grouped_gemm_act_quant": lambda s: mx.grouped_gemm_act_quant(u8(8, 128), torch.ones(8, 1), 0, layout(),
+                                                                  u8(2, 256, 128), SCALE, stream=s),
+    "grouped_ffn": lambda s: mx.grouped_ffn(u8(8, 128), torch.ones(8, 1), 0, layout(), u8(2, 256, 128), SCALE,
+                                            u8(2, 128, 128), SCALE, torch.ones(8), 0, stream=s),
+})
 
 
 @pytest.mark.parametrize("name", CALLS)
