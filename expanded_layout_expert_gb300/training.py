@@ -3,10 +3,11 @@ training calls of include/moe_expand.h, and the layer that strings them
 together.
 
 Each function marshals torch tensors and the current CUDA stream into one C
-call, as the package's other functions do. Row tensors may have a row stride
-larger than the row (a multiple of 8 values); rows outside the segments
-[start[e], psum[e]) of the layout are neither used nor written. A result that a
-call makes itself is made on the stream the call is queued on.
+call, as the package's other functions do. All tensors of a call, and a stream
+given to it, are on the current GPU; others are refused. Row tensors may have a
+row stride larger than the row (a multiple of 8 values); rows outside the
+segments [start[e], psum[e]) of the layout are neither used nor written. A
+result that a call makes itself is made on the stream the call is queued on.
 """
 from __future__ import annotations
 
@@ -24,12 +25,31 @@ TYPE_CODE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MO
 STATE_BLOCK = 128   # values that share a scale in an 8-bit AdamW state
 
 
-def _stream(stream, device_of: torch.Tensor):
-    """The given stream's handle, or that of the current stream of the
-    tensor's device (without building a stream object for it)."""
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """Index of the GPU a call runs on: that of its first tensor, which must be
+    the current one, because the library launches there. The call's other
+    tensors and its stream are held against it."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on the GPU")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on GPU {dev}, but the current one is {_current_device()}: enter its "
+                         "device first")
+    return dev
+
+
+def _stream(stream, dev: int):
+    """The given stream's handle, or that of the device's current stream
+    (without building a stream object for it)."""
     if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError(f"the stream is on GPU {stream.device_index}, the tensors on {dev}")
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device_of.get_device())
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _new(make, shape: tuple, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -50,7 +70,7 @@ def _code16(t: torch.Tensor, name: str) -> int:
     raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
 
 
-def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype) -> tuple:
+def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype, dev: int) -> tuple:
     """(pointer, row stride) of a [rows, width] tensor with contiguous rows."""
     if t.shape != (rows, width):
         raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
@@ -61,33 +81,33 @@ def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype) -> tuple:
         ld = width   # one row has no stride to speak of
     if (one != 1 and width > 1) or ld < width:
         raise ValueError(f"{name} must have contiguous, non-overlapping rows")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev}")
     return t.data_ptr(), ld
 
 
-def _whole(t: Optional[torch.Tensor], name: str, shape: tuple, dtype):
+def _whole(t: Optional[torch.Tensor], name: str, shape: tuple, dtype, dev: int):
     """Pointer of a contiguous tensor of the given shape and type (None: NULL)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous {dtype} GPU tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _word(t: Optional[torch.Tensor], name: str):
+def _word(t: Optional[torch.Tensor], name: str, dev: int):
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.numel() < 1 or not t.is_cuda:
-        raise ValueError(f"{name} must be an int32 GPU tensor of one element")
+    if t.dtype is not torch.int32 or t.numel() < 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be an int32 tensor of one element on GPU {dev}")
     return t.data_ptr()
 
 
-def _segments(lay) -> tuple:
+def _segments(lay, dev: int) -> tuple:
     E = lay.E
-    return _whole(lay.start, "lay.start", (E,), torch.int32), \
-        _whole(lay.psum, "lay.psum", (E,), torch.int32), E
+    return _whole(lay.start, "lay.start", (E,), torch.int32, dev), \
+        _whole(lay.psum, "lay.psum", (E,), torch.int32, dev), E
 
 
 def _most_rows(lay, M: int) -> int:
@@ -107,21 +127,22 @@ def expand_rows(x: torch.Tensor, lay, topk_w: Optional[torch.Tensor] = None,
     T, H = x.shape
     K = lay.src2dst.shape[1]
     _code16(x, "x")
+    dev = _device(x, "x")
     if out is None:
         out = _new(torch.zeros, (lay.M_cap, H), x.dtype, x, stream)
     if topk_w is not None and row_w is None:
         row_w = _new(torch.zeros, (lay.M_cap,), torch.float32, x, stream)
     if topk_w is None and row_w is not None:
         raise ValueError("row_w needs topk_w")
-    xp, ld_x = _rows(x, "x", T, H, x.dtype)
-    op, ld_o = _rows(out, "out", lay.M_cap, H, x.dtype)
+    xp, ld_x = _rows(x, "x", T, H, x.dtype, dev)
+    op, ld_o = _rows(out, "out", lay.M_cap, H, x.dtype, dev)
     rc = load().moe_expand_rows(
-        xp, ld_x, _whole(topk_w, "topk_w", (T, K), torch.float32),
-        _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32),
-        _whole(lay.psum, "lay.psum", (lay.E,), torch.int32), _word(n_valid, "n_valid"), T, H, K,
-        lay.E, lay.align, lay.M_cap, op, ld_o,
-        _whole(row_w, "row_w", (lay.M_cap,), torch.float32), _word(status, "status"),
-        _stream(stream, x))
+        xp, ld_x, _whole(topk_w, "topk_w", (T, K), torch.float32, dev),
+        _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32, dev),
+        _whole(lay.psum, "lay.psum", (lay.E,), torch.int32, dev), _word(n_valid, "n_valid", dev), T, H,
+        K, lay.E, lay.align, lay.M_cap, op, ld_o,
+        _whole(row_w, "row_w", (lay.M_cap,), torch.float32, dev), _word(status, "status", dev),
+        _stream(stream, dev))
     check(rc, "moe_expand_rows")
     return out if topk_w is None else (out, row_w)
 
@@ -131,12 +152,13 @@ def collect_row_grads(rows: torch.Tensor, lay, n_valid: Optional[torch.Tensor] =
     """Per-row values back to their pairs: out[t, k] = rows[src2dst[t, k]], 0
     where there is no pair (the gradient of the top-k weights)."""
     T, K = lay.src2dst.shape
+    dev = _device(rows, "rows")
     if out is None:
         out = _new(torch.zeros, (T, K), torch.float32, rows, stream)
     rc = load().moe_collect_row_grads(
-        _whole(rows, "rows", (lay.M_cap,), torch.float32),
-        _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32), _word(n_valid, "n_valid"), T, K,
-        lay.M_cap, _whole(out, "out", (T, K), torch.float32), _stream(stream, rows))
+        _whole(rows, "rows", (lay.M_cap,), torch.float32, dev),
+        _whole(lay.src2dst, "lay.src2dst", (T, K), torch.int32, dev), _word(n_valid, "n_valid", dev), T, K,
+        lay.M_cap, _whole(out, "out", (T, K), torch.float32, dev), _stream(stream, dev))
     check(rc, "moe_collect_row_grads")
     return out
 
@@ -145,17 +167,17 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, lay, out: Optional[torch.Te
                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[r] = x[r] @ w[e].T for the rows r of expert e; x [M, Kd], w
     [E, N, Kd], out [M, N], all bfloat16 or all float16."""
-    dt = _code16(x, "x")
-    start, psum, E = _segments(lay)
+    dt, dev = _code16(x, "x"), _device(x, "x")
+    start, psum, E = _segments(lay, dev)
     M, Kd = x.shape
     N = w.shape[1]
     if out is None:
         out = _new(torch.zeros, (M, N), x.dtype, x, stream)
-    xp, ld_x = _rows(x, "x", M, Kd, x.dtype)
-    op, ld_o = _rows(out, "out", M, N, x.dtype)
-    rc = load().moe_grouped_mm(xp, ld_x, _whole(w, "w", (E, N, Kd), x.dtype), start, psum, dt, E, N,
-                               Kd, M, _most_rows(lay, M), op, ld_o, _word(status, "status"),
-                               _stream(stream, x))
+    xp, ld_x = _rows(x, "x", M, Kd, x.dtype, dev)
+    op, ld_o = _rows(out, "out", M, N, x.dtype, dev)
+    rc = load().moe_grouped_mm(xp, ld_x, _whole(w, "w", (E, N, Kd), x.dtype, dev), start, psum, dt, E, N,
+                               Kd, M, _most_rows(lay, M), op, ld_o, _word(status, "status", dev),
+                               _stream(stream, dev))
     check(rc, "moe_grouped_mm")
     return out
 
@@ -164,17 +186,17 @@ def grouped_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, lay, out: Optional[t
                          status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient of grouped_matmul's x: out[r] = dy[r] @ w[e]; dy [M, N],
     out [M, Kd]."""
-    dt = _code16(dy, "dy")
-    start, psum, E = _segments(lay)
+    dt, dev = _code16(dy, "dy"), _device(dy, "dy")
+    start, psum, E = _segments(lay, dev)
     M, N = dy.shape
     Kd = w.shape[2]
     if out is None:
         out = _new(torch.zeros, (M, Kd), dy.dtype, dy, stream)
-    dp, ld_d = _rows(dy, "dy", M, N, dy.dtype)
-    op, ld_o = _rows(out, "out", M, Kd, dy.dtype)
-    rc = load().moe_grouped_mm_dgrad(dp, ld_d, _whole(w, "w", (E, N, Kd), dy.dtype), start, psum, dt,
+    dp, ld_d = _rows(dy, "dy", M, N, dy.dtype, dev)
+    op, ld_o = _rows(out, "out", M, Kd, dy.dtype, dev)
+    rc = load().moe_grouped_mm_dgrad(dp, ld_d, _whole(w, "w", (E, N, Kd), dy.dtype, dev), start, psum, dt,
                                      E, N, Kd, M, _most_rows(lay, M), op, ld_o,
-                                     _word(status, "status"), _stream(stream, dy))
+                                     _word(status, "status", dev), _stream(stream, dev))
     check(rc, "moe_grouped_mm_dgrad")
     return out
 
@@ -185,8 +207,8 @@ def grouped_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, lay, out: Optional[t
     """The gradient of grouped_matmul's w: out[e] = dy[rows of e].T @ x[rows of
     e], in the operands' type or float32 (``out_dtype``); ``accumulate`` adds
     it to what ``out`` holds, rounded once."""
-    dt = _code16(dy, "dy")
-    start, psum, E = _segments(lay)
+    dt, dev = _code16(dy, "dy"), _device(dy, "dy")
+    start, psum, E = _segments(lay, dev)
     M, N = dy.shape
     Kd = x.shape[1]
     if out is None:
@@ -197,11 +219,11 @@ def grouped_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, lay, out: Optional[t
         raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
     if out.dtype is not dy.dtype and out.dtype is not torch.float32:
         raise ValueError(f"out must be {dy.dtype} or float32, got {out.dtype}")
-    dp, ld_d = _rows(dy, "dy", M, N, dy.dtype)
-    xp, ld_x = _rows(x, "x", M, Kd, dy.dtype)
+    dp, ld_d = _rows(dy, "dy", M, N, dy.dtype, dev)
+    xp, ld_x = _rows(x, "x", M, Kd, dy.dtype, dev)
     rc = load().moe_grouped_mm_wgrad(dp, ld_d, xp, ld_x, start, psum, dt, E, N, Kd, M,
-                                     _whole(out, "out", (E, N, Kd), out.dtype), TYPE_CODE[out.dtype],
-                                     int(accumulate), _word(status, "status"), _stream(stream, dy))
+                                     _whole(out, "out", (E, N, Kd), out.dtype, dev), TYPE_CODE[out.dtype],
+                                     int(accumulate), _word(status, "status", dev), _stream(stream, dev))
     check(rc, "moe_grouped_mm_wgrad")
     return out
 
@@ -210,16 +232,16 @@ def swiglu(gu: torch.Tensor, lay, row_w: Optional[torch.Tensor] = None,
            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[r] = silu(g) * u * row_w[r] for the rows r < total of gu = [g | u]
     (row_w None: 1)."""
-    dt = _code16(gu, "gu")
+    dt, dev = _code16(gu, "gu"), _device(gu, "gu")
     M, two = gu.shape
     if two % 2:
         raise ValueError("gu must have an even number of columns")
     if out is None:
         out = _new(torch.zeros, (M, two // 2), gu.dtype, gu, stream)
-    gp, ld_g = _rows(gu, "gu", M, two, gu.dtype)
-    op, ld_o = _rows(out, "out", M, two // 2, gu.dtype)
-    rc = load().moe_swiglu(gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32),
-                           _word(lay.total, "lay.total"), M, op, ld_o, _stream(stream, gu))
+    gp, ld_g = _rows(gu, "gu", M, two, gu.dtype, dev)
+    op, ld_o = _rows(out, "out", M, two // 2, gu.dtype, dev)
+    rc = load().moe_swiglu(gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32, dev),
+                           _word(lay.total, "lay.total", dev), M, op, ld_o, _stream(stream, dev))
     check(rc, "moe_swiglu")
     return out
 
@@ -229,7 +251,7 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, lay, row_w: Optional[tor
                     stream=None):
     """(dgu, drow_w): the gradients of swiglu's gu and row_w. ``dgu`` may be
     ``gu`` itself, which is then overwritten."""
-    dt = _code16(gu, "gu")
+    dt, dev = _code16(gu, "gu"), _device(gu, "gu")
     M, two = gu.shape
     if two % 2:
         raise ValueError("gu must have an even number of columns")
@@ -237,13 +259,13 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, lay, row_w: Optional[tor
         dgu = _new(torch.zeros, (M, two), gu.dtype, gu, stream)
     if drow_w is None:
         drow_w = _new(torch.zeros, (M,), torch.float32, gu, stream)
-    gp, ld_g = _rows(gu, "gu", M, two, gu.dtype)
-    hp, ld_h = _rows(dh, "dh", M, two // 2, gu.dtype)
-    op, ld_o = _rows(dgu, "dgu", M, two, gu.dtype)
+    gp, ld_g = _rows(gu, "gu", M, two, gu.dtype, dev)
+    hp, ld_h = _rows(dh, "dh", M, two // 2, gu.dtype, dev)
+    op, ld_o = _rows(dgu, "dgu", M, two, gu.dtype, dev)
     rc = load().moe_swiglu_backward(
-        hp, ld_h, gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32),
-        _word(lay.total, "lay.total"), M, op, ld_o, _whole(drow_w, "drow_w", (M,), torch.float32),
-        _stream(stream, gu))
+        hp, ld_h, gp, ld_g, dt, two // 2, _whole(row_w, "row_w", (M,), torch.float32, dev),
+        _word(lay.total, "lay.total", dev), M, op, ld_o, _whole(drow_w, "drow_w", (M,), torch.float32, dev),
+        _stream(stream, dev))
     check(rc, "moe_swiglu_backward")
     return dgu, drow_w
 
@@ -259,7 +281,8 @@ class AdamW:
     """AdamW (decoupled weight decay) over a list of tensors, one launch per
     step and 400 tensors.
 
-    params   contiguous float32, bfloat16 or float16 tensors, updated in place
+    params   contiguous float32, bfloat16 or float16 tensors on one GPU, updated
+             in place
     copies   optional tensors of the same sizes that get the new parameters in
              their own type (the 16-bit weights the products read, beside
              float32 parameters); an entry may be None
@@ -313,6 +336,10 @@ class AdamW:
         for i, p in enumerate(self.params):
             if p.dtype not in TYPE_CODE or not p.is_contiguous() or not p.is_cuda:
                 raise ValueError(f"params[{i}] must be a contiguous float32, bfloat16 or float16 GPU tensor")
+            if p.get_device() != self.params[0].get_device():
+                raise ValueError(f"params[{i}] is on GPU {p.get_device()}, params[0] on "
+                                 f"{self.params[0].get_device()}: an optimizer for each GPU, since a step is "
+                                 "one launch")
             c = self.copies[i]
             if c is not None and (c.dtype not in TYPE_CODE or c.numel() != p.numel()
                                   or not c.is_contiguous() or c.device != p.device):
@@ -360,6 +387,7 @@ class AdamW:
         if not self.params:
             self.steps += 1
             return
+        dev = _device(self.params[0], "params[0]")
         # Every gradient is checked at every step; parameters and copies are
         # looked up anew, and checked when they have been given other storage.
         table, sizes, T = self._table, self._sizes, torch.Tensor
@@ -374,13 +402,13 @@ class AdamW:
         table["g"] = list(map(T.data_ptr, grads))
         table["g_type"] = TYPE_CODE[types[0]] if len(set(types)) == 1 else [TYPE_CODE[t] for t in types]
         if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1
-                                       or not grad_scale.is_cuda):
-            raise ValueError("grad_scale must be a float32 GPU tensor of one element")
+                                       or grad_scale.get_device() != dev):
+            raise ValueError(f"grad_scale must be a float32 tensor of one element on GPU {dev}")
         rc = load().moe_adamw_step(table.ctypes.data, len(self.params), self.state_bits,
                                    self.lr if lr is None else lr, self.betas[0], self.betas[1],
                                    self.eps, self.weight_decay, self.steps + 1,
                                    None if grad_scale is None else grad_scale.data_ptr(),
-                                   _stream(stream, self.params[0]))
+                                   _stream(stream, dev))
         check(rc, "moe_adamw_step")
         self.steps += 1
 
@@ -409,6 +437,8 @@ class TrainableExperts:
         for name, w in (("w13", w13), ("w2", w2)):
             if w.dtype is not torch.bfloat16 or not w.is_contiguous() or not w.is_cuda:
                 raise ValueError(f"{name} must be a contiguous bfloat16 GPU tensor")
+        if w2.get_device() != w13.get_device():
+            raise ValueError("w13 and w2 must be on the same GPU")
         self.w13, self.w2 = w13, w2
         self.E, self.H, self.I, self.K, self.align, self.T = E, H, twoI // 2, K, align, max_tokens
         dev = w13.device
@@ -438,8 +468,9 @@ class TrainableExperts:
 
     def forward(self, x, topk_ids, topk_w, n_valid=None, stream=None) -> torch.Tensor:
         from . import combine, expand_layout
-        _rows(x, "x", self.T, self.H, torch.bfloat16)
-        _whole(topk_ids, "topk_ids", (self.T, self.K), torch.int32)
+        dev = _device(self.w13, "w13")
+        _rows(x, "x", self.T, self.H, torch.bfloat16, dev)
+        _whole(topk_ids, "topk_ids", (self.T, self.K), torch.int32, dev)
         lay = self.lay
         expand_layout(topk_ids, self.E, self.align, self.M_cap, n_valid, self.ws, self.status, lay,
                       stream)
