@@ -339,6 +339,17 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int st
                 "moe_adamw_step: tensor %d: pointer not aligned to its type", i);
   }
   MOE_REQUIRE_DEVICE();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // lr and the step's bias corrections are values of the launch, so a graph
+  // would apply this one step's again at every replay
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+    const int rc = moe::check_launch("cudaStreamIsCapturing");
+    return rc != MOE_OK ? rc : MOE_ERR_CUDA;
+  }
+  MOE_REQUIRE(capture == cudaStreamCaptureStatusNone,
+              "moe_adamw_step: the stream is capturing a graph, whose replays would repeat this step's "
+              "bias correction and lr");
   const double t = static_cast<double>(step);
   moe::Hyper h;
   h.b1 = static_cast<float>(beta1);
@@ -350,7 +361,6 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int st
   h.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
   h.eps = static_cast<float>(eps);
   h.scale = d_grad_scale;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   moe::Table<moe::kMaxTensors> tab;
   int64_t chunks = 0;
   tab.count = 0;

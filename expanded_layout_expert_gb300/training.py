@@ -296,7 +296,9 @@ class AdamW:
 
     step(grads) takes one float32, bfloat16 or float16 gradient per parameter,
     and optionally ``grad_scale``, a float32 device word they are multiplied
-    by (a clipping factor, say) without a host read.
+    by (a clipping factor, say) without a host read. A step is one of its own
+    (its number and lr go with the launch), so it cannot be captured into a CUDA
+    graph: capture the forward and backward, and step between the replays.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], *, lr: float = 1e-3, betas=(0.9, 0.999),

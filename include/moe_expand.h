@@ -460,7 +460,9 @@ typedef struct {
  * positive sqrt(v) never becomes zero, a block below 1e-30 becomes zeros. A
  * gradient that is not finite spoils its value, and with 8-bit states what
  * shares its block of 128 after this step.
- * step counts from 1.
+ * step counts from 1. step and lr are values of the launch, so a stream that
+ * is capturing a graph is refused (MOE_ERR_INVALID_ARG): its replays would
+ * repeat this step's bias correction.
  */
 int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int state_bits, double lr,
                    double beta1, double beta2, double eps, double weight_decay, int64_t step,

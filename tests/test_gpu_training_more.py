@@ -63,3 +63,57 @@ def test_results_are_made_on_the_calls_stream(mx):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(early, want))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_is_not_captured(mx, bits):
+    """A graph would repeat one step's bias correction: the capture is refused,
+    and the optimizer is as it was."""
+    p, g = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    q = p.clone()
+    a, b = (mx.AdamW([t], state_bits=bits) for t in (p, q))
+    a.step([g])
+    b.step([g])
+    torch.cuda.synchronize()
+    with pytest.raises(mx.MoEError, match="captur"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            a.step([g])
+    torch.cuda.synchronize()
+    assert a.steps == 1 and torch.equal(p, q)
+    a.step([g])
+    b.step([g])
+    assert a.steps == 2 and torch.equal(p, q)
+
+
+def test_training_loop_around_a_graph(mx):
+    """Forward and backward replayed from a graph, the optimizer's step between
+    the replays, against the same loop without a graph."""
+    T, K, E, H, I = 48, 2, 4, 128, 64
+
+    def loop(graphed):
+        g = gen(3)
+        masters = [normal(g, E, 2 * I, H, std=0.1), normal(g, E, H, I, std=0.1)]
+        layer = mx.TrainableExperts(*(t.bfloat16() for t in masters), K=K, max_tokens=T)
+        opt = mx.AdamW(masters, copies=layer.parameters, lr=1e-2)
+        x, dy = normal(g, T, H, dtype=BF16), normal(g, T, H, dtype=BF16)
+        w, ids = torch.rand(T, E, generator=g, device="cuda").topk(K, dim=1)
+        ids, w = ids.to(torch.int32).contiguous(), w.contiguous()
+        layer.forward(x, ids, w)
+        layer.backward(dy)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        if graphed:
+            with torch.cuda.graph(graph):
+                layer.forward(x, ids, w)
+                layer.backward(dy)
+        for _ in range(4):
+            if graphed:
+                graph.replay()
+            else:
+                layer.forward(x, ids, w)
+                layer.backward(dy)
+            opt.step(layer.gradients)
+        torch.cuda.synchronize()
+        return masters + layer.parameters
+
+    assert all(torch.equal(a, b) for a, b in zip(loop(True), loop(False)))
