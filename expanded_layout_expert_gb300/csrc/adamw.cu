@@ -6,7 +6,7 @@
 // Every operation is rounded on its own (no contraction into fused
 // multiply-adds), so a step gives the same bits as the formula written with
 // elementwise fp32 tensor operations, whatever the tensors' split over
-// launches, blocks or lanes.
+// launches, blocks or lanes (8-bit codes: to nearest or at random, see below).
 //
 // 8-bit states: m and r = sqrt(v), not v, are stored as e4m3 codes with an
 // fp32 scale per 128 values (amax / 448). r has half of v's range in powers
@@ -16,6 +16,21 @@
 // by eps alone. A block whose largest value is below 1e-30 is stored as
 // zeros (its scale's inverse would overflow). The step itself uses the new m
 // and v before they are rounded.
+//
+// How codes are rounded. A step moves r by about 0.7 w of itself, w = (1 - b2) /
+// (1 - b2^t) being the newest gradient's share of the average, and where the
+// gradients get small by w / 2; a code's half step is 3 to 6 %. Where w is small,
+// rounding to nearest puts nearly every code back where it was, and r stays at
+// its old size for ever: with b2 = 0.98 to 0.999 and gradients that fall to 1 %
+// in half of every block, r was 6 to 130 times too large after 4000 steps. So
+// below w = 1/24 the codes of m and r are rounded up or down at random, with the
+// chances that make the mean exact: r then follows its average within some 20 %
+// (a step's variance, w times a code's step of 9 %, against a memory of 1 / w steps)
+// whatever b2, and a value without gradients stops moving. From 1/24 on (every step
+// with b2 <= 0.95, the first 24 with any b2) the average moves by code steps, and
+// rounding to nearest has the smaller error (r within 20 % at the 99th percentile,
+// 31 % at random, b2 = 0.95) and takes 420 instead of 480 us (134 M values). The bits come from the step's number and the value's
+// place (tensor in the list, index), so a step gives the same codes every time.
 //
 // Bytes a value: 8 (p) + 2|4 (g) + 16 (fp32 m, v) or 4 + 16/128 (8 bits) + 2
 // (copy): bound by HBM with 32-bit states (577 us for 134 M values, fp32
@@ -72,6 +87,8 @@ struct Hyper {
   float root;             // 1 / sqrt(1 - b2^t)
   float eps;
   const float* scale;
+  uint32_t step;          // random rounding: what its bits come from, besides a value's place
+  uint32_t first;         // non-empty tensors of earlier launches
 };
 
 MOE_DEV float load16(uint16_t b, int type) {
@@ -157,10 +174,37 @@ MOE_DEV uint32_t load_codes(const void* a, int64_t i, int64_t n, bool vec) {
   return c;
 }
 
-// The block's values as codes (Floor: a positive value never becomes zero),
-// given the block's largest magnitude; returns the block's scale.
-template <bool Floor>
-MOE_DEV float store_codes(void* a, int64_t i, int64_t n, bool vec, const float (&f)[4], float amax) {
+// 64 bits from a counter (x, y) and a key, seven rounds of the 2x32 multiply
+// and exclusive-or generator of Salmon, Moraes, Dror and Shaw (2011).
+MOE_DEV uint2 random_bits(uint32_t x, uint32_t y, uint32_t key) {
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const uint64_t w = static_cast<uint64_t>(x) * 0xD256D193u;
+    x = static_cast<uint32_t>(w >> 32) ^ key ^ y;
+    y = static_cast<uint32_t>(w);
+    key += 0x9E3779B9u;
+  }
+  return make_uint2(x, y);
+}
+
+// q rounded to one of its two neighbours among the codes' values, up where the
+// 20 random bits exceed what is missing: added to the 20 bits of fp32's mantissa
+// that a code does not have, they carry with that chance. Codes below 2^-6 are 2^-9
+// apart, as those of [2^-6, 2^-5) are, so these are rounded there. From 448 on (and
+// NaN) the conversion saturates.
+MOE_DEV float round_random(float q, uint32_t bits) {
+  const float a = fabsf(q);
+  const float off = a < 0x1p-6f ? 0x1p-6f : 0.0f;
+  const uint32_t up = (__float_as_uint(__fadd_rn(a, off)) + bits) & 0xFFF00000u;
+  return a < 448.0f ? copysignf(__fsub_rn(__uint_as_float(up), off), q) : q;
+}
+
+// The block's values as codes (Floor: a positive value never becomes zero;
+// Random: rounded at random with `bits`, else to nearest), given the block's
+// largest magnitude; returns the block's scale.
+template <bool Floor, bool Random>
+MOE_DEV float store_codes(void* a, int64_t i, int64_t n, bool vec, const float (&f)[4], float amax,
+                          uint2 bits) {
   const bool live = amax >= kTinyAmax;
   const float inv = live ? __fmul_rn(__frcp_rn(amax), 448.0f) : 0.0f;
   const float least = live ? 0x1p-9f : 0.0f;   // the smallest positive code
@@ -168,6 +212,10 @@ MOE_DEV float store_codes(void* a, int64_t i, int64_t n, bool vec, const float (
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     q[j] = __fmul_rn(f[j], inv);
+    if (Random) {
+      const uint32_t w = j < 2 ? bits.x : bits.y;   // a value's high bits are nobody else's
+      q[j] = round_random(q[j], j % 2 ? w >> 12 : w & 0xFFFFFu);
+    }
     if (Floor && f[j] > 0.0f && q[j] < least) q[j] = least;
   }
   const uint32_t c = encode4(q);
@@ -186,7 +234,7 @@ MOE_DEV float largest4(const float (&f)[4]) {
   return fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
 }
 
-template <int Bits, int Max>
+template <int Bits, bool Random, int Max>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __grid_constant__ Table<Max> tab,
                                                          const Hyper h) {
   const int chunk = blockIdx.x;
@@ -263,8 +311,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
       // The block's largest |m| and r: fp32 magnitudes compare as integers do.
       const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(largest4(m)));
       const uint32_t ar = __reduce_max_sync(0xffffffffu, __float_as_uint(largest4(r)));
-      const float ms = store_codes<false>(t.m, i, n, vec, m, __uint_as_float(am));
-      const float vs = store_codes<true>(t.v, i, n, vec, r, __uint_as_float(ar));
+      // m and r share their bits: rounded the same way, their quotient moves least
+      uint2 bits = make_uint2(0, 0);
+      if (Random) {
+        const uint64_t at = static_cast<uint64_t>(i) >> 2;
+        bits = random_bits(static_cast<uint32_t>(at),
+                           (h.first + lo) ^ (static_cast<uint32_t>(at >> 32) << 24), h.step);
+      }
+      const float ms = store_codes<false, Random>(t.m, i, n, vec, m, __uint_as_float(am), bits);
+      const float vs = store_codes<true, Random>(t.v, i, n, vec, r, __uint_as_float(ar), bits);
       if (lane == 0) {
         t.ms[b / kBlock] = ms;
         t.vs[b / kBlock] = vs;
@@ -287,25 +342,29 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
 constexpr int kMaxTensors = 400;
 constexpr int kFewTensors = 16;
 
-template <int Bits, int Max>
+template <int Bits, bool Random, int Max>
 int launch(const Table<kMaxTensors>& all, int chunks, const Hyper& h, cudaStream_t s) {
   if constexpr (Max == kMaxTensors) {
-    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(all, h);
+    adamw_kernel<Bits, Random, Max><<<chunks, kThreads, 0, s>>>(all, h);
   } else {
     Table<Max> few;
     for (int i = 0; i < all.count; ++i) few.t[i] = all.t[i];
     few.count = all.count;
-    adamw_kernel<Bits, Max><<<chunks, kThreads, 0, s>>>(few, h);
+    adamw_kernel<Bits, Random, Max><<<chunks, kThreads, 0, s>>>(few, h);
   }
   return check_launch("adamw_kernel");
 }
 
-int launch_all(const Table<kMaxTensors>& tab, int bits, int chunks, const Hyper& h, cudaStream_t s) {
-  if (bits == 32)
-    return tab.count <= kFewTensors ? launch<32, kFewTensors>(tab, chunks, h, s)
-                                    : launch<32, kMaxTensors>(tab, chunks, h, s);
-  return tab.count <= kFewTensors ? launch<8, kFewTensors>(tab, chunks, h, s)
-                                  : launch<8, kMaxTensors>(tab, chunks, h, s);
+template <int Bits, bool Random>
+int launch_of(const Table<kMaxTensors>& tab, int chunks, const Hyper& h, cudaStream_t s) {
+  return tab.count <= kFewTensors ? launch<Bits, Random, kFewTensors>(tab, chunks, h, s)
+                                  : launch<Bits, Random, kMaxTensors>(tab, chunks, h, s);
+}
+
+int launch_all(const Table<kMaxTensors>& tab, int bits, bool random, int chunks, const Hyper& h,
+               cudaStream_t s) {
+  if (bits == 32) return launch_of<32, false>(tab, chunks, h, s);
+  return random ? launch_of<8, true>(tab, chunks, h, s) : launch_of<8, false>(tab, chunks, h, s);
 }
 
 }  // namespace
@@ -361,6 +420,10 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int st
   h.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
   h.eps = static_cast<float>(eps);
   h.scale = d_grad_scale;
+  h.step = static_cast<uint32_t>(step);
+  h.first = 0;
+  const double newest = (1.0 - beta2) / (1.0 - std::pow(beta2, t));   // its share of the average
+  const bool random = newest < 1.0 / 24.0;
   moe::Table<moe::kMaxTensors> tab;
   int64_t chunks = 0;
   tab.count = 0;
@@ -370,8 +433,9 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int st
     if (a.n == 0) continue;
     const int64_t mine = (a.n + moe::kChunk - 1) / moe::kChunk;
     if (tab.count == moe::kMaxTensors || chunks + mine > INT32_MAX) {
-      const int rc = moe::launch_all(tab, state_bits, static_cast<int>(chunks), h, s);
+      const int rc = moe::launch_all(tab, state_bits, random, static_cast<int>(chunks), h, s);
       if (rc != MOE_OK) return rc;
+      h.first += static_cast<uint32_t>(tab.count);
       tab.count = 0;
       chunks = 0;
     }
@@ -394,5 +458,5 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int st
             moe::aligned(a.copy, a.copy_type == MOE_F32 ? 16 : 8) &&
             moe::aligned(a.m, eight ? 4 : 16) && moe::aligned(a.v, eight ? 4 : 16);
   }
-  return tab.count > 0 ? moe::launch_all(tab, state_bits, static_cast<int>(chunks), h, s) : MOE_OK;
+  return tab.count > 0 ? moe::launch_all(tab, state_bits, random, static_cast<int>(chunks), h, s) : MOE_OK;
 }

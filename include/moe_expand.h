@@ -457,7 +457,11 @@ typedef struct {
  * in fp32; p is rounded to its type, copy is rounded from the fp32 result.
  * state_bits 32: m and v in fp32. 8: m and sqrt(v) as e4m3 codes with a scale
  * amax/448 per 128 values; the step uses them before they are rounded, a
- * positive sqrt(v) never becomes zero, a block below 1e-30 becomes zeros. A
+ * positive sqrt(v) never becomes zero, a block below 1e-30 becomes zeros. Codes
+ * are rounded to nearest while the newest gradient's share of v's average,
+ * (1-b2)/(1-b2^step), is at least 1/24, then at random with an exact mean
+ * (nearest would hold sqrt(v) where it is), from bits that depend on step, the
+ * tensor's place among the non-empty ones and the index alone. A
  * gradient that is not finite spoils its value, and with 8-bit states what
  * shares its block of 128 after this step.
  * step counts from 1. step and lr are values of the launch, so a stream that

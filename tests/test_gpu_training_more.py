@@ -117,3 +117,103 @@ def test_training_loop_around_a_graph(mx):
         return masters + layer.parameters
 
     assert all(torch.equal(a, b) for a, b in zip(loop(True), loop(False)))
+
+
+# ------------------------------------------- AdamW with 8-bit states, long runs
+def decoded(codes, scales):
+    return codes.view(torch.float8_e4m3fn).float() * scales.repeat_interleave(128)[: codes.numel()]
+
+
+@pytest.mark.parametrize("b2,small,steps", [(0.97, 0.01, 2000), (0.98, 0.01, 2000), (0.99, 0.01, 3000),
+                                            (0.999, 0.3, 4000)])
+def test_adamw_8_bit_states_follow_their_gradients(mx, b2, small, steps):
+    """Half of every block's gradients fall to a fraction; the stored root
+    against that of 32-bit states over the same gradients.
+
+    A step's rounding moves a root by about its own change and its block's
+    scale's, (1 - b2) together, times the step of a code (6-12 %, 9 on average)
+    in variance, and the average forgets at 1 - b2, so its logarithm has a
+    variance of 0.045; a fall by a factor D on the way adds log(D) * 0.09 (a
+    walk of code steps), at most 0.11 for D = 3.3 (the others' fall is
+    forgotten). One deviation is up to 0.4, 1 % and 99 % are at 2.33 of them:
+    factors of 0.39 and 2.54; the median is within exp(-var / 2) = 0.93, taken
+    twice as wide."""
+    n = 12800
+    g = gen(1)
+    p, q = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    eight = mx.AdamW([p], state_bits=8, betas=(0.9, b2), lr=1e-3, weight_decay=0.0)
+    full = mx.AdamW([q], betas=(0.9, b2), lr=1e-3, weight_decay=0.0)
+    scale = torch.ones(n, device="cuda")
+    moved = []
+    for t in range(steps):
+        if t == steps // 4:
+            scale[::2] = small
+        grad = torch.randn(n, generator=g, device="cuda") * scale
+        before = p.clone(), q.clone()
+        eight.step([grad])
+        full.step([grad])
+        if t >= steps - 50:
+            moved.append([float((a - b)[::2].square().mean()) for a, b in zip((p, q), before)])
+    ratio = decoded(eight.exp_avg_sq[0], eight.exp_avg_sq_scale[0]) / full.exp_avg_sq[0].sqrt()
+    for half in (ratio[::2], ratio[1::2]):
+        low, mid, high = torch.quantile(half, torch.tensor([0.01, 0.5, 0.99], device="cuda")).tolist()
+        assert 0.86 < mid < 1.16 and low > 0.39 and high < 2.54, (low, mid, high)
+    # and the steps are as large: m / r, with r's deviation of up to 0.4
+    a, b = torch.tensor(moved).mean(0).sqrt().tolist()
+    assert 0.7 < a / b < 1.5, (a, b)
+
+
+def test_adamw_random_rounding_has_an_exact_mean(mx):
+    """Every code, 25400 times, through one step without gradients beside a
+    largest value that stays: each comes out as one of its value's two
+    neighbours, on average as the value itself; the same again, and otherwise
+    at another step or place in the list."""
+    b1, b2, t = 0.9, 0.999, 5000
+    start = torch.full((126, 200, 128), 126, dtype=torch.uint8, device="cuda")   # a block's first value: its largest
+    start[:, :, 1:] = torch.arange(1, 127, dtype=torch.uint8, device="cuda")[:, None, None]
+    grad = torch.zeros(126, 200, 128, device="cuda")
+    grad[:, :, 0] = 448.0
+    start, grad = start.reshape(-1), grad.reshape(-1)
+    n = start.numel()
+    sign = torch.where(torch.arange(n, device="cuda") % 2 == 0, 0, 128).to(torch.uint8)
+
+    def run(step, place=0):
+        zeros = lambda dtype=F32, count=8: [torch.zeros(count, dtype=dtype, device="cuda")] * place  # noqa: E731
+        one = torch.ones(n // 128, device="cuda")
+        opt = mx.AdamW(zeros() + [torch.zeros(n, device="cuda")], state_bits=8, betas=(b1, b2),
+                       weight_decay=0.0, step=step, exp_avg=zeros(torch.uint8) + [start | sign],
+                       exp_avg_sq=zeros(torch.uint8) + [start.clone()],
+                       exp_avg_scale=zeros(F32, 1) + [one], exp_avg_sq_scale=zeros(F32, 1) + [one.clone()])
+        opt.step(zeros() + [grad])
+        return opt.exp_avg[-1], opt.exp_avg_scale[-1], opt.exp_avg_sq[-1], opt.exp_avg_sq_scale[-1]
+
+    m, ms, v, vs = run(t)
+    again, other, moved = run(t), run(t + 1), run(t, place=1)
+    assert torch.equal(m, again[0]) and torch.equal(v, again[2])
+    assert not torch.equal(m, other[0]) and not torch.equal(v, other[2])
+    assert not torch.equal(v, moved[2])
+    table = torch.arange(0, 127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).float()
+    was = start.view(torch.float8_e4m3fn).float()
+    for got, scale, factor, signed in ((m, ms, b1, True), (v, vs, b2 ** 0.5, False)):
+        value = (got & 127).view(torch.float8_e4m3fn).float()
+        if signed:
+            assert torch.equal((got & 128)[value > 0], sign[value > 0])
+        exact = was.double() * factor / scale.repeat_interleave(128).double()   # in the block's new scale
+        exact[grad > 0] = 448.0
+        low = torch.searchsorted(table.double(), exact * (1 - 2.0 ** -20), right=True) - 1
+        high = torch.searchsorted(table.double(), exact * (1 + 2.0 ** -20)).clamp(max=126)
+        at = (got & 127).long()
+        assert ((at >= low) & (at <= high)).all()
+        inner = torch.ones_like(got, dtype=torch.bool).view(-1, 128)
+        inner[:, 0] = False
+        for c in range(1, 127):
+            these = (start == c) & inner.view(-1)
+            if not signed and c == 1:
+                assert (at[these] == 1).all()    # a positive root never becomes zero
+                continue
+            x, mean = value[these].double(), float(exact[these].mean())
+            below, above = table[table <= mean].max().item(), table[table > mean].min().item()
+            chance = (mean - below) / (above - below)
+            # five deviations of a mean of len(x) roundings, one of them, and fp32's own
+            sd = (above - below) * (chance * (1 - chance) / len(x)) ** 0.5
+            assert abs(float(x.mean()) - mean) <= 5 * sd + (above - below) / len(x) + 2.0 ** -20 * mean, (c, factor)
