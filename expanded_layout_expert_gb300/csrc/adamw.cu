@@ -26,24 +26,29 @@
 // below w = 1/24 the codes of m and r are rounded up or down at random, with the
 // chances that make the mean exact: r then follows its average within some 20 %
 // (a step's variance, w times a code's step of 9 %, against a memory of 1 / w steps)
-// whatever b2, and a value without gradients stops moving. From 1/24 on (every step
-// with b2 <= 0.95, the first 24 with any b2) the average moves by code steps, and
-// rounding to nearest has the smaller error (r within 20 % at the 99th percentile,
-// 31 % at random, b2 = 0.95) and takes 420 instead of 480 us (134 M values). The bits come from the step's number and the value's
-// place (tensor in the list, index), so a step gives the same codes every time.
+// whatever b2. The bits come from the step's number and the value's place (tensor
+// in the list, index), so a step gives the same codes every time. From 1/24 on (every
+// step with b2 <= 0.958, the first 24 with any b2) the average moves by code steps,
+// and rounding to nearest has the smaller error (r within 20 % at the 99th
+// percentile, 31 % at random, b2 = 0.95) and takes 439 instead of 480 us (134 M
+// values). One thing it would hold there too: m's codes below 2^-6 are whole
+// multiples of the least, whose 0.9th part rounds back to themselves up to four,
+// so a value whose gradients have ended would be moved on by 0.15 lr at every step,
+// for ever. At a step whose gradient is zero those codes become zero (4 % of the
+// time: 420 us without).
 //
 // Bytes a value: 8 (p) + 2|4 (g) + 16 (fp32 m, v) or 4 + 16/128 (8 bits) + 2
 // (copy): bound by HBM with 32-bit states (577 us for 134 M values, fp32
 // gradients, bf16 copies: 6.97 TB/s). With 8-bit states the time hardly depends
-// on the gradients' bytes (420 us in fp32, 407 in bf16: 5.8 and 5.3 TB/s): there
+// on the gradients' bytes (439 us in fp32, 428 in bf16: 5.5 and 5.1 TB/s): there
 // the instructions of the exactly rounded root, quotient and codes set it (78 %
 // of the issue slots), and many small blocks keep them flowing (128 threads, 1024
-// values, 14 blocks an SM; with 256 threads, 4096 values and five blocks it
-// took 549 us). A warp takes 128 consecutive values, 4 per lane (16 bytes of
+// values, 14 blocks an SM; when they took 420 us, 256 threads, 4096 values and
+// five blocks took 549). A warp takes 128 consecutive values, 4 per lane (16 bytes of
 // each fp32 array), which is also one scale block, so its largest magnitudes are
 // two warp reductions. The tensors' table is a kernel parameter: nothing is
 // copied to the device before the launch. Types are asked at every access:
-// kernels compiled for one set of types took 418 instead of 420 us.
+// kernels compiled for one set of types took 418 us then.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -56,7 +61,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBlocksPerSm = 14;            // 36 registers a thread
+constexpr int kBlocksPerSm = 14;            // 32 registers a thread
 constexpr int kBlock = 128;                 // values that share a scale = values of a warp
 constexpr int kChunk = 1024;                // values of a block: two scale blocks per warp
 constexpr float kTinyAmax = 1e-30f;
@@ -292,11 +297,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (h.scale != nullptr) g[j] = __fmul_rn(g[j], scale);
+      const bool ended = Bits == 8 && !Random && g[j] == 0.0f && fabsf(m[j]) < 0x1p-6f * x.ms;
       m[j] = __fadd_rn(__fmul_rn(m[j], h.b1), __fmul_rn(g[j], h.c1));
       v[j] = __fadd_rn(__fmul_rn(v[j], h.b2), __fmul_rn(__fmul_rn(g[j], g[j]), h.c2));
       r[j] = __fsqrt_rn(v[j]);
       const float d = __fadd_rn(__fmul_rn(r[j], h.root), h.eps);
       p[j] = __fsub_rn(__fmul_rn(p[j], h.decay), __fdiv_rn(__fmul_rn(m[j], h.step_size), d));
+      if (ended) m[j] = 0.0f;
     }
     store4(t.p, p_type, i, n, vec, p);
     if (has_copy) store4(t.copy, copy_type, i, n, vec, p);

@@ -461,7 +461,8 @@ typedef struct {
  * are rounded to nearest while the newest gradient's share of v's average,
  * (1-b2)/(1-b2^step), is at least 1/24, then at random with an exact mean
  * (nearest would hold sqrt(v) where it is), from bits that depend on step, the
- * tensor's place among the non-empty ones and the index alone. A
+ * tensor's place among the non-empty ones and the index alone. With nearest, a
+ * code of m below 2^-6 becomes zero at a step whose gradient is zero. A
  * gradient that is not finite spoils its value, and with 8-bit states what
  * shares its block of 128 after this step.
  * step counts from 1. step and lr are values of the launch, so a stream that

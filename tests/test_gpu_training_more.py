@@ -217,3 +217,47 @@ def test_adamw_random_rounding_has_an_exact_mean(mx):
             # five deviations of a mean of len(x) roundings, one of them, and fp32's own
             sd = (above - below) * (chance * (1 - chance) / len(x)) ** 0.5
             assert abs(float(x.mean()) - mean) <= 5 * sd + (above - below) / len(x) + 2.0 ** -20 * mean, (c, factor)
+
+
+@pytest.mark.parametrize("b1,b2", [(0.9, 0.95), (0.95, 0.95), (0.9, 0.98)])
+def test_adamw_8_bit_states_of_values_without_gradients(mx, b1, b2):
+    """Half of every block gets no gradients any more, while the other half
+    does: its first moments reach zero and it stops moving. A first moment of
+    the largest code is under the smallest after log(448 * 512) / -log(b1) =
+    241 steps at 0.95; rounded at random (b2 = 0.98) it is then gone by each
+    step with a chance of 1 - b1, and 450 more leave none."""
+    n = 12800
+    g = gen(2)
+    p = torch.zeros(n, device="cuda")
+    opt = mx.AdamW([p], state_bits=8, betas=(b1, b2), lr=1e-3, weight_decay=0.0)
+    for t in range(1000):
+        grad = normal(g, n)
+        if t >= 200:
+            grad[::2] = 0
+        opt.step([grad])
+        if t == 900:
+            at = p.clone()
+    assert (opt.exp_avg[0][::2] & 127 == 0).all()
+    assert torch.equal(p[::2], at[::2]) and not torch.equal(p[1::2], at[1::2])
+
+
+def test_adamw_8_bit_states_of_blocks_without_gradients(mx):
+    """No gradient in a whole block (an expert without tokens): the moments
+    decay with the block's scale, as they do in 32 bits, and the codes stay,
+    but for m's below 2^-6, which become zero."""
+    n = 12800
+    g = gen(4)
+    p, q, grad = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), normal(g, n)
+    eight = mx.AdamW([p], state_bits=8, betas=(0.9, 0.95), weight_decay=0.0)
+    full = mx.AdamW([q], betas=(0.9, 0.95), weight_decay=0.0)
+    for opt in (eight, full):
+        opt.step([grad])
+    codes = eight.exp_avg[0].clone(), eight.exp_avg_sq[0].clone()
+    for _ in range(40):
+        for opt in (eight, full):
+            opt.step([torch.zeros_like(grad)])
+    assert torch.equal(eight.exp_avg_sq[0], codes[1])
+    assert torch.equal(eight.exp_avg[0] & 127, torch.where(codes[0] & 127 < 8, 0, codes[0] & 127))
+    for scales, value in ((eight.exp_avg_scale[0], full.exp_avg[0]), (eight.exp_avg_sq_scale[0], full.exp_avg_sq[0].sqrt())):
+        want = value.abs().view(-1, 128).amax(1) / 448
+        assert ((scales - want).abs() <= 50 * 2.0 ** -22 * want).all()
