@@ -326,6 +326,11 @@ class AdamW:
         self.copies = [None] * n if copies is None else list(copies)
         if len(self.copies) != n:
             raise ValueError(f"{len(self.copies)} copies for {n} parameters")
+        for codes, scales, name in ((exp_avg, exp_avg_scale, "exp_avg"),
+                                    (exp_avg_sq, exp_avg_sq_scale, "exp_avg_sq")):
+            if state_bits == 8 and (codes is None) != (scales is None):
+                raise ValueError(f"8-bit {name} and {name}_scale come together: codes without their scales "
+                                 "stand for nothing")
         code = torch.float32 if state_bits == 32 else torch.uint8
 
         def state(given, name, dtype, count):

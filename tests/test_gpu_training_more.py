@@ -261,3 +261,13 @@ def test_adamw_8_bit_states_of_blocks_without_gradients(mx):
     for scales, value in ((eight.exp_avg_scale[0], full.exp_avg[0]), (eight.exp_avg_sq_scale[0], full.exp_avg_sq[0].sqrt())):
         want = value.abs().view(-1, 128).amax(1) / 448
         assert ((scales - want).abs() <= 50 * 2.0 ** -22 * want).all()
+
+
+@pytest.mark.parametrize("name,dtype,count", [("exp_avg", torch.uint8, 256), ("exp_avg_scale", F32, 2),
+                                              ("exp_avg_sq", torch.uint8, 256), ("exp_avg_sq_scale", F32, 2)])
+def test_adamw_checkpoint_in_part_is_refused(mx, name, dtype, count):
+    """8-bit codes without their scales (or scales without codes) would go on
+    as zeros."""
+    p = torch.zeros(256, device="cuda")
+    with pytest.raises(ValueError, match="come together"):
+        mx.AdamW([p], state_bits=8, **{name: [torch.ones(count, dtype=dtype, device="cuda")]})
