@@ -484,7 +484,12 @@ class TrainableExperts:
         dev = _device(self.w13, "w13")
         _rows(x, "x", self.T, self.H, torch.bfloat16, dev)
         _whole(topk_ids, "topk_ids", (self.T, self.K), torch.int32, dev)
+        if _whole(topk_w, "topk_w", (self.T, self.K), torch.float32, dev) is None:
+            raise ValueError("topk_w is needed")
+        _word(n_valid, "n_valid", dev)
+        _stream(stream, dev)
         lay = self.lay
+        self._ready = False   # from here on the buffers are another forward's
         expand_layout(topk_ids, self.E, self.align, self.M_cap, n_valid, self.ws, self.status, lay,
                       stream)
         expand_rows(x, lay, topk_w, n_valid, self.xe, self.row_w, self.status, stream)
@@ -499,9 +504,9 @@ class TrainableExperts:
         from . import combine
         if not self._ready:
             raise RuntimeError("backward needs a forward before it")
-        self._ready = False
         lay, nv, st = self.lay, self._n_valid, self.status
-        ddown = expand_rows(dy, lay, None, nv, self.down, None, st, stream)
+        ddown = expand_rows(dy, lay, None, nv, self.down, None, st, stream)   # a dy it refuses costs nothing
+        self._ready = False
         grouped_matmul_wgrad(ddown, self.h, lay, self.dw2, accumulate, status=st, stream=stream)
         grouped_matmul_dgrad(ddown, self.w2, lay, self.dh, st, stream)
         dgu, drow_w = swiglu_backward(self.dh, self.gu, lay, self.row_w, self.gu, self.drow_w, stream)

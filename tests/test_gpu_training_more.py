@@ -271,3 +271,40 @@ def test_adamw_checkpoint_in_part_is_refused(mx, name, dtype, count):
     p = torch.zeros(256, device="cuda")
     with pytest.raises(ValueError, match="come together"):
         mx.AdamW([p], state_bits=8, **{name: [torch.ones(count, dtype=dtype, device="cuda")]})
+
+
+# --------------------------------------------------------------- the layer
+def small_layer(mx, T=16, K=2, E=4, H=64, I=64):
+    g = gen(1)
+    layer = mx.TrainableExperts(normal(g, E, 2 * I, H, dtype=BF16, std=0.1), normal(g, E, H, I, dtype=BF16, std=0.1),
+                                K=K, max_tokens=T)
+    w, ids = torch.rand(T, E, generator=g, device="cuda").topk(K, dim=1)
+    return layer, normal(g, T, H, dtype=BF16), ids.to(torch.int32).contiguous(), w.contiguous()
+
+
+def test_refused_calls_leave_the_forward(mx):
+    """A forward or backward refused for its arguments leaves the forward
+    before it, and the backward that belongs to it, as they were."""
+    layer, x, ids, w = small_layer(mx)
+    layer.forward(x, ids, w)
+    layer.backward(x)
+    want = [t.clone() for t in (layer.dx, layer.dtopk_w, *layer.gradients)]
+    layer.forward(x, ids, w)
+    other = ids.flip(0).contiguous()
+    for bad in ((x.float(), other, w), (x, other.long(), w), (x, other, w.double()), (x, other, None),
+                (x, other, w, torch.ones(1, device="cuda")), (x, other, w[:, :1])):
+        with pytest.raises(ValueError):
+            layer.forward(*bad)
+    for bad in (x.float(), x.half(), x[:-1], x[:, :-8]):
+        with pytest.raises(ValueError):
+            layer.backward(bad)
+    with pytest.raises(mx.MoEError):   # rows that do not begin on 16 bytes
+        layer.backward(torch.zeros(16, 72, dtype=BF16, device="cuda")[:, 1:65])
+    layer.backward(x)
+    assert all(torch.equal(a, b) for a, b in zip(want, (layer.dx, layer.dtopk_w, *layer.gradients)))
+    # refused by the library, once the layout was made: no backward of a mixture
+    layer.forward(x, ids, w)
+    with pytest.raises(mx.MoEError):
+        layer.forward(torch.zeros(16, 72, dtype=BF16, device="cuda")[:, 1:65], other, w)
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
