@@ -308,3 +308,24 @@ def test_refused_calls_leave_the_forward(mx):
         layer.forward(torch.zeros(16, 72, dtype=BF16, device="cuda")[:, 1:65], other, w)
     with pytest.raises(RuntimeError):
         layer.backward(x)
+
+
+def test_n_valid_belongs_to_the_forward(mx):
+    """backward reads the word again: one changed on the way would mix two
+    batches' rows."""
+    layer, x, ids, w = small_layer(mx)
+    n_valid = torch.tensor([9], dtype=torch.int32, device="cuda")
+    layer.forward(x, ids, w, n_valid)
+    layer.backward(x)
+    want = layer.dx.clone()
+    layer.forward(x, ids, w, n_valid)
+    n_valid.fill_(14)
+    with pytest.raises(RuntimeError, match="n_valid"):
+        layer.backward(x)
+    layer.forward(x, ids, w, n_valid.fill_(9))
+    layer.backward(x)
+    assert torch.equal(layer.dx[:9], want[:9])
+    with torch.inference_mode():   # such a tensor counts no changes
+        layer.forward(x, ids, w, torch.tensor([9], dtype=torch.int32, device="cuda"))
+        layer.backward(x)
+    assert torch.equal(layer.dx[:9], want[:9])
