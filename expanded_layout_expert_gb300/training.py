@@ -104,11 +104,6 @@ def _word(t: Optional[torch.Tensor], name: str, dev: int):
     return t.data_ptr()
 
 
-def _version(t: Optional[torch.Tensor]):
-    """Counts the in-place changes of a tensor (None: it has none to count)."""
-    return None if t is None or t.is_inference() else t._version
-
-
 def _segments(lay, dev: int) -> tuple:
     E = lay.E
     return _whole(lay.start, "lay.start", (E,), torch.int32, dev), \
@@ -443,8 +438,8 @@ class TrainableExperts:
     y[t] = sum_k w[t, k] * w2[e] (silu(g) * u), [g | u] = w13[e] x[t], e =
     topk_ids[t, k]. x and topk_ids, topk_w as in ExpandedMoELayer, with x in
     bfloat16; rows t >= n_valid are neither read nor written. backward belongs
-    to the last forward, whose n_valid it reads again, and overwrites what that
-    kept of gate_up.
+    to the last forward, of which the layer keeps what it needs (n_valid and x
+    may be refilled before it), and overwrites what that kept of gate_up.
     """
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, *, K: int, max_tokens: int,
@@ -474,7 +469,8 @@ class TrainableExperts:
         self.dh, self.drow_w = b16(M, self.I), f32(M)
         self.y, self.dx, self.dtopk_w = b16(max_tokens, H), b16(max_tokens, H), f32(max_tokens, K)
         self.dw13, self.dw2 = f32(E, twoI, H), f32(E, H, self.I)
-        self._n_valid = self._n_valid_version = None
+        self._n_valid = None          # the last forward's: None or the copy of its word
+        self._n_valid_word = i32(1)
         self._ready = False
 
     @property
@@ -496,6 +492,10 @@ class TrainableExperts:
         _stream(stream, dev)
         lay = self.lay
         self._ready = False   # from here on the buffers are another forward's
+        if n_valid is not None:
+            with torch.cuda.stream(stream):
+                n_valid = self._n_valid_word.copy_(n_valid.as_strided((1,), (1,)))
+        self._n_valid = n_valid
         expand_layout(topk_ids, self.E, self.align, self.M_cap, n_valid, self.ws, self.status, lay,
                       stream)
         expand_rows(x, lay, topk_w, n_valid, self.xe, self.row_w, self.status, stream)
@@ -503,15 +503,13 @@ class TrainableExperts:
         swiglu(self.gu, lay, self.row_w, self.h, stream)
         grouped_matmul(self.h, self.w2, lay, self.down, self.status, stream)
         combine(self.down, lay.src2dst, None, n_valid, self.y, stream)
-        self._n_valid, self._n_valid_version, self._ready = n_valid, _version(n_valid), True
+        self._ready = True
         return self.y
 
     def backward(self, dy: torch.Tensor, accumulate: bool = False, stream=None):
         from . import combine
         if not self._ready:
             raise RuntimeError("backward needs a forward before it")
-        if _version(self._n_valid) != self._n_valid_version:
-            raise RuntimeError("n_valid has been changed in place since the forward that this backward belongs to")
         lay, nv, st = self.lay, self._n_valid, self.status
         ddown = expand_rows(dy, lay, None, nv, self.down, None, st, stream)   # a dy it refuses costs nothing
         self._ready = False

@@ -310,22 +310,53 @@ def test_refused_calls_leave_the_forward(mx):
         layer.backward(x)
 
 
-def test_n_valid_belongs_to_the_forward(mx):
-    """backward reads the word again: one changed on the way would mix two
-    batches' rows."""
+@pytest.mark.parametrize("side", [False, True])
+def test_n_valid_belongs_to_the_forward(mx, side):
+    """A caller may refill its word (and x) for the next batch before the
+    backward, which takes the forward's."""
     layer, x, ids, w = small_layer(mx)
-    n_valid = torch.tensor([9], dtype=torch.int32, device="cuda")
-    layer.forward(x, ids, w, n_valid)
-    layer.backward(x)
-    want = layer.dx.clone()
-    layer.forward(x, ids, w, n_valid)
-    n_valid.fill_(14)
-    with pytest.raises(RuntimeError, match="n_valid"):
+    n_valid = torch.tensor([9, 5], dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    results = []
+    for refill in (False, True):
+        mine, word = x.clone(), n_valid.clone()
+        torch.cuda.synchronize()
+        layer.forward(mine, ids, w, word, stream=stream)
+        torch.cuda.synchronize()
+        if refill:
+            word.fill_(14)
+            mine.fill_(float("nan"))
+            torch.cuda.synchronize()
+        layer.dx.fill_(7)
+        layer.dtopk_w.fill_(7)
+        torch.cuda.synchronize()
+        layer.backward(x, stream=stream)
+        torch.cuda.synchronize()
+        results.append([t.clone() for t in (layer.dx, layer.dtopk_w, *layer.gradients)])
+        assert (layer.dx[9:] == 7).all() and (layer.dtopk_w[9:] == 7).all() and not (layer.dx[:9] == 7).any()
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_n_valid_in_a_graph(mx):
+    """The word is copied by the graph, at each replay."""
+    layer, x, ids, w = small_layer(mx)
+    n_valid = torch.tensor([16], dtype=torch.int32, device="cuda")
+
+    def once():
+        layer.forward(x, ids, w, n_valid)
         layer.backward(x)
-    layer.forward(x, ids, w, n_valid.fill_(9))
-    layer.backward(x)
-    assert torch.equal(layer.dx[:9], want[:9])
-    with torch.inference_mode():   # such a tensor counts no changes
-        layer.forward(x, ids, w, torch.tensor([9], dtype=torch.int32, device="cuda"))
-        layer.backward(x)
-    assert torch.equal(layer.dx[:9], want[:9])
+
+    once()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once()
+    for n in (16, 3, 11):
+        n_valid.fill_(n)
+        once()
+        want = [t.clone() for t in (layer.dx[:n], *layer.gradients)]
+        layer.dx.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, (layer.dx[:n], *layer.gradients)))
+        assert (layer.dx[n:] == 0).all()
