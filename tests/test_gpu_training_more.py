@@ -360,3 +360,96 @@ def test_n_valid_in_a_graph(mx):
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(want, (layer.dx[:n], *layer.gradients)))
         assert (layer.dx[n:] == 0).all()
+
+
+# --------------------------------------------------------------- the products
+U = {BF16: 2.0 ** -8, F16: 2.0 ** -11, F32: 2.0 ** -24}
+
+
+def near(got, a, b, dtype, what):
+    """got = a b^T rounded to dtype, a [i, c] and b [j, c] in 64 bits, by the
+    norm: each result is off by half a step at most, and each of its sum's c / 16
+    additions of 16 products by a step of fp32 at most (the tensor core
+    truncates). A lost term of 4104 is 1.6 % of the norm, the bound 0.5 %."""
+    exact = a @ b.T
+    bound = U[dtype] * float(exact.norm()) + (a.shape[1] // 16 + 1) * 2.0 ** -23 * float((a.abs() @ b.abs().T).norm())
+    assert float((got.double() - exact).norm()) <= bound, what
+
+
+def operands(mx, counts, N, Kd, dtype, seed=0):
+    lay, bounds = layout_of(mx, counts)
+    g = gen(seed + N + Kd)
+    x, dy = normal(g, lay.M_cap, Kd, dtype=dtype), normal(g, lay.M_cap, N, dtype=dtype)
+    return lay, bounds, x, dy, normal(g, lay.E, N, Kd, dtype=dtype, std=0.1)
+
+
+def check_products(mx, lay, bounds, x, dy, w, only=None):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = mx.grouped_matmul(x, w, lay, status=status)
+    dx = mx.grouped_matmul_dgrad(dy, w, lay, status=status)
+    dw = {t: mx.grouped_matmul_wgrad(dy, x, lay, out_dtype=t, status=status) for t in (x.dtype, F32)}
+    assert status.item() == 0
+    for e, (a, b) in enumerate(bounds):
+        if only is not None and e not in only:
+            continue
+        if a == b:
+            assert all((t[e] == 0).all() for t in dw.values())
+            continue
+        X, DY, W = x[a:b].double(), dy[a:b].double(), w[e].double()
+        near(y[a:b], X, W, x.dtype, f"forward {e}")
+        near(dx[a:b], DY, W.T, x.dtype, f"dgrad {e}")
+        for t, got in dw.items():
+            near(got[e], DY.T, X.T, t, f"wgrad {t} {e}")
+
+
+@pytest.mark.parametrize("E,N,Kd", [(33, 136, 520), (160, 264, 72), (160, 40, 264), (1024, 40, 64)])
+def test_many_experts_with_many_rows(mx, E, N, Kd):
+    """Over 40 rows an expert on average, so the pairs take them: several
+    experts a thread and several warps in the search for a tile's expert."""
+    counts = [0 if e % 11 == 5 else (e * 37) % 131 + (300 if e % 40 == 7 else 0) for e in range(E)]
+    assert sum(counts) > 40 * E
+    only = None if E <= 160 else set(range(0, E, 13)) | {E - 1}
+    check_products(mx, *operands(mx, counts, N, Kd, BF16), only=only)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("counts", [[4700, 3, 2049], [1, 2048, 2047, 0, 5000]], ids=["a", "b"])
+def test_experts_with_many_row_tiles(mx, counts, dtype):
+    """More than eight tiles of 256 rows, several columns of tiles: the order of
+    the tiles begins a second column of its own."""
+    check_products(mx, *operands(mx, counts, 1032, 776, dtype))
+
+
+@pytest.mark.parametrize("counts", [[1400] + [(e * 7) % 61 for e in range(159)], [0] * 63 + [2500]],
+                         ids=["skewed", "one of 64"])
+def test_few_rows_on_average(mx, counts):
+    """At most 40 rows an expert on average, most of them with one expert."""
+    assert sum(counts) <= 40 * len(counts)
+    check_products(mx, *operands(mx, counts, 520, 1032, BF16), only={0, 1, 2, 30, len(counts) - 1})
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("N,Kd", [(136, 4104), (4104, 136), (2048, 768)])
+def test_long_contractions(mx, N, Kd, dtype):
+    """No term of a long sum is lost, whole and split over a cluster, few rows
+    and many."""
+    check_products(mx, *operands(mx, [1, 9, 0, 30, 5], N, Kd, dtype))
+    check_products(mx, *operands(mx, [700, 64, 0, 351], N, Kd, dtype))
+
+
+@pytest.mark.parametrize("mean", [0.0, 0.5])
+def test_long_sums_of_many_tiles_do_not_drift(mx, mean):
+    """wgrad with too many tiles to share an expert's rows among CTAs: pairs,
+    whose sums leave the tensor core after at most 56 additions (896 rows),
+    each truncated by 2^-24 of its size at most, as in the shared form."""
+    lay, bounds = layout_of(mx, [16384, 0, 897])
+    g = gen(6)
+    x = (normal(g, lay.M_cap, 1032) + mean).to(BF16)
+    dy = (normal(g, lay.M_cap, 1032) + mean).to(BF16)
+    base = normal(g, 3, 1032, 1032)
+    dw = mx.grouped_matmul_wgrad(dy, x, lay, out_dtype=F32)
+    added = mx.grouped_matmul_wgrad(dy, x, lay, out=base.clone(), accumulate=True)
+    for e, (a, b) in enumerate(bounds):
+        r = dy[a:b].double().T @ x[a:b].double()
+        for got, want in ((dw[e], r), (added[e], r + base[e].double())):
+            assert float((got.double() - want).norm()) <= 60 * 2.0 ** -24 * float(want.norm())
