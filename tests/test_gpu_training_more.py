@@ -453,3 +453,37 @@ def test_long_sums_of_many_tiles_do_not_drift(mx, mean):
         r = dy[a:b].double().T @ x[a:b].double()
         for got, want in ((dw[e], r), (added[e], r + base[e].double())):
             assert float((got.double() - want).norm()) <= 60 * 2.0 ** -24 * float(want.norm())
+
+
+# ------------------------------------------------------ gradients not finite
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("bits,b2", [(32, 0.95), (8, 0.95), (8, 0.999)])
+def test_adamw_gradients_that_are_not_finite(mx, bits, b2, value):
+    """Each spoils its own parameter at once; with 8-bit states the rest of
+    its block of 128 is right at this step and the other blocks always."""
+    n, at = 1000, [5, 300, 301, 302, 303, 999]
+    g = gen(8)
+    start, grads = normal(g, n), [normal(g, n) for _ in range(30)]
+    p, q, copy = start.clone(), start.clone(), torch.zeros(n, dtype=BF16, device="cuda")
+    bad = mx.AdamW([p], copies=[copy], state_bits=bits, betas=(0.9, b2))
+    good = mx.AdamW([q], state_bits=bits, betas=(0.9, b2))
+    spoilt = torch.zeros(n, dtype=torch.bool, device="cuda")
+    spoilt[at] = True
+    for t in range(26):
+        bad.step([grads[t]])
+        good.step([grads[t]])
+    wrong = grads[26].clone()
+    wrong[at] = value
+    bad.step([wrong])
+    good.step([grads[26]])
+    assert p[spoilt].isnan().all() and torch.equal(p[~spoilt], q[~spoilt])
+    assert torch.equal(copy[~spoilt], q[~spoilt].bfloat16()) and copy[spoilt].isnan().all()
+    if bits == 8:
+        spoilt = spoilt.nonzero().view(-1) // 128
+        spoilt = torch.isin(torch.arange(n, device="cuda") // 128, spoilt)
+    for t in range(27, 30):
+        bad.step([grads[t]])
+        good.step([grads[t]])
+    assert torch.equal(p[~spoilt], q[~spoilt]) and p[at].isnan().all()
+    for a, b in zip((bad.exp_avg[0], bad.exp_avg_sq[0]), (good.exp_avg[0], good.exp_avg_sq[0])):
+        assert torch.equal(a[~spoilt], b[~spoilt])
