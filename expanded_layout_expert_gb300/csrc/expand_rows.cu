@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) expand_rows_kernel(
   if (static_cast<int>(blockIdx.x) < pad_blocks) {
     const int e = blockIdx.x / pad_blocks_per_expert;
     const int sub = blockIdx.x % pad_blocks_per_expert;
-    const int64_t end = psum[e];
+    const int64_t end = max(psum[e], 0);   // clamped into the buffer, as the products' segments are
     int64_t seg_end = (end + align - 1) / align * align;
     if (seg_end > M_cap) seg_end = M_cap;
     const int64_t r0 = end + static_cast<int64_t>(sub) * kPadRowsPerBlock;

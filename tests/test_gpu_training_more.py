@@ -487,3 +487,18 @@ def test_adamw_gradients_that_are_not_finite(mx, bits, b2, value):
     assert torch.equal(p[~spoilt], q[~spoilt]) and p[at].isnan().all()
     for a, b in zip((bad.exp_avg[0], bad.exp_avg_sq[0]), (good.exp_avg[0], good.exp_avg_sq[0])):
         assert torch.equal(a[~spoilt], b[~spoilt])
+
+
+def test_expand_rows_of_segments_outside_the_buffer(mx):
+    """Ends before the buffer or past it: only rows inside are zeroed (the
+    buffer is the middle of a larger one)."""
+    lay, _ = layout_of(mx, [5, 5, 5, 5])
+    lay.align, lay.src2dst = 16, torch.full((4, 2), -1, dtype=torch.int32, device="cuda")
+    lay.psum = torch.tensor([-7, 20, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+    large = torch.full((60, 64), 5.0, dtype=BF16, device="cuda")
+    weights = torch.full((60,), 5.0, device="cuda")
+    mx.expand_rows(torch.ones(4, 64, dtype=BF16, device="cuda"), lay, torch.ones(4, 2, device="cuda"),
+                   out=large[20:40], row_w=weights[20:40])
+    assert (large[:20] == 5).all() and (large[40:] == 5).all()
+    assert (weights[:20] == 5).all() and (weights[40:] == 5).all()
+    assert (large[20:40] == 5).all() and (weights[20:40] == 5).all()   # 0 and 20 end on no gap inside
