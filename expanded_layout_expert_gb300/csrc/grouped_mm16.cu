@@ -31,7 +31,7 @@
 // at 16384, 8.7e-5 at 65536 against 1e-7 to 5e-7 of fp32 products). In
 // forward and dgrad that is far below the rounding to 16 bits. wgrad contracts
 // over as many rows as an expert has, so its sums leave tensor memory after at
-// most 896 rows (fp32 results; 4096 for 16-bit ones) and are added up, rounding to
+// most 512 rows (fp32 results; 4096 for 16-bit ones) and are added up, rounding to
 // nearest, in the epilogue's registers.
 //
 // Persistent CTAs, one per SM, warp-specialised as in grouped_gemm.cu: warp 0
@@ -76,20 +76,23 @@ constexpr int kTmemCols = kAcc * BN;
 constexpr int kEpiWarps = 8;     // two per TMEM lane quarter
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kMaxE = 1024;
-// wgrad: blocks of BC summed in tensor memory at a time, at most. Short chunks
-// make the tensor core wait for an epilogue that is still storing the tile
-// before: with 8 blocks 16-bit results of 1024 rows an expert (4096 x 4096) take
-// 844 us, with up to 64 804, those of the Zipf batch (7168 x 2048) 2.08 and 1.97 ms;
-// fp32 results with 8 and 14 take 899 and 893 us.
-constexpr int max_chunk(bool out16) { return out16 ? 64 : 14; }
+// wgrad: blocks of BC summed in tensor memory at a time, at most. fp32 results:
+// 512 rows, whose error is 5e-7 (plain fp32 products: 2e-7 to 1.7e-6); 896 rows were
+// 9e-7 off and took 906-911 us instead of 910-919 (1024 rows an expert, 4096 x
+// 4096). 16-bit results round to 2^-8 or 2^-11 anyway, and short chunks make the tensor
+// core wait for an epilogue that is still storing the tile before: with 8 blocks
+// they take 844-849 us there, with up to 64 813; those of the Zipf batch (124 k rows,
+// 7168 x 2048) 2.62-2.65 and 2.52-2.55 ms.
+constexpr int max_chunk(bool out16) { return out16 ? 64 : 8; }
 // wgrad: warps 0-3 hand registers to the epilogue, whose threads hold 128 sums
 // (56 * 128 + 224 * 256 = 168 * 384, the registers the block is launched with).
 constexpr int kRegsLow = 56;
 constexpr int kRegsHigh = 224;
 static_assert(kRegsLow * 128 + kRegsHigh * 256 == 168 * kThreads, "register split");
-// Row tiles in a column of the raster (see tile_at). Forward takes 3.52 ms with 8,
-// 3.62 with 4, 3.53 with 16 (Zipf rows, 4096 x 7168); wgrad added to fp32 1.07, 1.03
-// and 1.11 ms (1024 rows an expert, 4096 x 4096).
+// Row tiles in a column of the raster (see tile_at). Seconds long, at the power
+// limit, it decides little: forward takes 4.76 ms with 4, 8 and 16 (Zipf batch, 124 k
+// rows, 4096 x 7168); wgrad of that batch 2.51, 2.53 and 2.53 ms with 2, 4 and 8, and
+// added to fp32 (1024 rows an expert, 4096 x 4096) 1.03, 1.06 and 1.04 ms.
 constexpr int raster(int mode) { return mode == kWgrad ? 4 : 8; }
 
 // kCtas CTAs work on one tile of kCtas * 128 x 256.

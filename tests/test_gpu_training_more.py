@@ -502,3 +502,20 @@ def test_expand_rows_of_segments_outside_the_buffer(mx):
     assert (large[:20] == 5).all() and (large[40:] == 5).all()
     assert (weights[:20] == 5).all() and (weights[40:] == 5).all()
     assert (large[20:40] == 5).all() and (weights[20:40] == 5).all()   # 0 and 20 end on no gap inside
+
+
+@pytest.mark.parametrize("rows,N", [(896, 136), (16384, 136), (16384, 1032)], ids=["short", "shared", "pairs"])
+@pytest.mark.parametrize("mean", [0.0, 0.5])
+def test_fp32_sums_of_rows(mx, rows, N, mean):
+    """wgrad into fp32, by the norm. The tensor core adds 16 rows at a time
+    and truncates: half a step, 0.72 * 2^-24 of the sum so far, which is half of
+    the whole on average. At most 32 additions (512 rows) follow one another,
+    then the partial sums are rounded to nearest: 32 / 2 * 0.72 * 2^-24."""
+    lay, bounds = layout_of(mx, [rows, rows])
+    g = gen(3)
+    x = (normal(g, lay.M_cap, 1032) + mean).to(BF16)
+    dy = (normal(g, lay.M_cap, N) + mean).to(BF16)
+    dw = mx.grouped_matmul_wgrad(dy, x, lay, out_dtype=F32)
+    for e, (a, b) in enumerate(bounds):
+        r = dy[a:b].double().T @ x[a:b].double()
+        assert float((dw[e].double() - r).norm()) <= 11.5 * 2.0 ** -24 * float(r.norm())
