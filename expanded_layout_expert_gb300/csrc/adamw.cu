@@ -24,24 +24,24 @@
 // its old size for ever: with b2 = 0.98 to 0.999 and gradients that fall to 1 %
 // in half of every block, r was 6 to 130 times too large after 4000 steps. So
 // below w = 1/24 the codes of m and r are rounded up or down at random, with the
-// chances that make the mean exact: r then follows its average within some 20 %
-// (a step's variance, w times a code's step of 9 %, against a memory of 1 / w steps)
-// whatever b2. The bits come from the step's number and the value's place (tensor
-// in the list, index), so a step gives the same codes every time. From 1/24 on (every
-// step with b2 <= 0.958, the first 24 with any b2) the average moves by code steps,
-// and rounding to nearest has the smaller error (r within 20 % at the 99th
-// percentile, 31 % at random, b2 = 0.95) and takes 439 instead of 480 us (134 M
-// values). One thing it would hold there too: m's codes below 2^-6 are whole
-// multiples of the least, whose 0.9th part rounds back to themselves up to four,
-// so a value whose gradients have ended would be moved on by 0.15 lr at every step,
-// for ever. At a step whose gradient is zero those codes become zero (4 % of the
-// time: 420 us without).
+// chances that make the mean exact. A step's rounding then has a variance of at
+// most w times a code's step of 9 %, forgotten over 1 / w steps: r follows its
+// average with a deviation of 14 to 17 % (b2 = 0.98 to 0.999), a step's norm within
+// 3 %. The bits come from the step's number and the value's place (tensor in the
+// list, index), so a step gives the same codes every time. From w = 1/24 on (every
+// step with b2 <= 0.958, the first 24 with any b2) the average moves by code steps;
+// rounding to nearest has the smaller error there (8 % at b2 = 0.95, at random 12 %
+// at 0.96) and takes 439 instead of 480 us (134 M values). One thing it would still
+// hold: m's codes below 2^-6 are whole multiples of the least, and 0.9 of one rounds
+// back to itself up to four, so a value whose gradients have ended would be moved
+// on by 0.15 lr at every step, for ever. At a step whose gradient is zero those
+// codes become zero (4 % of the time: 420 us without).
 //
 // Bytes a value: 8 (p) + 2|4 (g) + 16 (fp32 m, v) or 4 + 16/128 (8 bits) + 2
 // (copy): bound by HBM with 32-bit states (577 us for 134 M values, fp32
 // gradients, bf16 copies: 6.97 TB/s). With 8-bit states the time hardly depends
 // on the gradients' bytes (439 us in fp32, 428 in bf16: 5.5 and 5.1 TB/s): there
-// the instructions of the exactly rounded root, quotient and codes set it (78 %
+// the instructions of the exactly rounded root, quotient and codes set it (82 %
 // of the issue slots), and many small blocks keep them flowing (128 threads, 1024
 // values, 14 blocks an SM; when they took 420 us, 256 threads, 4096 values and
 // five blocks took 549). A warp takes 128 consecutive values, 4 per lane (16 bytes of

@@ -47,9 +47,10 @@
 // their rows are shared by a cluster; forward and dgrad of experts with few rows
 // are grouped_mm16_few.cu's.
 //
-// What bounds it: power. Forward and dgrad run at 1.6 PFLOP/s with the SM clock
-// held near 1.4 GHz by the power limit, 92-97 % of what the library's product
-// of the same rows and weights reaches there. wgrad (both operands i/j-contiguous)
+// What bounds it: power. Forward and dgrad of long segments run at 1.5 to 1.6
+// PFLOP/s with the SM clock held near 1.4 GHz by the power limit, 92-97 % of what
+// the library's product of the same rows and weights reaches there; segments of
+// 160 to 600 rows are bound by whole tiles (300 rows an expert: 384 in tiles). wgrad (both operands i/j-contiguous)
 // is bound by the rate at which the tensor core reads such an A: 668 cycles a
 // block on long segments, against 531 for the others.
 #include <algorithm>
@@ -909,7 +910,9 @@ int check_rows(const char* what, const char* name, const void* a, int64_t ld, in
 // Rows per expert, on average, up to which the few-rows form is taken. With 24
 // rows it takes 171 us and the pairs 176 (32 experts of 4096 x 4096, forward;
 // dgrad 166 and 166), with 48 rows 183 and 178 (180 and 169); with 32 rows of
-// 64 experts of 4096 x 7168 it takes 551 and the pairs 587.
+// 64 experts of 4096 x 7168 it takes 551 and the pairs 587. The rows may all be
+// one expert's: 160 experts of 2048 x 4096, 6080 rows, 1400 of them with one, take
+// 427 us (dgrad 430), the weights alone 400 at HBM's rate.
 constexpr int kFewRows = 40;
 
 // Forward and dgrad: rows [M_cap, in] times weights -> rows [M_cap, out].

@@ -293,9 +293,9 @@ class AdamW:
              rounds it at random with an exact mean (repeatably: by the step's
              number and the value's place) once the newest gradient is under
              1/24 of the average (betas[1] over 0.958, after 24 steps); before,
-             to nearest. The root then follows its average within about 20 %
-             (one standard deviation); values under 4e-6 of their block's
-             largest are held at that.
+             to nearest. The root then follows its average with a deviation of
+             about 15 %; roots under 4e-6 of their block's largest are held at
+             that.
     exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, step: states to go on
              from (a checkpoint's); zeros by default. They are the optimizer's
              from then on.
