@@ -519,3 +519,27 @@ def test_fp32_sums_of_rows(mx, rows, N, mean):
     for e, (a, b) in enumerate(bounds):
         r = dy[a:b].double().T @ x[a:b].double()
         assert float((dw[e].double() - r).norm()) <= 11.5 * 2.0 ** -24 * float(r.norm())
+
+
+def test_adamw_random_rounding_of_many_tensors(mx):
+    """Every tensor of the list has bits of its own, those of a second launch
+    (from the 401st on) too; empty ones have no place."""
+    n, count = 512, 802
+    start, grad = torch.full((n,), 100, dtype=torch.uint8, device="cuda"), torch.zeros(n, device="cuda")
+    start[::128], grad[::128] = 126, 448.0
+    none = torch.zeros(0, device="cuda")
+
+    def run(empty):
+        params = [torch.zeros(n, device="cuda") for _ in range(count)]
+        codes = lambda: [start.clone() for _ in range(count)]  # noqa: E731
+        ones = lambda: [torch.ones(n // 128, device="cuda") for _ in range(count)]  # noqa: E731
+        pad = [none] * empty
+        opt = mx.AdamW(pad + params, state_bits=8, betas=(0.9, 0.999), weight_decay=0.0, step=5000,
+                       exp_avg=[none.byte()] * empty + codes(), exp_avg_sq=[none.byte()] * empty + codes(),
+                       exp_avg_scale=pad + ones(), exp_avg_sq_scale=pad + ones())
+        opt.step(pad + [grad] * count)
+        return torch.stack(opt.exp_avg[empty:])
+
+    m = run(0)
+    assert len(torch.unique(m, dim=0)) == count
+    assert torch.equal(m, run(3))
