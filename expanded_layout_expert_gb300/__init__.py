@@ -24,6 +24,8 @@ from ._capi import (MOE_BLOCK_M, MOE_FFN_UNFUSED, MOE_FOLD_WEIGHT_INTO_SCALE,
                     MOE_WEIGHT_OUTPUT_ROWS, MoEError, check, load)
 from .training import (AdamW, TrainableExperts, collect_row_grads, expand_rows, grouped_matmul,
                        grouped_matmul_dgrad, grouped_matmul_wgrad, swiglu, swiglu_backward)
+from .routing import combine_rows, combine_rows_backward, route_topk, route_topk_backward
+from .w4 import grouped_matmul_w4
 
 __all__ = [
     "expanded_capacity", "workspace_size", "expand_layout", "expand_scatter",
@@ -37,6 +39,8 @@ __all__ = [
     "scale_layout_of",
     "expand_rows", "collect_row_grads", "grouped_matmul", "grouped_matmul_dgrad",
     "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "AdamW", "TrainableExperts",
+    "route_topk", "route_topk_backward", "combine_rows", "combine_rows_backward",
+    "grouped_matmul_w4",
 ]
 
 

@@ -32,6 +32,9 @@ MOE_BF16 = 0
 MOE_F16 = 1
 MOE_F32 = 2
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
 MOE_BLOCK_M = 128
 
 ERROR_NAMES = {
@@ -44,7 +47,7 @@ ERROR_NAMES = {
 }
 
 # Every symbol include/moe_expand.h declares, with (restype, argtypes).
-P, I32, I64, SZ, F64 = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_double
+P, I32, I64, SZ, F32, F64 = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float, C.c_double
 SIGNATURES = {
     "moe_expanded_capacity": (I64, [I64, I32, I32, I32]),
     "moe_workspace_size": (SZ, [I64, I32, I32]),
@@ -73,6 +76,12 @@ SIGNATURES = {
     "moe_swiglu": (I32, [P, I64, I32, I32, P, P, I64, P, I64, P]),
     "moe_swiglu_backward": (I32, [P, I64, P, I64, I32, I32, P, P, I64, P, I64, P, P]),
     "moe_adamw_step": (I32, [P, I32, I32, F64, F64, F64, F64, F64, I64, P, P]),
+    "moe_route_topk": (I32, [P, I64, I32, P, P, I64, I32, I32, I32, I32, F32, P, P, P]),
+    "moe_route_topk_backward": (I32, [P, P, I64, I32, P, P, I64, I32, I32, I32, I32, F32, P, I64, P]),
+    "moe_combine_rows": (I32, [P, I64, I32, P, P, P, I64, I32, I32, I64, P, I64, P, I64, P, P]),
+    "moe_combine_rows_backward": (I32, [P, I64, P, I64, I32, P, P, P, P, I64, I32, I32, I32, I32, I64, P,
+                                        I64, P, P, P]),
+    "moe_grouped_mm_w4": (I32, [P, I64, P, P, P, I32, P, P, I32, I32, I32, I32, I64, I64, P, I64, P, P]),
     "moe_gemm_set_trace": (I32, [P]),
     "moe_selftest_bounded_wait": (I32, [I64, P, P, P]),
     "moe_last_error_string": (C.c_char_p, []),

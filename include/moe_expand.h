@@ -71,10 +71,14 @@ typedef struct CUstream_st* moe_stream_t; /* the same type as cudaStream_t */
                                             the tensor core's block scaling */
 #define MOE_FFN_UNFUSED          128 /* moe_grouped_ffn: gate_up, act+quant and down as three launches */
 
-/* Types of the 16-bit training calls and of moe_adamw_step. */
+/* Types of the 16-bit calls, of moe_route_topk's logits and of moe_adamw_step. */
 #define MOE_BF16 0
 #define MOE_F16  1
 #define MOE_F32  2
+
+/* Scores of moe_route_topk. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
 
 /* Rows per grouped-GEMM tile; tile_prefix counts tiles of this height. */
 #define MOE_BLOCK_M 128
@@ -472,6 +476,104 @@ typedef struct {
 int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int state_bits, double lr,
                    double beta1, double beta2, double eps, double weight_decay, int64_t step,
                    const float* d_grad_scale, moe_stream_t stream);
+
+/*
+ * ------------------------------------------------ router, weighted return
+ * The layer's two ends, in serving and training. The conventions above hold.
+ */
+
+/*
+ * The choice of K of E experts by the router's logits l [T, E], rows
+ * t < *d_n_valid (others are neither read nor written):
+ *   key_e = fl32(l_e + bias_e)  (bias NULL: 0), ids = the K largest keys, the
+ *   largest first, of equal ones the lowest e first
+ *   MOE_SCORE_SOFTMAX: topk_w[k] = factor p[ids[k]], p = softmax of l over E,
+ *                      or, with renormalize, over the chosen alone
+ *   MOE_SCORE_SIGMOID: topk_w[k] = factor s[ids[k]], s = 1 / (1 + e^-l), with
+ *                      renormalize divided by the sum of the chosen's s
+ * bias moves the choice alone (a load balancer's), not the weights. An expert
+ * whose key is -inf or NaN is never chosen; where fewer than K are left, the
+ * others get id -1 (no pair) and weight 0. A softmax over a row with a NaN or
+ * +inf has NaN weights.
+ *   logits   device fp32, bf16 or fp16 [T, ld >= E]; bias device fp32 [E]
+ *   topk_ids device int32 [T, K], topk_w device fp32 [T, K]
+ * E <= 1024, K <= 32, K <= E.
+ */
+int moe_route_topk(const void* logits, int64_t ld, int dtype, const float* bias,
+                   const int32_t* d_n_valid, int64_t T, int E, int K, int score, int renormalize,
+                   float factor, int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/*
+ * The gradient of moe_route_topk's logits, given topk_w's and the ids it chose
+ * (the choice itself has none, so bias has none). With c = factor, g = dtopk_w:
+ *   softmax                dl_e = c p_e (sum of g of e's pairs - sum_k g_k p[ids[k]])
+ *   softmax, renormalize   dl[ids[k]] += c r_k (g_k - sum_j g_j r_j), r = topk_w / c
+ *   sigmoid                dl[ids[k]] += c g_k s (1 - s)
+ *   sigmoid, renormalize   dl[ids[k]] += c r_k (1 - s) (g_k - sum_j g_j r_j)
+ * in fp32, rounded once; every dl of rows t < *d_n_valid is written (0 where it
+ * has no term). Pairs with an id outside [0, E) count for nothing; an id that
+ * comes twice adds twice.
+ *   dlogits  device, of logits' type, [T, ld_d >= E], not logits itself
+ */
+int moe_route_topk_backward(const float* dtopk_w, const void* logits, int64_t ld, int dtype,
+                            const int32_t* topk_ids, const int32_t* d_n_valid, int64_t T, int E, int K,
+                            int score, int renormalize, float factor, void* dlogits, int64_t ld_d,
+                            moe_stream_t stream);
+
+/*
+ * The experts' 16-bit rows back to their tokens, with weights by pair:
+ *   out[t] = residual[t] + sum_{k: src2dst[t,k] >= 0} topk_w[t,k] rows[src2dst[t,k]]
+ * for t < *d_n_valid, in fp32 in k order, rounded once (residual NULL: 0, topk_w
+ * NULL: 1). Other rows of out are not written. A token without pairs gets its
+ * residual. The weight of a k without a pair is not used, whatever it is.
+ *   rows     device 16-bit [M_cap, ld_rows >= H] of dtype; residual, out [T, ld >= H]
+ *            of the same; out may be residual itself (same stride)
+ * H and the strides are multiples of 8, pointers 16-byte aligned, K <= 32. A
+ * row >= M_cap is skipped and sets MOE_ERR_DEVICE_CHECK.
+ */
+int moe_combine_rows(const void* rows, int64_t ld_rows, int dtype, const float* topk_w,
+                     const int32_t* src2dst, const int32_t* d_n_valid, int64_t T, int H, int K,
+                     int64_t M_cap, const void* residual, int64_t ld_res, void* out, int64_t ld_out,
+                     int32_t* d_status, moe_stream_t stream);
+
+/*
+ * The gradients of moe_combine_rows (residual's is dy itself): for t < *d_n_valid
+ *   drows[src2dst[t,k]] = topk_w[t,k] dy[t]    (16-bit, rounded once)
+ *   dtopk_w[t,k] = sum_h dy[t,h] rows[src2dst[t,k],h]   (fp32; 0 where there is no pair)
+ * and the alignment gaps [psum[e], align(psum[e])) of drows are zeroed, as
+ * moe_expand_rows does. Other rows are not written. drows may be rows itself
+ * (same stride): a place is read before it is written. src2dst names a row
+ * once, as moe_expand_layout's does.
+ *   dy [T, ld_dy >= H], rows, drows [M_cap, ld >= H]: device 16-bit of dtype;
+ *   dtopk_w device fp32 [T, K]
+ */
+int moe_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, int64_t ld_rows,
+                              int dtype, const float* topk_w, const int32_t* src2dst,
+                              const int32_t* psum, const int32_t* d_n_valid, int64_t T, int H, int K,
+                              int E, int align, int64_t M_cap, void* drows, int64_t ld_drows,
+                              float* dtopk_w, int32_t* d_status, moe_stream_t stream);
+
+/*
+ * Product of the experts over their rows r in [start[e], psum[e]), from 4-bit
+ * weights with a scale (and a zero point) per `group` contracted values:
+ *   out[r, n] = sum_k x[r, k] scales[e, n, k/group] (q[e, n, k] - z[e, n, k/group])
+ * Sums in fp32, each result rounded once; the weights are never rounded to
+ * 16 bits. Rows outside the segments are neither used nor written. Segments
+ * are read on the device and clamped to [0, M_cap]; they need not be aligned.
+ *   codes    device uint8 [E, N, Kd/2]: q[e, n, 2j] in the low four bits of byte
+ *            j, q[e, n, 2j+1] in the high ones
+ *   scales   device, of dtype, [E, N, Kd/group]; group 32, 64 or 128
+ *   zeros    device uint8 [E, N, Kd/group], values 0 to 15 (only the low four
+ *            bits are used); NULL: 8 everywhere
+ *   x, out   16-bit of dtype, [M_cap, ld >= Kd] and [M_cap, ld >= N]
+ *   max_rows as in moe_grouped_mm
+ * N and the row strides are multiples of 8, Kd a multiple of group, pointers
+ * (zeros apart) 16-byte aligned, E <= 1024.
+ */
+int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* codes, const void* scales,
+                      const uint8_t* zeros, int group, const int32_t* start, const int32_t* psum,
+                      int dtype, int E, int N, int Kd, int64_t M_cap, int64_t max_rows, void* out,
+                      int64_t ld_out, int32_t* d_status, moe_stream_t stream);
 
 /* Host. Diagnostics: when d_trace is not NULL, every later grouped-GEMM
  * launch (moe_grouped_gemm, moe_grouped_gemm_act_quant) writes 8 uint64
