@@ -22,6 +22,10 @@ int make_tmap_rows16(CUtensorMap* tm, const void* base, uint64_t width, uint64_t
                      uint32_t box_rows);
 int make_tmap_weights16(CUtensorMap* tm, const void* base, uint64_t Kd, uint64_t N, uint64_t E,
                         uint32_t box_n);
+// 4-bit weights' codes, [rows, row_bytes] contiguous, in boxes of box_rows rows x
+// 64 bytes (128 values; 64-byte swizzling).
+int make_tmap_codes4(CUtensorMap* tm, const void* base, uint64_t row_bytes, uint64_t rows,
+                     uint32_t box_rows);
 // Results [E, rows, width] with a row stride of `ld` values, 16-bit or fp32,
 // stored in boxes of 32 rows x 64 bytes (64-byte swizzling).
 int make_tmap_result(CUtensorMap* tm, void* base, bool f32, uint64_t width, uint64_t rows, uint64_t E,
@@ -59,6 +63,28 @@ int launch_grouped_mm16_few(bool dgrad, bool half, const void* a, int64_t ld_a, 
                             const int32_t* start, const int32_t* psum, int E, int N, int Kd,
                             int64_t M_cap, int64_t max_rows, uint16_t* out, int64_t ld_out,
                             int32_t* status, cudaStream_t s);
+
+// Arguments of the 4-bit product, already validated.
+struct W4Args {
+  const void* x;
+  int64_t ld_x;
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  int group;
+  const int32_t* start;
+  const int32_t* psum;
+  bool half;
+  int E, N, Kd;
+  int64_t M_cap, max_rows;
+  uint16_t* out;
+  int64_t ld_out;
+  int32_t* status;
+};
+// Its form for chunks of R rows, 8 or 16, with the scales and zero points of 32
+// weight rows in at most kW4FewScaleBytes.
+constexpr int kW4FewScaleBytes = 128 * 1024;
+int launch_grouped_w4_few(const W4Args& a, int R, cudaStream_t s);
 
 // Launches the tcgen05 block-scaled kernel (N % 256 == 0).
 int launch_grouped_gemm_mx(const MxGemmArgs& a, cudaStream_t s);

@@ -1,294 +1,498 @@
 // moe_grouped_mm_w4: the experts' product over 4-bit weights with group scales,
 //   out[r, n] = sum_k x[r, k] s[e, n, k / g] (q[e, n, k] - z[e, n, k / g]),
 // for batches of single tokens, where the time is that of reading the weights.
+// This is the form for more than a dozen rows an expert; grouped_w4_few.cu has
+// the other.
 //
-// D = W X^T on mma.sync (m16n8k16): the weights are the first operand, so that
-// they go from memory to registers and, as integers, into the tensor core with
-// no stop in shared memory; 8 rows of x are the second operand's columns. Which
-// of 128 contracted values stands at which place of the eight instructions is
-// free as long as both operands agree, and is chosen so that a lane reads 16
-// contiguous bytes of codes per weight row and the 8 values of x that go with
-// each word of them. q - z is exact in 16 bits (q is put into the mantissa of
-// 128 or 1024, and 128 + z or 1024 + z taken off); a group's sum is exact
-// products in fp32, and the scale multiplies that sum in fp32, so nothing is
-// rounded but the sums and, once, the result.
+// The weights are the tensor core's first operand, read from tensor memory:
+//   D[i, r] = sum_c W[i, c] X[r, c],
+// a tile being 128 weight rows by kR activation rows (32 or 64) of one expert.
+// TMA brings 128 contracted values at a time, 64 bytes of codes a row and the rows
+// of x; a thread takes one weight row: it makes 64 codes at a time 16-bit values
+// (w4.cuh: exact) and stores them into its lane of tensor memory. Each scale
+// group has sums of its own there, which the thread multiplies by its scale and
+// adds up in fp32 registers. So nothing is rounded but the sums and, once, the
+// result.
 //
-// A block does 64 weight rows by up to 32 rows of one expert; its warps share
-// the weight rows (two) and the contraction (four), whose sums meet in shared
-// memory in a fixed order.
+// Four CTAs of four warps fit an SM. The warps meet at a barrier per 64 values,
+// after which one thread issues the products and refills the ring: with warps of
+// their own for that, which poll for their turn, half of the instructions were
+// polls (4096 x 7168 weights of 64 experts, 32 rows each: 414 us). A CTA makes the
+// next 64 values while its products run, so it rarely finds them unfinished. With
+// few tiles the contraction is split over the CTAs of a cluster, whose partial
+// sums meet in a fixed order through distributed shared memory.
 #include <algorithm>
+#include <atomic>
 
 #include "dtype16.cuh"
 #include "gemm_host.h"
 #include "host_util.h"
+#include "mm16.cuh"
+#include "w4.cuh"
 
 namespace moe {
 namespace {
 
+constexpr int kHalf = 128;               // weight rows of a warpgroup
+constexpr int kI = 2 * kHalf;            // of a tile
+constexpr int BC = 128;                  // contracted per stage
+constexpr int kUmmaK = 16;
+constexpr int kHalfBytes = kHalf * BC / 2;
+constexpr int kCodeBytes = 2 * kHalfBytes;
 constexpr int kThreads = 256;
-constexpr int kMaxE = 1024;
-constexpr int kRows = 32;      // rows of x of a block
-constexpr int kTile = 64;      // weight rows of a block
-constexpr int kSplit = 4;      // warps along the contraction
-constexpr int kMT = 2;         // 16-row tiles of a warp
-constexpr int kBlock = 128;    // contracted per step of a warp
+constexpr int kHalfCols = 128;           // tensor memory: at most 64 of a step's weights, 64 of its sums
+constexpr int kTmemCols = 2 * kHalfCols;
+
+// Contracted values of a step, a batch of products: their sums, of every scale
+// group apart, have 64 columns.
+constexpr int step_k(int group, int R) { return 64 * group / R < 128 ? 64 * group / R : 128; }
+
+constexpr int stage_bytes(int R) { return kCodeBytes + R * BC * 2; }
+constexpr int stages_for(int R) { return 96 * 1024 / stage_bytes(R); }
+constexpr int ring_bytes(int R) { return stages_for(R) * stage_bytes(R) + 1024; }
 
 struct W4Params {
   const int32_t* start;
   const int32_t* psum;
-  const uint16_t* x;
-  int64_t ld_x;
-  const uint8_t* codes;
-  const uint16_t* scales;
-  const uint8_t* zeros;
-  int E, N, Kd, groups;   // groups along Kd
+  const uint2* scales;    // 4 to a vector
+  const uint32_t* zeros;  // 4 to a word, or NULL
+  int E, N;
+  int blocks;             // stages along the contraction
+  int groups;             // scales of a row
+  int splits;             // CTAs of a cluster
   int64_t M_cap;
   uint16_t* out;
   int64_t ld_out;
   int32_t* status;
 };
 
-template <bool Half>
-MOE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (Half)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands, K = 16.
+MOE_DEV void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
-// Nibbles i and i + 4 of a word, less the zero point (already with the offset,
-// twice): two 16-bit values.
-template <bool Half, int i>
-MOE_DEV uint32_t code_pair(uint32_t word, uint32_t off) {
-  const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | (Half ? 0x64006400u : 0x43004300u);
-  if constexpr (Half) {
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&off));
-    return *reinterpret_cast<const uint32_t*>(&d);
-  } else {
-    const __nv_bfloat162 d =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&off));
-    return *reinterpret_cast<const uint32_t*>(&d);
+MOE_DEV void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A row's scales and zero points, four groups at a time, in registers: those
+// four, and the aligned vectors that the next four lie in, asked for in advance.
+// N being a multiple of 8, the tensors are whole vectors.
+struct GroupStream {
+  const uint2* scales;
+  const uint32_t* zeros;
+  int next, last;   // vectors of four, from the row's first one
+  int skew;         // of the first group in its vector
+  uint2 s0, s1;
+  uint32_t z0, z1;
+  uint32_t s[2], z;   // the four
+  MOE_DEV void load() {
+    s1 = __ldg(scales + min(next, last));
+    if (zeros != nullptr) z1 = __ldg(zeros + min(next, last));
   }
+  MOE_DEV void begin(const uint2* sc, const uint32_t* ze, int64_t first, int64_t values) {
+    scales = sc + (first >> 2);
+    zeros = ze != nullptr ? ze + (first >> 2) : nullptr;
+    last = static_cast<int>(min(static_cast<int64_t>(INT32_MAX), values / 4 - 1 - (first >> 2)));
+    skew = static_cast<int>(first) & 3;
+    z = 0x01010101u * kW4Zero;
+    next = 0;
+    load();
+    s0 = s1;
+    z0 = z1;
+    next = 1;
+    load();
+  }
+  MOE_DEV void refill() {
+    const bool up = skew & 2;
+    const uint32_t a = up ? s0.y : s0.x, b = up ? s1.x : s0.y, c = up ? s1.y : s1.x;
+    s[0] = __funnelshift_r(a, b, 16 * (skew & 1));
+    s[1] = __funnelshift_r(b, c, 16 * (skew & 1));
+    if (zeros != nullptr) z = __funnelshift_r(z0, z1, 8 * skew);
+    s0 = s1;
+    z0 = z1;
+    ++next;
+    load();
+  }
+  template <int n>   // n of the four are used up: 1, 2 or 4
+  MOE_DEV void pass() {
+    s[0] = n == 1 ? __funnelshift_r(s[0], s[1], 16) : s[1];
+    s[1] = n == 1 ? s[1] >> 16 : 0u;
+    if (zeros != nullptr && n < 4) z >>= 8 * (n & 3);
+  }
+};
+
+// A value that all lanes hold, so that the compiler knows it: tensor core and TMA
+// instructions take their operands from uniform registers, and where it does not
+// know that they are uniform it loops over the lanes.
+MOE_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// mbar_wait_warp on a barrier given by its shared-memory address: forming the
+// address anew at every wait costs as much as the wait.
+MOE_DEV bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
 }
 
-template <bool Half>
-MOE_DEV float to_f32(uint16_t v) {
-  return unpack2<Half>(v).x;
+// The 128 threads of a warpgroup meet; true if `flag` is so for any.
+MOE_DEV bool meet_or(int group, bool flag) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(flag)), "r"(group + 1)
+      : "memory");
+  return any != 0;
 }
 
-// The contraction of one warp: its share of the steps, kMT x kNT tiles of sums.
-// kGroup values share a scale. Word c of a lane (t = lane % 4) stands for the 8
-// contracted values from offset(c) of a step on.
-template <bool Half, int kGroup, int kNT>
-MOE_DEV void contract(const W4Params& p, int e, int n0, int64_t row0, int rows, int split,
-                      float (&acc)[kMT][kNT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  constexpr int kWide = kGroup / 32;   // words a lane reads at once: 4, 2 or 1
-  const int64_t row_bytes = p.Kd / 2;
-  const uint8_t* w[kMT][2];
-  int64_t sc[kMT][2];
-#pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
+// True in one lane of a converged warp.
+MOE_DEV bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+template <bool Half, int kGroup, int kR>
+__global__ void __launch_bounds__(kThreads, 2)
+    grouped_w4_kernel(const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmX, const W4Params p) {
+  constexpr int kStages = stages_for(kR);
+  constexpr int kStageBytes = stage_bytes(kR);
+  constexpr int kGroups = BC / kGroup;   // of a stage
+  constexpr int kStep = step_k(kGroup, kR);
+  constexpr int kSteps = BC / kStep;     // of a stage: 1 or 2
+  constexpr int kEnds = kStep / kGroup;  // groups of a step
+  constexpr int kACols = kStep / 2;
+  constexpr int kChunks = kStep / 32;    // of 32 values, a 16-byte vector of codes
+  // made before the products of the step before are waited for, as registers allow
+  constexpr int kAhead = kR <= 32 ? 2 : 1;
+  static_assert(kEnds >= 1 && kACols + kEnds * kR <= kHalfCols, "tensor memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[kStages], d_ready[2], done[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_used[kStages];
+  __shared__ int s_warp_sum[kThreads / 32], s_found[3];
+  volatile int* abort_flag = &s_abort;
+  const int warp = uniform(threadIdx.x >> 5);
+  const int splits = p.splits;
+  const int rank = static_cast<int>(blockIdx.x) % splits;
+  const int tile = static_cast<int>(blockIdx.x) / splits;
+  const int ni = (p.N + kI - 1) / kI;
+  const int chunk = tile / ni;
+  const int i0 = (tile - chunk * ni) * kI;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      s_used[s] = 0;
+    }
     for (int h = 0; h < 2; ++h) {
-      const int n = min(n0 + m * 16 + h * 8 + g, p.N - 1);   // past the last: not stored
-      const int64_t row = static_cast<int64_t>(e) * p.N + n;
-      w[m][h] = p.codes + row * row_bytes;
-      sc[m][h] = row * p.groups;
+      mbar_init(&d_ready[h], 1);
+      mbar_init(&done[h], 1);
     }
-  const uint16_t* x[kNT];
-#pragma unroll
-  for (int j = 0; j < kNT; ++j) x[j] = p.x + (row0 + min(j * 8 + g, rows - 1)) * p.ld_x;
-#pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+    s_abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 0) {
+    __syncwarp();
+    tmem_alloc(&s_tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  const int all = w4_find_chunk<kThreads, kR>(p.start, p.psum, p.E, p.M_cap, chunk, s_warp_sum, s_found);
+  // more chunks than the grid has: the caller's bound on the rows was wrong
+  if (blockIdx.x == 0 && threadIdx.x == kThreads - 1 &&
+      static_cast<int64_t>(all) * ni * splits > static_cast<int64_t>(gridDim.x))
+    set_status(p.status, MOE_ERR_DEVICE_CHECK);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int e = uniform(s_found[0]), row0 = uniform(s_found[1]), rows = uniform(s_found[2]);
+  const uint32_t tmem = uniform(s_tmem);
 
-  const int steps = (p.Kd + kBlock - 1) / kBlock;
-  for (int b = split; b < steps; b += kSplit) {
-    const int k0 = b * kBlock;
-    uint32_t word[kMT][2][4];
+  if (e >= 0) {   // the same for the whole cluster
+    const int b0 = p.blocks * rank / splits, b1 = p.blocks * (rank + 1) / splits;
+    constexpr int kBox = kR / 2;                    // rows of x that a copy brings
+    const int boxes = (rows + kBox - 1) / kBox;
+    const uint32_t idesc = idesc_f16(Half, false, false, kHalf, (rows + 15) / 16 * 16);
+    const uint64_t x0 = sw128_kmajor_desc(smem_u32(smem) + kCodeBytes);
+    const bool both = i0 + kHalf < p.N;   // else the second warpgroup has no rows
+    const int half = warp >> 2, row = threadIdx.x & (kHalf - 1);
+    const uint32_t bars = smem_u32(full), d_bar = smem_u32(&d_ready[half]);
+    auto wait = [&](uint32_t bar, uint64_t* at, uint32_t parity) {
+      return try_wait(bar, parity) || mbar_wait_warp(at, parity, abort_flag, p.status);
+    };
+    auto load = [&](int b, int stage) {   // by one lane of warp 1
+      uint8_t* sw = smem + stage * kStageBytes;
+      uint8_t* sx = sw + kCodeBytes;
+      const uint32_t bar = smem_u32(&full[stage]);
+      mbar_arrive_expect_tx(&full[stage], (both ? kCodeBytes : kHalfBytes) + boxes * (kBox * BC * 2));
+      load_2d<1>(sw, &tmW, b * (BC / 2), e * p.N + i0, bar);
+      if (both) load_2d<1>(sw + kHalfBytes, &tmW, b * (BC / 2), e * p.N + i0 + kHalf, bar);
 #pragma unroll
-    for (int m = 0; m < kMT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 4; c += kWide) {
-          const int k = k0 + (c / kWide) * kGroup + t * (8 * kWide);
-          uint32_t* to = &word[m][h][c];
-          const uint8_t* from = w[m][h] + k / 2;
-          if constexpr (kWide == 4) {
-            const uint4 v = k < p.Kd ? __ldcs(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
-            to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
-          } else if constexpr (kWide == 2) {
-            const uint2 v = k < p.Kd ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0, 0);
-            to[0] = v.x, to[1] = v.y;
-          } else {
-            to[0] = k < p.Kd ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0u;
-          }
-        }
-#pragma unroll
-    for (int q = 0; q < kBlock / kGroup; ++q) {
-      const int gi = k0 / kGroup + q;
-      const bool in = gi < p.groups;
-      float s[kMT][2];
-      uint32_t off[kMT][2];
-#pragma unroll
-      for (int m = 0; m < kMT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[m][h] = in ? to_f32<Half>(__ldg(p.scales + sc[m][h] + gi)) : 0.0f;
-          const uint32_t z = p.zeros == nullptr ? 8u : (in ? __ldg(p.zeros + sc[m][h] + gi) & 15u : 0u);
-          off[m][h] = (Half ? 0x64006400u : 0x43004300u) | (z * 0x00010001u);
-        }
-      float part[kMT][kNT][4];
-#pragma unroll
-      for (int m = 0; m < kMT; ++m)
-#pragma unroll
-        for (int j = 0; j < kNT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) part[m][j][i] = 0.0f;
-#pragma unroll
-      for (int cc = 0; cc < kWide; ++cc) {
-        const int c = q * kWide + cc;
-        const int k = k0 + q * kGroup + t * (8 * kWide) + cc * 8;
-        uint4 xv[kNT];
-#pragma unroll
-        for (int j = 0; j < kNT; ++j)
-          xv[j] = k < p.Kd && j * 8 + g < rows ? __ldg(reinterpret_cast<const uint4*>(x[j] + k))
-                                               : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t a[kMT][4];
-#pragma unroll
-          for (int m = 0; m < kMT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              a[m][h] = half == 0 ? code_pair<Half, 0>(word[m][h][c], off[m][h])
-                                  : code_pair<Half, 2>(word[m][h][c], off[m][h]);
-              a[m][2 + h] = half == 0 ? code_pair<Half, 1>(word[m][h][c], off[m][h])
-                                      : code_pair<Half, 3>(word[m][h][c], off[m][h]);
-            }
-#pragma unroll
-          for (int j = 0; j < kNT; ++j) {
-            // (x[i], x[i + 4]) for i = 2 half, 2 half + 1
-            const uint32_t lo = half == 0 ? xv[j].x : xv[j].y, hi = half == 0 ? xv[j].z : xv[j].w;
-            const uint32_t b0 = __byte_perm(lo, hi, 0x5410), b1 = __byte_perm(lo, hi, 0x7632);
-#pragma unroll
-            for (int m = 0; m < kMT; ++m) mma16816<Half>(part[m][j], a[m], b0, b1);
-          }
-        }
+      for (int i = 0; i < 2; ++i) {
+        if (i >= boxes) break;
+        load_2d<1>(sx + i * (kBox * 128), &tmX, b * BC, row0 + i * kBox, bar);
+        load_2d<1>(sx + (kR + i * kBox) * 128, &tmX, b * BC + 64, row0 + i * kBox, bar);
       }
+    };
+    int loaded = min(kStages, b1 - b0);   // stages asked for
+    if (warp == 1 && elect_one())
+      for (int s = 0; s < loaded; ++s) load(b0 + s, s);
+    // Thread t holds weight row i0 + t, a column of `out`. A warpgroup's TMEM
+    // columns: a step's weights, then the chunk's rows, group by group.
+    const int i = i0 + threadIdx.x;
+    const bool i_ok = i < p.N;
+    const uint32_t half_tmem = tmem + half * kHalfCols;
+    const uint32_t my_tmem = half_tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    GroupStream groups;
+    groups.begin(p.scales, p.zeros, (static_cast<int64_t>(e) * p.N + min(i, p.N - 1)) * p.groups + b0 * kGroups,
+                 static_cast<int64_t>(p.E) * p.N * p.groups);
+    float2 acc[kR / 2];
 #pragma unroll
-      for (int m = 0; m < kMT; ++m)
+    for (int r = 0; r < kR / 2; ++r) acc[r] = make_float2(0.0f, 0.0f);
+    // the last step's sums, times their scales
+    float f[kEnds];
+    auto add = [&] {
 #pragma unroll
-        for (int j = 0; j < kNT; ++j)
+      for (int q = 0; q < kEnds; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[m][j][i] = fmaf(s[m][i >> 1], part[m][j][i], acc[m][j][i]);
+        for (int r0 = 0; r0 < kR; r0 += 16) {
+          if (r0 >= rows) break;
+          uint32_t v[16];
+          tc_ld16_wait(my_tmem + kACols + q * kR + r0, v);
+#pragma unroll
+          for (int r = 0; r < 16; r += 2)
+            fma2(acc[(r0 + r) / 2], f[q], __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
+        }
+    };
+    bool got = true, stop = false;
+    int stage = 0, b = b0;
+    uint32_t phase = 0, turn = 0;
+    const uint32_t my_codes = smem_u32(smem) + threadIdx.x * 64, swizzle = ((row >> 1) & 3) << 4;
+    if (half == 1 && !both) b = b1;
+    for (; b < b1 && !stop; ++b) {
+      if ((b - b0) % (4 / kGroups) == 0) groups.refill();
+      got = wait(bars + stage * 8, &full[stage], phase) && got;
+      const uint32_t codes = my_codes + stage * kStageBytes;
+#pragma unroll
+      for (int h = 0; h < kSteps; ++h) {
+        auto values = [&](int c, uint32_t (&v)[16]) {   // of chunk c of the step
+          const int piece = h * kChunks + c;            // of the stage's four
+          uint4 w;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                       : "r"(codes + ((piece << 4) ^ swizzle))
+                       : "memory");
+          const uint32_t o = w4_offset<Half>((groups.z >> (piece * 32 / kGroup * 8)) & 15u);
+          w4_values<Half>(w.x, o, v);
+          w4_values<Half>(w.y, o, v + 4);
+          w4_values<Half>(w.z, o, v + 8);
+          w4_values<Half>(w.w, o, v + 12);
+        };
+        {
+          uint32_t ahead[kAhead][16];
+#pragma unroll
+          for (int c = 0; c < kAhead; ++c) values(c, ahead[c]);
+          if (h > 0 || b > b0) {
+            got = wait(d_bar, &d_ready[half], turn ^ 1u) && got;
+            tc_fence_after();
+            add();
+          }
+#pragma unroll
+          for (int c = 0; c < kAhead; ++c) tc_st16(my_tmem + c * 16, ahead[c]);
+#pragma unroll
+          for (int c = kAhead; c < kChunks; ++c) {
+            uint32_t v[16];
+            values(c, v);
+            tc_st16(my_tmem + c * 16, v);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kEnds; ++q) {   // a group past the contraction has products with zeros
+          const int g = h * kEnds + q;
+          const uint32_t s = g & 1 ? groups.s[g / 2] >> 16 : groups.s[g / 2] & 0xffffu;
+          f[q] = b * kGroups + g < p.groups ? unpack2<Half>(s).x : 0.0f;
+        }
+        tc_wait_st();
+        tc_fence_before();
+        stop = meet_or(half, !got);
+        if (stop) break;
+        if ((warp & 3) == 0 && elect_one()) {
+          tc_fence_after();
+          const uint64_t xs = x0 + static_cast<uint32_t>(stage * (kStageBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < kStep; k += kUmmaK) {
+            const int c = h * kStep + k;   // of the stage
+            tc_mma_f16_ta(half_tmem + kACols + k / kGroup * kR, half_tmem + k / 2,
+                          xs + ((c / 64 * (kR * 128) + c % 64 * 2) >> 4), idesc, k % kGroup != 0 ? 1u : 0u);
+          }
+          tc_commit(&d_ready[half]);
+        }
+        if (h == 0 && b > b0 && b0 + loaded < b1) {
+          // this warpgroup has used up the stage before; the later one fills it
+          if ((warp & 3) == 1 && elect_one()) {
+            const int old = stage == 0 ? kStages - 1 : stage - 1;
+            __threadfence_block();
+            if (!both || atomicAdd(&s_used[old], 1) & 1) load(b0 + loaded, old);
+          }
+          ++loaded;
+        }
+        turn ^= 1u;
+      }
+      groups.pass<kGroups>();
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
     }
+    if (!stop && b1 > b0 && (half == 0 || both)) {
+      stop = !(wait(d_bar, &d_ready[half], turn ^ 1u) && got);
+      tc_fence_after();
+      add();
+      tc_fence_before();
+    }
+    stop = __syncthreads_or(stop);   // the ring is free: every product is done
+    if (stop && row == 0) {
+      // what is under way has landed before the CTA can exit
+      tc_commit(&done[half]);
+      drain_wait(&done[half], 0);
+      for (int s = 0; s < kStages && s < loaded; ++s)
+        drain_wait(&full[s], static_cast<uint32_t>((loaded - 1 - s) / kStages) & 1u);
+    }
+    uint16_t* out = p.out + static_cast<int64_t>(row0) * p.ld_out + i;
+    float* part = reinterpret_cast<float*>(smem);
+    if (!stop) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        if (r >= rows) break;
+        const float v = (r & 1 ? acc[r / 2].y : acc[r / 2].x) * kW4Unit<Half>;
+        if (splits > 1)
+          part[r * kI + threadIdx.x] = v;
+        else if (i_ok)
+          out[r * p.ld_out] = static_cast<uint16_t>(pack2<Half>(v, 0.0f) & 0xffffu);
+      }
+    }
+    if (splits > 1) {
+      cluster_sync();
+      // this CTA's share of the rows: the partials of all CTAs, in order
+      const int ra = rows * rank / splits, rb = rows * (rank + 1) / splits;
+      uint32_t from[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        from[c] = c < splits ? cta_smem(smem, c) + static_cast<uint32_t>(threadIdx.x) * 4 : 0;
+      for (int r = ra; r < rb; ++r) {
+        float v[8], sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < splits)
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(v[c])
+                         : "r"(from[c] + static_cast<uint32_t>(r * kI * 4)));
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < splits) sum += v[c];
+        if (i_ok && !stop) out[r * p.ld_out] = static_cast<uint16_t>(pack2<Half>(sum, 0.0f) & 0xffffu);
+      }
+      cluster_sync();   // no CTA leaves while its partials are read
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    __syncwarp();
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-template <bool Half, int kGroup, int kNT>
-MOE_DEV void tile(const W4Params& p, int e, int i0, int64_t row0, int rows, float* sums) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int split = warp % kSplit, part = warp / kSplit;
-  float acc[kMT][kNT][4];
-  contract<Half, kGroup, kNT>(p, e, i0 + part * kMT * 16, row0, rows, split, acc);
-  // sums[split][row][weight row]
-#pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sums[(split * kRows + j * 8 + t * 2 + (i & 1)) * kTile + part * kMT * 16 + m * 16 + (i >> 1) * 8 + g] =
-            acc[m][j][i];
-  __syncthreads();
-  for (int v = threadIdx.x; v < rows * (kTile / 8); v += kThreads) {
-    const int r = v / (kTile / 8), n = v % (kTile / 8) * 8;
-    if (i0 + n >= p.N) continue;
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[i] = sums[r * kTile + n + i];
-#pragma unroll
-      for (int s = 1; s < kSplit; ++s) f[i] += sums[(s * kRows + r) * kTile + n + i];
-    }
-    *reinterpret_cast<uint4*>(p.out + (row0 + r) * p.ld_out + i0 + n) = pack8<Half>(f);
+template <bool Half, int kGroup, int kR>
+int launch(const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int64_t tiles, cudaStream_t s) {
+  auto* kernel = grouped_w4_kernel<Half, kGroup, kR>;
+  constexpr int kSmem = ring_bytes(kR);
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+      return check_launch("cudaFuncSetAttribute(grouped_w4_kernel)");
+    if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(p.splits);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
+  return check_launch("grouped_w4_kernel");
 }
 
 template <bool Half, int kGroup>
-__global__ void __launch_bounds__(kThreads, 2) grouped_w4_kernel(const W4Params p) {
-  __shared__ float s_sums[kSplit * kRows * kTile];
-  __shared__ int s_warp_sum[kThreads / 32];
-  __shared__ int s_e, s_row, s_rows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ni = (p.N + kTile - 1) / kTile;
-  const int chunk = static_cast<int>(blockIdx.x) / ni;
-  const int i0 = (static_cast<int>(blockIdx.x) - chunk * ni) * kTile;
-  // Which expert has chunk number `chunk`? Thread i counts the chunks of experts
-  // per i .. per i + per - 1; segments are clamped into the buffer.
-  constexpr int kPer = kMaxE / kThreads;
-  const int per = (p.E + kThreads - 1) / kThreads;
-  if (threadIdx.x == 0) s_e = -1;
-  int a[kPer], n[kPer], mine = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = threadIdx.x * per + j;
-    a[j] = n[j] = 0;
-    if (j < per && e < p.E) {
-      const int cap = static_cast<int>(p.M_cap);
-      a[j] = min(max(p.start[e], 0), cap);
-      n[j] = min(max(p.psum[e], a[j]), cap) - a[j];
-      mine += (n[j] + kRows - 1) / kRows;
-    }
-  }
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) s_warp_sum[warp] = incl;
-  __syncthreads();
-  int base = incl - mine;
-  for (int w = 0; w < warp; ++w) base += s_warp_sum[w];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int c = (n[j] + kRows - 1) / kRows;
-    if (chunk >= base && chunk < base + c) {
-      s_e = threadIdx.x * per + j;
-      s_row = a[j] + (chunk - base) * kRows;
-      s_rows = min(kRows, n[j] - (chunk - base) * kRows);
-    }
-    base += c;
-  }
-  // more chunks than the grid has: the caller's bound on the rows was wrong
-  if (blockIdx.x == 0 && threadIdx.x == kThreads - 1 &&
-      static_cast<int64_t>(base) * ni > static_cast<int64_t>(gridDim.x))
-    set_status(p.status, MOE_ERR_DEVICE_CHECK);
-  __syncthreads();
-  const int e = s_e, rows = s_rows;
-  if (e < 0) return;
-  if (rows <= 8)
-    tile<Half, kGroup, 1>(p, e, i0, s_row, rows, s_sums);
-  else if (rows <= 16)
-    tile<Half, kGroup, 2>(p, e, i0, s_row, rows, s_sums);
-  else
-    tile<Half, kGroup, 4>(p, e, i0, s_row, rows, s_sums);
+int launch_rows(int R, const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int64_t tiles,
+                cudaStream_t s) {
+  if constexpr (kGroup > 32)
+    if (R > 32) return launch<Half, kGroup, 64>(tw, tx, p, tiles, s);
+  return launch<Half, kGroup, 32>(tw, tx, p, tiles, s);
+}
+
+int launch_grouped_w4_many(const W4Args& a, int R, cudaStream_t s) {
+  W4Params p;
+  p.start = a.start;
+  p.psum = a.psum;
+  p.scales = static_cast<const uint2*>(a.scales);
+  p.zeros = reinterpret_cast<const uint32_t*>(a.zeros);
+  p.E = a.E;
+  p.N = a.N;
+  p.blocks = (a.Kd + BC - 1) / BC;
+  p.groups = a.Kd / a.group;
+  p.M_cap = a.M_cap;
+  p.out = a.out;
+  p.ld_out = a.ld_out;
+  p.status = a.status;
+  const int64_t live = std::min<int64_t>(a.E, a.max_rows), ni = (a.N + kI - 1) / kI;
+  const int64_t want = 2 * device_sm_count();
+  p.splits = 1;
+  while (p.splits < 8 && live * ni * p.splits < want && p.blocks / (2 * p.splits) >= 4) p.splits *= 2;
+  const int64_t tiles = (a.max_rows / R + live) * ni;
+  MOE_REQUIRE(tiles * p.splits <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
+  CUtensorMap tw, tx;
+  int rc = make_tmap_codes4(&tw, a.codes, a.Kd / 2, static_cast<uint64_t>(a.E) * a.N, kHalf);
+  if (rc != MOE_OK) return rc;
+  rc = make_tmap_rows16(&tx, a.x, a.Kd, a.M_cap, a.ld_x, R / 2);
+  if (rc != MOE_OK) return rc;
+  auto* launch = a.group == 128  ? (a.half ? launch_rows<true, 128> : launch_rows<false, 128>)
+                 : a.group == 64 ? (a.half ? launch_rows<true, 64> : launch_rows<false, 64>)
+                                 : (a.half ? launch_rows<true, 32> : launch_rows<false, 32>);
+  return launch(R, tw, tx, p, tiles, s);
 }
 
 }  // namespace
@@ -301,7 +505,7 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
                                  moe_stream_t stream) {
   MOE_REQUIRE(start && psum, "moe_grouped_mm_w4: null segments");
   MOE_REQUIRE(dtype == MOE_BF16 || dtype == MOE_F16, "moe_grouped_mm_w4: dtype must be MOE_BF16 or MOE_F16");
-  MOE_REQUIRE(E > 0 && E <= moe::kMaxE, "moe_grouped_mm_w4: E must be in [1, 1024]");
+  MOE_REQUIRE(E > 0 && E <= moe::kW4MaxE, "moe_grouped_mm_w4: E must be in [1, 1024]");
   MOE_REQUIRE(group == 32 || group == 64 || group == 128, "moe_grouped_mm_w4: group must be 32, 64 or 128");
   MOE_REQUIRE(N > 0 && N % 8 == 0 && Kd > 0 && Kd % group == 0,
               "moe_grouped_mm_w4: N must be a positive multiple of 8, Kd of the group");
@@ -311,33 +515,21 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
   MOE_REQUIRE(ld_x >= Kd && ld_out >= N && ld_x % 8 == 0 && ld_out % 8 == 0,
               "moe_grouped_mm_w4: a row stride must be a multiple of 8, at least the row");
   MOE_REQUIRE(moe::aligned(x, 16) && moe::aligned(codes, 16) && moe::aligned(out, 16) &&
-                  moe::aligned(scales, 16),
-              "moe_grouped_mm_w4: x, codes, scales and out must be 16-byte aligned");
+                  moe::aligned(scales, 16) && moe::aligned(zeros, 8),
+              "moe_grouped_mm_w4: x, codes, scales and out must be 16-byte aligned, zeros 8-byte");
+  MOE_REQUIRE(static_cast<int64_t>(E) * N <= INT32_MAX, "moe_grouped_mm_w4: E N exceeds 32 bits");
   const int64_t live = std::min<int64_t>(E, max_rows);
-  const int64_t tiles = (max_rows / moe::kRows + live) * ((N + moe::kTile - 1) / moe::kTile);
-  MOE_REQUIRE(tiles <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
+  const int64_t mean = live > 0 ? (max_rows + live - 1) / live : 0;
+  MOE_REQUIRE((max_rows / 8 + live) * ((N + 31) / 32) <= INT32_MAX,
+              "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
   MOE_REQUIRE_DEVICE();
   if (max_rows == 0) return MOE_OK;
-  moe::W4Params p;
-  p.start = start;
-  p.psum = psum;
-  p.x = static_cast<const uint16_t*>(x);
-  p.ld_x = ld_x;
-  p.codes = codes;
-  p.scales = static_cast<const uint16_t*>(scales);
-  p.zeros = zeros;
-  p.E = E;
-  p.N = N;
-  p.Kd = Kd;
-  p.groups = Kd / group;
-  p.M_cap = M_cap;
-  p.out = static_cast<uint16_t*>(out);
-  p.ld_out = ld_out;
-  p.status = d_status;
-  const bool half = dtype == MOE_F16;
-  auto* kernel = group == 128  ? (half ? moe::grouped_w4_kernel<true, 128> : moe::grouped_w4_kernel<false, 128>)
-                 : group == 64 ? (half ? moe::grouped_w4_kernel<true, 64> : moe::grouped_w4_kernel<false, 64>)
-                               : (half ? moe::grouped_w4_kernel<true, 32> : moe::grouped_w4_kernel<false, 32>);
-  kernel<<<static_cast<unsigned>(tiles), moe::kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return moe::check_launch("grouped_w4_kernel");
+  const moe::W4Args a = {x,  ld_x, codes, scales,   zeros, group,
+                         start, psum, dtype == MOE_F16, E, N, Kd, M_cap, max_rows,
+                         static_cast<uint16_t*>(out), ld_out, d_status};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t scale_bytes = 32ll * (Kd / group) * 3;
+  if (mean <= 12 && scale_bytes <= moe::kW4FewScaleBytes)
+    return moe::launch_grouped_w4_few(a, mean <= 4 ? 8 : 16, s);
+  return moe::launch_grouped_w4_many(a, mean <= 16 || group == 32 ? 32 : 64, s);
 }

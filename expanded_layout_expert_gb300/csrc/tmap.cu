@@ -76,6 +76,28 @@ int make_tmap_result(CUtensorMap* tm, void* base, bool f32, uint64_t width, uint
                      CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+int make_tmap_codes4(CUtensorMap* tm, const void* base, uint64_t row_bytes, uint64_t rows,
+                     uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) {
+    set_error("cuTensorMapEncodeTiled is not available from the driver");
+    return MOE_ERR_CUDA;
+  }
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {64u, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
 int make_tmap_k128(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t stride, uint32_t box_outer) {
   EncodeTiledFn enc = encode_fn();
