@@ -6,6 +6,8 @@
 //
 // Bytes: a row's 2H per pair, read (and, in the gradient, written), and 2H per
 // token: both are bound by HBM.
+#include <algorithm>
+
 #include "dtype16.cuh"
 #include "host_util.h"
 
@@ -23,24 +25,26 @@ MOE_DEV int64_t valid_rows(const int32_t* d_n_valid, int64_t T) {
   return nv < 0 ? 0 : (nv > T ? T : nv);
 }
 
-// A warp takes a token's 256 columns: lane k holds pair k's row and weight, each
-// lane one 16-byte vector of the columns, four rows' loads before their sum.
+// `parts` warps take a token, each a share of its columns, a 16-byte vector a lane
+// at a time; lane k holds pair k's row and weight, and the vectors of kDeep rows
+// are asked for before their sum.
+constexpr int kDeep = 4;
+constexpr int kCombineThreads = 128;
+
 template <bool Half>
-__global__ void __launch_bounds__(kThreads) combine_rows_kernel(
+__global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(
     const uint16_t* __restrict__ rows, int64_t ld_rows, const float* __restrict__ topk_w,
     const int32_t* __restrict__ src2dst, const int32_t* __restrict__ d_n_valid, int64_t T, int nvec,
     int K, int64_t M_cap, const uint16_t* residual, int64_t ld_res, uint16_t* y, int64_t ld_y,
-    int32_t* __restrict__ status) {
+    int parts, int32_t* __restrict__ status) {
   const int lane = threadIdx.x & 31;
-  const int nchunk = (nvec + 31) / 32;
-  const int64_t tasks = valid_rows(d_n_valid, T) * nchunk;
-  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * kThreads) >> 5;
-  for (int64_t task = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; task < tasks;
+  const int64_t tasks = valid_rows(d_n_valid, T) * parts;
+  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * kCombineThreads) >> 5;
+  for (int64_t task = (static_cast<int64_t>(blockIdx.x) * kCombineThreads + threadIdx.x) >> 5; task < tasks;
        task += nwarps) {
-    const int64_t t = task <= UINT32_MAX ? static_cast<uint32_t>(task) / static_cast<uint32_t>(nchunk)
-                                         : task / nchunk;
-    const int v = static_cast<int>(task - t * nchunk) * 32 + lane;
-    const bool act = v < nvec;
+    const int64_t t = task <= UINT32_MAX ? static_cast<uint32_t>(task) / static_cast<uint32_t>(parts)
+                                         : task / parts;
+    const int part = static_cast<int>(task - t * parts);
     int my = -1;
     float my_w = 1.0f;
     if (lane < K) {
@@ -51,32 +55,37 @@ __global__ void __launch_bounds__(kThreads) combine_rows_kernel(
       }
       if (topk_w != nullptr) my_w = topk_w[t * K + lane];
     }
-    float a[8];
+    // warp-uniform (the shuffles need every lane); lanes past the row idle
+    for (int v0 = part * 32; v0 < nvec; v0 += parts * 32) {
+      const int v = v0 + lane;
+      const bool act = v < nvec;
+      float a[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = 0.0f;
-    if (residual != nullptr && act) unpack8<Half>(reinterpret_cast<const uint4*>(residual + t * ld_res)[v], a);
-    for (int k0 = 0; k0 < K; k0 += 4) {
-      uint4 d[4];
-      int r[4];
-      float w[4];
+      for (int i = 0; i < 8; ++i) a[i] = 0.0f;
+      if (residual != nullptr && act) unpack8<Half>(reinterpret_cast<const uint4*>(residual + t * ld_res)[v], a);
+      for (int k0 = 0; k0 < K; k0 += kDeep) {
+        uint4 d[kDeep];
+        int r[kDeep];
+        float w[kDeep];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r[j] = __shfl_sync(kAll, my, (k0 + j) & 31);
-        w[j] = __shfl_sync(kAll, my_w, (k0 + j) & 31);
-        if (k0 + j >= K || !act) r[j] = -1;
-        d[j] = make_uint4(0, 0, 0, 0);
-        if (r[j] >= 0) d[j] = __ldcs(reinterpret_cast<const uint4*>(rows + r[j] * ld_rows) + v);
+        for (int j = 0; j < kDeep; ++j) {
+          r[j] = __shfl_sync(kAll, my, (k0 + j) & 31);
+          w[j] = __shfl_sync(kAll, my_w, (k0 + j) & 31);
+          if (k0 + j >= K || !act) r[j] = -1;
+          d[j] = make_uint4(0, 0, 0, 0);
+          if (r[j] >= 0) d[j] = __ldcs(reinterpret_cast<const uint4*>(rows + r[j] * ld_rows) + v);
+        }
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+          if (r[j] < 0) w[j] = 0.0f;   // zeros times this; a branch would wait for each row apart
+          float f[8];
+          unpack8<Half>(d[j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = fmaf(f[i], w[j], a[i]);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (r[j] < 0) continue;
-        float f[8];
-        unpack8<Half>(d[j], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = fmaf(f[i], w[j], a[i]);
-      }
+      if (act) reinterpret_cast<uint4*>(y + t * ld_y)[v] = pack8<Half>(a);
     }
-    if (act) reinterpret_cast<uint4*>(y + t * ld_y)[v] = pack8<Half>(a);
   }
 }
 
@@ -173,6 +182,13 @@ __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
   }
 }
 
+// A warp for each token where there are tokens for every warp that fits, or a warp
+// holds a row at once; else a block.
+bool many_tokens(int64_t T, int nvec) {
+  return T >= static_cast<int64_t>(device_sm_count()) * 32 || nvec <= 32;
+}
+constexpr int kCombineBlocks = 64;
+
 }  // namespace
 }  // namespace moe
 
@@ -194,14 +210,18 @@ extern "C" int moe_combine_rows(const void* rows, int64_t ld_rows, int dtype, co
               "moe_combine_rows: in place needs the same row stride for residual and out");
   MOE_REQUIRE_DEVICE();
   if (T == 0) return MOE_OK;
-  int64_t grid = static_cast<int64_t>(moe::device_sm_count()) * (2048 / moe::kThreads);
-  const int64_t tasks = T * ((H / 8 + 31) / 32);
-  const int64_t need = (tasks + (moe::kThreads / 32) - 1) / (moe::kThreads / 32);
-  if (grid > need) grid = need;
+  // warps for a token: one where there are tokens for every warp that fits, up to
+  // one for every 32 vectors where there are few
+  const int chunks = (H / 8 + 31) / 32;
+  const int64_t fit = static_cast<int64_t>(moe::device_sm_count()) * 48;
+  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, fit / T)));
+  const int64_t need = (T * parts + moe::kCombineThreads / 32 - 1) / (moe::kCombineThreads / 32);
+  const int64_t most = static_cast<int64_t>(moe::device_sm_count()) * moe::kCombineBlocks;
+  const int64_t grid = need < most ? need : most;
   auto* kernel = dtype == MOE_F16 ? moe::combine_rows_kernel<true> : moe::combine_rows_kernel<false>;
-  kernel<<<static_cast<unsigned>(grid), moe::kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  kernel<<<static_cast<unsigned>(grid), moe::kCombineThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       static_cast<const uint16_t*>(rows), ld_rows, topk_w, src2dst, d_n_valid, T, H / 8, K, M_cap,
-      static_cast<const uint16_t*>(residual), ld_res, static_cast<uint16_t*>(out), ld_out, d_status);
+      static_cast<const uint16_t*>(residual), ld_res, static_cast<uint16_t*>(out), ld_out, parts, d_status);
   return moe::check_launch("combine_rows_kernel");
 }
 
@@ -231,7 +251,7 @@ extern "C" int moe_combine_rows_backward(const void* dy, int64_t ld_dy, const vo
   MOE_REQUIRE_DEVICE();
   const int nvec = H / 8;
   const int64_t most = static_cast<int64_t>(moe::device_sm_count()) * (2048 / moe::kThreads) * 8;
-  const bool many = T >= static_cast<int64_t>(moe::device_sm_count()) * 32 || nvec <= 32;
+  const bool many = moe::many_tokens(T, nvec);
   const int64_t need = many ? (T + moe::kThreads / 32 - 1) / (moe::kThreads / 32) : T;
   const int64_t blocks = need < most ? need : most;
   if (pad + blocks == 0) return MOE_OK;

@@ -81,10 +81,10 @@ struct W4Args {
   int64_t ld_out;
   int32_t* status;
 };
-// Its form for chunks of R rows, 8 or 16, with the scales and zero points of 32
-// weight rows in at most kW4FewScaleBytes.
+// Its form for chunks of 8 rows, with the scales and zero points of 32 weight
+// rows in at most kW4FewScaleBytes.
 constexpr int kW4FewScaleBytes = 128 * 1024;
-int launch_grouped_w4_few(const W4Args& a, int R, cudaStream_t s);
+int launch_grouped_w4_few(const W4Args& a, cudaStream_t s);
 
 // Launches the tcgen05 block-scaled kernel (N % 256 == 0).
 int launch_grouped_gemm_mx(const MxGemmArgs& a, cudaStream_t s);

@@ -528,8 +528,18 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
                          start, psum, dtype == MOE_F16, E, N, Kd, M_cap, max_rows,
                          static_cast<uint16_t*>(out), ld_out, d_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // Which form, by the mean rows of an expert with rows and the weights read.
+  // Up to four rows mma.sync is the faster (64 experts of 2048 x 4096: 41, 54 and
+  // 64 us for 1, 2 and 4 rows, here 57, 68 and 78), from eight on this form (86 and
+  // 79); with fewer weights its few large tiles leave SMs idle longer: 8 experts
+  // of 4096 x 4096 take 27 us there and 31 here with 8 rows, 41 and 33 with 16; of
+  // 1024 x 1024 5.2 and 9.0 with 8, 9.4 and 11.5 with 32.
+  const int64_t weights = live * N * Kd;
   const int64_t scale_bytes = 32ll * (Kd / group) * 3;
-  if (mean <= 12 && scale_bytes <= moe::kW4FewScaleBytes)
-    return moe::launch_grouped_w4_few(a, mean <= 4 ? 8 : 16, s);
+  if ((mean <= 4 || (mean <= 8 && weights <= (1ll << 27)) || (mean <= 32 && weights <= (1ll << 23))) &&
+      scale_bytes <= moe::kW4FewScaleBytes)
+    return moe::launch_grouped_w4_few(a, s);
+  // Rows of a tile: 16 rows an expert (64 of 4096 x 7168) take 231 us with 32, 239
+  // with 64; 32 rows 316 and 249.
   return moe::launch_grouped_w4_many(a, mean <= 16 || group == 32 ? 32 : 64, s);
 }

@@ -1,4 +1,4 @@
-// The 4-bit product of grouped_w4.cu for chunks of at most 16 rows: an expert's
+// The 4-bit product of grouped_w4.cu for chunks of at most 8 rows: an expert's
 // few single tokens, or one.
 //
 // D = W X^T on mma.sync (m16n8k16), the weights as the first operand: from
@@ -9,11 +9,15 @@
 // codes, and the 16 bytes of x that go with them. A group's sums are exact
 // products in fp32; the scale multiplies that sum in fp32.
 //
-// Bound by HBM (the weights' bytes) up to 16 rows; mma.sync has a quarter of
-// tcgen05's rate, which no longer suffices beyond. A block of four warps does 32
+// mma.sync has a quarter of tcgen05's rate, enough for 8 rows at HBM's. What
+// bounds the kernel is the making of the values, ten instructions for eight, six
+// of them on the pipe with half a warp a cycle: one token of 8 out of 64 experts
+// of 4096 x 7168 takes 27.5 us (4.4 TB/s of codes and scales; 22.5 without the
+// copies, 24.4 with the codes taken as they are). A block of four warps does 32
 // weight rows by one expert's chunk; the warps take every fourth 128 contracted
 // values and meet once, at the end, in shared memory in a fixed order. Blocks
-// are small so that those of a single token all fit the GPU at once.
+// are small so that those of a single token all fit the GPU at once (with six
+// to an SM instead of seven 30 us).
 #include <algorithm>
 #include <atomic>
 
@@ -27,6 +31,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;        // weight rows
+constexpr int kRows = 8;         // of x: the columns of an instruction's second operand
 constexpr int kBlock = 128;      // contracted per step of a warp
 constexpr int kStages = 3;
 constexpr int kSlot = kTile * kBlock / 2;             // bytes of a warp's step
@@ -81,8 +86,8 @@ MOE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32
           "f"(c[3]));
 }
 
-template <bool Half, int kGroup, int kNT, bool kZeros>
-__global__ void __launch_bounds__(kThreads, kNT == 1 ? 7 : 4) grouped_w4_few_kernel(const FewParams p) {
+template <bool Half, int kGroup, bool kZeros>
+__global__ void __launch_bounds__(kThreads, 7) grouped_w4_few_kernel(const FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];   // ring, then the tile's scales and zero points
   __shared__ int s_warp_sum[kWarps], s_found[3];
   constexpr int kWide = kGroup / 32;   // words of a lane that share a group: 4, 2 or 1
@@ -92,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 7 : 4) grouped_w4_few_ker
   const int ni = (p.N + kTile - 1) / kTile;
   const int chunk = static_cast<int>(blockIdx.x) / ni;
   const int i0 = (static_cast<int>(blockIdx.x) - chunk * ni) * kTile;
-  const int all = w4_find_chunk<kThreads, 8 * kNT>(p.start, p.psum, p.E, p.M_cap, chunk, s_warp_sum, s_found);
+  const int all = w4_find_chunk<kThreads, kRows>(p.start, p.psum, p.E, p.M_cap, chunk, s_warp_sum, s_found);
   // more chunks than the grid has: the caller's bound on the rows was wrong
   if (blockIdx.x == 0 && threadIdx.x == kThreads - 1 &&
       static_cast<int64_t>(all) * ni > static_cast<int64_t>(gridDim.x))
@@ -142,26 +147,20 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 7 : 4) grouped_w4_few_ker
 
   // Columns past the chunk's rows repeat its last row, and are not stored; the
   // steps past the last repeat it, and are not used.
-  const uint16_t* x[kNT];
-#pragma unroll
-  for (int j = 0; j < kNT; ++j) x[j] = p.x + (row0 + min(j * 8 + g, rows - 1)) * p.ld_x + t * (8 * kWide);
-  auto load_x = [&](int j, int b, int c) {
+  const uint16_t* x = p.x + (row0 + min(g, rows - 1)) * p.ld_x + t * (8 * kWide);
+  auto load_x = [&](int b, int c) {
     const int k = b * kBlock + (c / kWide) * kGroup + (c % kWide) * 8;
-    return !kRagged || k + t * (8 * kWide) < p.Kd ? __ldg(reinterpret_cast<const uint4*>(x[j] + k))
+    return !kRagged || k + t * (8 * kWide) < p.Kd ? __ldg(reinterpret_cast<const uint4*>(x + k))
                                                   : make_uint4(0, 0, 0, 0);
   };
-  uint4 xv[kNT][4];
+  uint4 xv[4];
 #pragma unroll
-  for (int j = 0; j < kNT; ++j)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) xv[j][c] = load_x(j, min(warp, steps - 1), c);
-  float2 acc[2][kNT][2];   // of weight rows g and g + 8
+  for (int c = 0; c < 4; ++c) xv[c] = load_x(min(warp, steps - 1), c);
+  float2 acc[2][2];   // of weight rows g and g + 8, of 16 m + that
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) acc[m][j][h] = make_float2(0.0f, 0.0f);
+    for (int h = 0; h < 2; ++h) acc[m][h] = make_float2(0.0f, 0.0f);
   // rows g, g + 8, g + 16 and g + 24 in the scales and zero points
   int at[4];
 #pragma unroll
@@ -201,27 +200,25 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 7 : 4) grouped_w4_few_ker
             word[h][0] = *reinterpret_cast<const uint32_t*>(c + ((q ^ swizzle) << 4) + t * 4);
           }
         }
-        float part[kNT][4];
+        float part[4];
 #pragma unroll
         for (int c = 0; c < kWide; ++c) {
-          uint32_t lo[4], hi[4];   // rows g and g + 8
-          w4_values<Half>(word[0][c], off[0], lo);
-          w4_values<Half>(word[1][c], off[1], hi);
-#pragma unroll
-          for (int j = 0; j < kNT; ++j) {
-            const uint4 v = xv[j][q * kWide + c];
-            if (c == 0)
-              mma16816<Half, true>(part[j], {lo[0], hi[0], lo[1], hi[1]}, v.x, v.y);
-            else
-              mma16816<Half, false>(part[j], {lo[0], hi[0], lo[1], hi[1]}, v.x, v.y);
-            mma16816<Half, false>(part[j], {lo[2], hi[2], lo[3], hi[3]}, v.z, v.w);
-            if (m == 1) xv[j][q * kWide + c] = load_x(j, b_next, q * kWide + c);
-          }
+          const uint32_t l0 = word[0][c] & 0x0f0f0f0fu, h0 = word[0][c] & 0xf0f0f0f0u;   // row g
+          const uint32_t l1 = word[1][c] & 0x0f0f0f0fu, h1 = word[1][c] & 0xf0f0f0f0u;   // row g + 8
+          const uint4 v = xv[q * kWide + c];
+          const uint32_t a[4] = {w4_pair<Half, 0>(l0, h0, off[0]), w4_pair<Half, 0>(l1, h1, off[1]),
+                                 w4_pair<Half, 1>(l0, h0, off[0]), w4_pair<Half, 1>(l1, h1, off[1])};
+          if (c == 0)
+            mma16816<Half, true>(part, a, v.x, v.y);
+          else
+            mma16816<Half, false>(part, a, v.x, v.y);
+          const uint32_t a2[4] = {w4_pair<Half, 2>(l0, h0, off[0]), w4_pair<Half, 2>(l1, h1, off[1]),
+                                  w4_pair<Half, 3>(l0, h0, off[0]), w4_pair<Half, 3>(l1, h1, off[1])};
+          mma16816<Half, false>(part, a2, v.z, v.w);
+          if (m == 1) xv[q * kWide + c] = load_x(b_next, q * kWide + c);
         }
 #pragma unroll
-        for (int j = 0; j < kNT; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) fma2(acc[m][j][h], s[h], part[j][2 * h], part[j][2 * h + 1]);
+        for (int h = 0; h < 2; ++h) fma2(acc[m][h], s[h], part[2 * h], part[2 * h + 1]);
       }
     }
     if (++slot == kStages) slot = 0;
@@ -234,11 +231,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 7 : 4) grouped_w4_few_ker
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sums[(warp * 8 * kNT + j * 8 + t * 2 + (i & 1)) * kLd + m * 16 + (i >> 1) * 8 + g] =
-            i & 1 ? acc[m][j][i >> 1].y : acc[m][j][i >> 1].x;
+    for (int i = 0; i < 4; ++i)
+      sums[(warp * kRows + t * 2 + (i & 1)) * kLd + m * 16 + (i >> 1) * 8 + g] =
+          i & 1 ? acc[m][i >> 1].y : acc[m][i >> 1].x;
   __syncthreads();
   for (int v = threadIdx.x; v < rows * (kTile / 2); v += kThreads) {
     const int r = v / (kTile / 2), n = v % (kTile / 2) * 2;
@@ -246,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 7 : 4) grouped_w4_few_ker
     float2 f = *reinterpret_cast<const float2*>(sums + r * kLd + n);
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
-      const float2 o = *reinterpret_cast<const float2*>(sums + (w * 8 * kNT + r) * kLd + n);
+      const float2 o = *reinterpret_cast<const float2*>(sums + (w * kRows + r) * kLd + n);
       f.x += o.x;
       f.y += o.y;
     }
@@ -255,9 +250,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 7 : 4) grouped_w4_few_ker
   }
 }
 
-template <bool Half, int kGroup, int kNT, bool kZeros>
+template <bool Half, int kGroup, bool kZeros>
 int launch(const FewParams& p, int64_t tiles, size_t bytes, cudaStream_t s) {
-  auto* kernel = grouped_w4_few_kernel<Half, kGroup, kNT, kZeros>;
+  auto* kernel = grouped_w4_few_kernel<Half, kGroup, kZeros>;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -272,17 +267,14 @@ int launch(const FewParams& p, int64_t tiles, size_t bytes, cudaStream_t s) {
 }
 
 template <bool Half, int kGroup>
-int launch_rows(int R, const FewParams& p, int64_t tiles, size_t bytes, cudaStream_t s) {
-  if (p.zeros != nullptr)
-    return R <= 8 ? launch<Half, kGroup, 1, true>(p, tiles, bytes, s)
-                  : launch<Half, kGroup, 2, true>(p, tiles, bytes, s);
-  return R <= 8 ? launch<Half, kGroup, 1, false>(p, tiles, bytes, s)
-                : launch<Half, kGroup, 2, false>(p, tiles, bytes, s);
+int launch_zeros(const FewParams& p, int64_t tiles, size_t bytes, cudaStream_t s) {
+  return p.zeros != nullptr ? launch<Half, kGroup, true>(p, tiles, bytes, s)
+                            : launch<Half, kGroup, false>(p, tiles, bytes, s);
 }
 
 }  // namespace
 
-int launch_grouped_w4_few(const W4Args& a, int R, cudaStream_t s) {
+int launch_grouped_w4_few(const W4Args& a, cudaStream_t s) {
   FewParams p;
   p.start = a.start;
   p.psum = a.psum;
@@ -300,13 +292,13 @@ int launch_grouped_w4_few(const W4Args& a, int R, cudaStream_t s) {
   p.ld_out = a.ld_out;
   p.status = a.status;
   const int64_t tiles =
-      (a.max_rows / R + std::min<int64_t>(a.E, a.max_rows)) * ((a.N + kTile - 1) / kTile);
+      (a.max_rows / kRows + std::min<int64_t>(a.E, a.max_rows)) * ((a.N + kTile - 1) / kTile);
   MOE_REQUIRE(tiles <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
   const size_t bytes = kRing + static_cast<size_t>(kTile) * p.groups * (a.zeros != nullptr ? 3 : 2);
-  auto* launch = a.group == 128  ? (a.half ? launch_rows<true, 128> : launch_rows<false, 128>)
-                 : a.group == 64 ? (a.half ? launch_rows<true, 64> : launch_rows<false, 64>)
-                                 : (a.half ? launch_rows<true, 32> : launch_rows<false, 32>);
-  return launch(R, p, tiles, bytes, s);
+  auto* launch = a.group == 128  ? (a.half ? launch_zeros<true, 128> : launch_zeros<false, 128>)
+                 : a.group == 64 ? (a.half ? launch_zeros<true, 64> : launch_zeros<false, 64>)
+                                 : (a.half ? launch_zeros<true, 32> : launch_zeros<false, 32>);
+  return launch(p, tiles, bytes, s);
 }
 
 }  // namespace moe
