@@ -19,13 +19,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import expanded_layout_expert_gb300 as mx  # noqa: E402
 
 
-def route(x, router, K):
-    """Top-k experts per token and their softmax weights."""
-    probs = (x.float() @ router).softmax(dim=1)
-    w, ids = probs.topk(K, dim=1)
-    return ids.to(torch.int32).contiguous(), w.contiguous()
-
-
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
@@ -54,7 +47,7 @@ def main(argv=None):
     batches = []
     for _ in range(2):
         x = normal(T, H, std=1.0).bfloat16()
-        ids, w = route(x, router, K)
+        ids, w = mx.route_topk(x.float() @ router, K)
         batches.append((x, ids, w, teacher.forward(x, ids, w).float()))
     losses = []
     for step in range(a.steps):

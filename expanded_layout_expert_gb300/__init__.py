@@ -7,7 +7,9 @@ CUDA kernels. Results and workspaces that a call makes itself are made on the
 stream it is queued on. ``ExpandedMoELayer`` strings the calls together with
 buffers allocated once. The experts' training in 16 bits over the same layout
 is in ``training.py``: grouped products with both gradients, SwiGLU, AdamW, and
-``TrainableExperts``, which strings those together.
+``TrainableExperts``, which strings those together. ``routing.py`` has the
+layer's two ends with their gradients (the top-k router, the weighted return of
+rows), ``w4.py`` the experts in 4 bits for decode batches.
 """
 from __future__ import annotations
 
@@ -25,7 +27,7 @@ from ._capi import (MOE_BLOCK_M, MOE_FFN_UNFUSED, MOE_FOLD_WEIGHT_INTO_SCALE,
 from .training import (AdamW, TrainableExperts, collect_row_grads, expand_rows, grouped_matmul,
                        grouped_matmul_dgrad, grouped_matmul_wgrad, swiglu, swiglu_backward)
 from .routing import combine_rows, combine_rows_backward, route_topk, route_topk_backward
-from .w4 import grouped_matmul_w4
+from .w4 import FourBitExperts, grouped_matmul_w4
 
 __all__ = [
     "expanded_capacity", "workspace_size", "expand_layout", "expand_scatter",
@@ -40,7 +42,7 @@ __all__ = [
     "expand_rows", "collect_row_grads", "grouped_matmul", "grouped_matmul_dgrad",
     "grouped_matmul_wgrad", "swiglu", "swiglu_backward", "AdamW", "TrainableExperts",
     "route_topk", "route_topk_backward", "combine_rows", "combine_rows_backward",
-    "grouped_matmul_w4",
+    "grouped_matmul_w4", "FourBitExperts",
 ]
 
 

@@ -517,7 +517,7 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
   MOE_REQUIRE(moe::aligned(x, 16) && moe::aligned(codes, 16) && moe::aligned(out, 16) &&
                   moe::aligned(scales, 16) && moe::aligned(zeros, 8),
               "moe_grouped_mm_w4: x, codes, scales and out must be 16-byte aligned, zeros 8-byte");
-  MOE_REQUIRE(static_cast<int64_t>(E) * N <= INT32_MAX, "moe_grouped_mm_w4: E N exceeds 32 bits");
+  MOE_REQUIRE(static_cast<int64_t>(E) * N <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit row numbers");
   const int64_t live = std::min<int64_t>(E, max_rows);
   const int64_t mean = live > 0 ? (max_rows + live - 1) / live : 0;
   MOE_REQUIRE((max_rows / 8 + live) * ((N + 31) / 32) <= INT32_MAX,

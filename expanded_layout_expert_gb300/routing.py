@@ -55,12 +55,15 @@ def route_topk(logits: torch.Tensor, K: int, *, score: str = "softmax", renormal
         if n_valid is not None:
             with torch.cuda.stream(stream):
                 ids.fill_(-1)
+    else:
+        _whole(ids, "ids", (T, K), torch.int32, dev)
     if weights is None:
         weights = _new(torch.empty if n_valid is None else torch.zeros, (T, K), torch.float32, logits, stream)
+    else:
+        _whole(weights, "weights", (T, K), torch.float32, dev)
     rc = load().moe_route_topk(
         lp, ld, dt, _whole(bias, "bias", (E,), torch.float32, dev), _word(n_valid, "n_valid", dev), T, E, K,
-        code, int(renormalize), factor, _whole(ids, "ids", (T, K), torch.int32, dev),
-        _whole(weights, "weights", (T, K), torch.float32, dev), _stream(stream, dev))
+        code, int(renormalize), factor, ids.data_ptr(), weights.data_ptr(), _stream(stream, dev))
     check(rc, "moe_route_topk")
     return ids, weights
 

@@ -440,11 +440,18 @@ class TrainableExperts:
     bfloat16; rows t >= n_valid are neither read nor written. backward belongs
     to the last forward, of which the layer keeps what it needs (n_valid and x
     may be refilled before it), and overwrites what that kept of gate_up.
+
+    weighting "expanded" (default): the weight multiplies a pair's row between
+    the products (swiglu's row weight). "gather": the products run unweighted and
+    combine_rows applies the weights, as ExpandedMoELayer's "gather" does; the
+    layer then keeps topk_w for the backward too.
     """
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, *, K: int, max_tokens: int,
-                 align: int = 1):
+                 align: int = 1, weighting: str = "expanded"):
         from . import Layout, expanded_capacity, workspace_size
+        if weighting not in ("expanded", "gather"):
+            raise ValueError(f"weighting must be 'expanded' or 'gather', got {weighting!r}")
         E, twoI, H = w13.shape
         if twoI % 2 or w2.shape != (E, H, twoI // 2):
             raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
@@ -469,6 +476,8 @@ class TrainableExperts:
         self.dh, self.drow_w = b16(M, self.I), f32(M)
         self.y, self.dx, self.dtopk_w = b16(max_tokens, H), b16(max_tokens, H), f32(max_tokens, K)
         self.dw13, self.dw2 = f32(E, twoI, H), f32(E, H, self.I)
+        self.weighting = weighting
+        self._topk_w = f32(max_tokens, K) if weighting == "gather" else None   # the last forward's
         self._n_valid = None          # the last forward's: None or the copy of its word
         self._n_valid_word = i32(1)
         self._ready = False
@@ -482,7 +491,7 @@ class TrainableExperts:
         return [self.dw13, self.dw2]
 
     def forward(self, x, topk_ids, topk_w, n_valid=None, stream=None) -> torch.Tensor:
-        from . import combine, expand_layout
+        from . import combine, combine_rows, expand_layout
         dev = _device(self.w13, "w13")
         _rows(x, "x", self.T, self.H, torch.bfloat16, dev)
         _whole(topk_ids, "topk_ids", (self.T, self.K), torch.int32, dev)
@@ -496,28 +505,44 @@ class TrainableExperts:
             with torch.cuda.stream(stream):
                 n_valid = self._n_valid_word.copy_(n_valid.as_strided((1,), (1,)))
         self._n_valid = n_valid
+        gather = self.weighting == "gather"
+        if gather:
+            with torch.cuda.stream(stream):
+                self._topk_w.copy_(topk_w)
         expand_layout(topk_ids, self.E, self.align, self.M_cap, n_valid, self.ws, self.status, lay,
                       stream)
-        expand_rows(x, lay, topk_w, n_valid, self.xe, self.row_w, self.status, stream)
+        expand_rows(x, lay, None if gather else topk_w, n_valid, self.xe, None if gather else self.row_w,
+                    self.status, stream)
         grouped_matmul(self.xe, self.w13, lay, self.gu, self.status, stream)
-        swiglu(self.gu, lay, self.row_w, self.h, stream)
+        swiglu(self.gu, lay, None if gather else self.row_w, self.h, stream)
         grouped_matmul(self.h, self.w2, lay, self.down, self.status, stream)
-        combine(self.down, lay.src2dst, None, n_valid, self.y, stream)
+        if gather:
+            combine_rows(self.down, lay, self._topk_w, n_valid, None, self.y, self.status, stream)
+        else:
+            combine(self.down, lay.src2dst, None, n_valid, self.y, stream)
         self._ready = True
         return self.y
 
     def backward(self, dy: torch.Tensor, accumulate: bool = False, stream=None):
-        from . import combine
+        from . import combine, combine_rows_backward
         if not self._ready:
             raise RuntimeError("backward needs a forward before it")
         lay, nv, st = self.lay, self._n_valid, self.status
-        ddown = expand_rows(dy, lay, None, nv, self.down, None, st, stream)   # a dy it refuses costs nothing
+        gather = self.weighting == "gather"
+        # a dy that either refuses costs nothing
+        if gather:
+            ddown, _ = combine_rows_backward(dy, self.down, lay, self._topk_w, nv, self.down, self.dtopk_w, st,
+                                             stream)
+        else:
+            ddown = expand_rows(dy, lay, None, nv, self.down, None, st, stream)
         self._ready = False
         grouped_matmul_wgrad(ddown, self.h, lay, self.dw2, accumulate, status=st, stream=stream)
         grouped_matmul_dgrad(ddown, self.w2, lay, self.dh, st, stream)
-        dgu, drow_w = swiglu_backward(self.dh, self.gu, lay, self.row_w, self.gu, self.drow_w, stream)
+        dgu, drow_w = swiglu_backward(self.dh, self.gu, lay, None if gather else self.row_w, self.gu,
+                                      self.drow_w, stream)
         grouped_matmul_wgrad(dgu, self.xe, lay, self.dw13, accumulate, status=st, stream=stream)
         dxe = grouped_matmul_dgrad(dgu, self.w13, lay, self.down, st, stream)
         combine(dxe, lay.src2dst, None, nv, self.dx, stream)
-        collect_row_grads(drow_w, lay, nv, self.dtopk_w, stream)
+        if not gather:
+            collect_row_grads(drow_w, lay, nv, self.dtopk_w, stream)
         return self.dx, self.dtopk_w
