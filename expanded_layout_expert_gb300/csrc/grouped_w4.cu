@@ -1,26 +1,35 @@
 // moe_grouped_mm_w4: the experts' product over 4-bit weights with group scales,
 //   out[r, n] = sum_k x[r, k] s[e, n, k / g] (q[e, n, k] - z[e, n, k / g]),
 // for batches of single tokens, where the time is that of reading the weights.
-// This is the form for more than a dozen rows an expert; grouped_w4_few.cu has
-// the other.
+// This is the form for more than a few rows an expert; grouped_w4_few.cu has
+// the other, and the end of this file the choice.
 //
 // The weights are the tensor core's first operand, read from tensor memory:
 //   D[i, r] = sum_c W[i, c] X[r, c],
-// a tile being 128 weight rows by kR activation rows (32 or 64) of one expert.
-// TMA brings 128 contracted values at a time, 64 bytes of codes a row and the rows
-// of x; a thread takes one weight row: it makes 64 codes at a time 16-bit values
-// (w4.cuh: exact) and stores them into its lane of tensor memory. Each scale
-// group has sums of its own there, which the thread multiplies by its scale and
-// adds up in fp32 registers. So nothing is rounded but the sums and, once, the
-// result.
+// a tile being 256 weight rows, 128 to each of two warpgroups, by kR activation
+// rows (32 or 64) of one expert. TMA brings 128 contracted values at a time, 64
+// bytes of codes a weight row and the rows of x; a thread takes one weight row,
+// makes its codes 16-bit values (w4.cuh: exact) and stores them into its lane of
+// tensor memory. Each scale group has sums of its own there, which the thread
+// multiplies by its scale and adds up in fp32 registers. So nothing is rounded
+// but the sums and, once, the result.
 //
-// Four CTAs of four warps fit an SM. The warps meet at a barrier per 64 values,
-// after which one thread issues the products and refills the ring: with warps of
-// their own for that, which poll for their turn, half of the instructions were
-// polls (4096 x 7168 weights of 64 experts, 32 rows each: 414 us). A CTA makes the
-// next 64 values while its products run, so it rarely finds them unfinished. With
-// few tiles the contraction is split over the CTAs of a cluster, whose partial
-// sums meet in a fixed order through distributed shared memory.
+// Bound: a 128 x 128 block of codes has 360 cycles at HBM's rate on an SM; making
+// its values is 43 instructions a scheduler and 32 values, all in all 350 a
+// warp, and 4 warps a scheduler (their accumulators fill the registers) issue in
+// 58 % of the cycles. 64 experts of 4096 x 7168 with 8, 16 and 32 rows each take
+// 228, 230 and 245 us (4.4, 4.4 and 4.2 TB/s), 32 experts with 64 rows 194.
+// What got there, in us for 32 rows: one CTA of four dequantising warps, a TMA
+// and an MMA warp, sums waited for at once 490; the next values made meanwhile
+// 386; no warps of their own for the loads and products, which poll for their
+// turn with half of all instructions, 374; the operands of those known to be
+// uniform 300; 256 rows a CTA, so that four stages fit, 279; the warpgroups'
+// barriers apart 249; the loop's arithmetic off the uniform pipe 247.
+// Eight warps for 128 rows, three CTAs, were slower (362), and so were sums
+// fetched while the next values are made (267).
+//
+// With few tiles the contraction is split over the CTAs of a cluster, whose
+// partial sums meet in a fixed order through distributed shared memory.
 #include <algorithm>
 #include <atomic>
 
@@ -60,20 +69,23 @@ struct W4Params {
   int blocks;             // stages along the contraction
   int groups;             // scales of a row
   int splits;             // CTAs of a cluster
+  int code_rows;          // rows of codes that a copy brings: 256 or 128
   int64_t M_cap;
   uint16_t* out;
   int64_t ld_out;
   int32_t* status;
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands, K = 16.
-MOE_DEV void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                           uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands, K = 16. B's descriptor comes
+// in halves, of which only the low one moves: a 64-bit sum takes two steps.
+template <bool kAdd>
+MOE_DEV void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t b_high, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(b_high), "r"(idesc), "n"(kAdd ? 1 : 0)
       : "memory");
 }
 
@@ -153,18 +165,15 @@ MOE_DEV bool try_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok != 0);
 }
 
-// The 128 threads of a warpgroup meet; true if `flag` is so for any.
-MOE_DEV bool meet_or(int group, bool flag) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(static_cast<uint32_t>(flag)), "r"(group + 1)
-      : "memory");
-  return any != 0;
+// The 128 threads of a warpgroup meet.
+MOE_DEV void meet(int group) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(group + 1) : "memory");
+}
+
+// Arrive once on `bar` when every tcgen05 operation this thread issued before has
+// completed.
+MOE_DEV void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // True in one lane of a converged warp.
@@ -237,8 +246,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (e >= 0) {   // the same for the whole cluster
     const int b0 = p.blocks * rank / splits, b1 = p.blocks * (rank + 1) / splits;
-    constexpr int kBox = kR / 2;                    // rows of x that a copy brings
-    const int boxes = (rows + kBox - 1) / kBox;
     const uint32_t idesc = idesc_f16(Half, false, false, kHalf, (rows + 15) / 16 * 16);
     const uint64_t x0 = sw128_kmajor_desc(smem_u32(smem) + kCodeBytes);
     const bool both = i0 + kHalf < p.N;   // else the second warpgroup has no rows
@@ -247,21 +254,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto wait = [&](uint32_t bar, uint64_t* at, uint32_t parity) {
       return try_wait(bar, parity) || mbar_wait_warp(at, parity, abort_flag, p.status);
     };
-    auto load = [&](int b, int stage) {   // by one lane of warp 1
+    // A wait that gave up, here or in another warp, ends the waits and the loads;
+    // the rest of the loop goes on with whatever there is, and nothing is stored.
+    bool got = true;
+    auto expect = [&](uint32_t bar, uint64_t* at, uint32_t parity) {
+      if (got) got = wait(bar, at, parity);
+    };
+    // By one lane. The copies are few, because the warp that asks for them keeps
+    // the other three waiting: 256 rows of codes at once where all are the
+    // expert's, and all of the tile's rows of x, needed or not.
+    auto load = [&](int b, int stage) {
       uint8_t* sw = smem + stage * kStageBytes;
       uint8_t* sx = sw + kCodeBytes;
       const uint32_t bar = smem_u32(&full[stage]);
-      mbar_arrive_expect_tx(&full[stage], (both ? kCodeBytes : kHalfBytes) + boxes * (kBox * BC * 2));
+      mbar_arrive_expect_tx(&full[stage], (both ? kCodeBytes : kHalfBytes) + kR * BC * 2);
       load_2d<1>(sw, &tmW, b * (BC / 2), e * p.N + i0, bar);
-      if (both) load_2d<1>(sw + kHalfBytes, &tmW, b * (BC / 2), e * p.N + i0 + kHalf, bar);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (i >= boxes) break;
-        load_2d<1>(sx + i * (kBox * 128), &tmX, b * BC, row0 + i * kBox, bar);
-        load_2d<1>(sx + (kR + i * kBox) * 128, &tmX, b * BC + 64, row0 + i * kBox, bar);
-      }
+      if (both && p.code_rows == kHalf) load_2d<1>(sw + kHalfBytes, &tmW, b * (BC / 2), e * p.N + i0 + kHalf, bar);
+      load_2d<1>(sx, &tmX, b * BC, row0, bar);
+      load_2d<1>(sx + kR * 128, &tmX, b * BC + 64, row0, bar);
     };
-    int loaded = min(kStages, b1 - b0);   // stages asked for
+    const int loaded = min(kStages, b1 - b0);   // stages asked for in advance
     if (warp == 1 && elect_one())
       for (int s = 0; s < loaded; ++s) load(b0 + s, s);
     // Thread t holds weight row i0 + t, a column of `out`. A warpgroup's TMEM
@@ -291,15 +303,21 @@ __global__ void __launch_bounds__(kThreads, 2)
             fma2(acc[(r0 + r) / 2], f[q], __uint_as_float(v[r]), __uint_as_float(v[r + 1]));
         }
     };
-    bool got = true, stop = false;
-    int stage = 0, b = b0;
+    // The loop's own arithmetic is kept short: what the compiler knows to be uniform
+    // goes through a slower pipe, step after step in all warps.
+    const uint32_t swizzle = ((row >> 1) & 3) << 4;
+    uint32_t codes = smem_u32(smem) + threadIdx.x * 64, bar = bars;   // of the stage
+    uint32_t xs = static_cast<uint32_t>(x0);
+    const uint32_t x_high = static_cast<uint32_t>(x0 >> 32);
     uint32_t phase = 0, turn = 0;
-    const uint32_t my_codes = smem_u32(smem) + threadIdx.x * 64, swizzle = ((row >> 1) & 3) << 4;
-    if (half == 1 && !both) b = b1;
-    for (; b < b1 && !stop; ++b) {
-      if ((b - b0) % (4 / kGroups) == 0) groups.refill();
-      got = wait(bars + stage * 8, &full[stage], phase) && got;
-      const uint32_t codes = my_codes + stage * kStageBytes;
+    int slot = 0, old = 0;                     // the stage's place in the ring, and the one before's
+    int left = half == 1 && !both ? 0 : b1 - b0, to_load = left - loaded;
+    int groups_left = p.groups - b0 * kGroups;   // of the rows
+    const bool some = left > 0;
+    bool first = true;
+    for (int n = 0; left > 0; --left, ++n) {
+      if (n % (4 / kGroups) == 0) groups.refill();
+      expect(bar, &full[slot], phase);
 #pragma unroll
       for (int h = 0; h < kSteps; ++h) {
         auto values = [&](int c, uint32_t (&v)[16]) {   // of chunk c of the step
@@ -319,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint32_t ahead[kAhead][16];
 #pragma unroll
           for (int c = 0; c < kAhead; ++c) values(c, ahead[c]);
-          if (h > 0 || b > b0) {
-            got = wait(d_bar, &d_ready[half], turn ^ 1u) && got;
+          if (h > 0 || !first) {
+            expect(d_bar, &d_ready[half], turn ^ 1u);
             tc_fence_after();
             add();
           }
@@ -337,50 +355,63 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int q = 0; q < kEnds; ++q) {   // a group past the contraction has products with zeros
           const int g = h * kEnds + q;
           const uint32_t s = g & 1 ? groups.s[g / 2] >> 16 : groups.s[g / 2] & 0xffffu;
-          f[q] = b * kGroups + g < p.groups ? unpack2<Half>(s).x : 0.0f;
+          f[q] = kGroup == BC || g < groups_left ? unpack2<Half>(s).x : 0.0f;
         }
         tc_wait_st();
         tc_fence_before();
-        stop = meet_or(half, !got);
-        if (stop) break;
+        meet(half);
         if ((warp & 3) == 0 && elect_one()) {
           tc_fence_after();
-          const uint64_t xs = x0 + static_cast<uint32_t>(stage * (kStageBytes >> 4));
 #pragma unroll
           for (int k = 0; k < kStep; k += kUmmaK) {
             const int c = h * kStep + k;   // of the stage
-            tc_mma_f16_ta(half_tmem + kACols + k / kGroup * kR, half_tmem + k / 2,
-                          xs + ((c / 64 * (kR * 128) + c % 64 * 2) >> 4), idesc, k % kGroup != 0 ? 1u : 0u);
+            const uint32_t d = half_tmem + kACols + k / kGroup * kR, x_low = xs + ((c / 64 * (kR * 128) + c % 64 * 2) >> 4);
+            if (k % kGroup != 0)
+              tc_mma_f16_ta<true>(d, half_tmem + k / 2, x_low, x_high, idesc);
+            else
+              tc_mma_f16_ta<false>(d, half_tmem + k / 2, x_low, x_high, idesc);
           }
-          tc_commit(&d_ready[half]);
+          commit(d_bar);
         }
-        if (h == 0 && b > b0 && b0 + loaded < b1) {
+        if (h == 0 && !first && to_load > 0) {
           // this warpgroup has used up the stage before; the later one fills it
-          if ((warp & 3) == 1 && elect_one()) {
-            const int old = stage == 0 ? kStages - 1 : stage - 1;
+          if ((warp & 3) == 1 && got && elect_one()) {
             __threadfence_block();
-            if (!both || atomicAdd(&s_used[old], 1) & 1) load(b0 + loaded, old);
+            if (!both || atomicAdd(&s_used[old], 1) & 1) load(b1 - to_load, old);
           }
-          ++loaded;
+          --to_load;
         }
         turn ^= 1u;
       }
+      first = false;
       groups.pass<kGroups>();
-      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      groups_left -= kGroups;
+      old = slot;
+      codes += kStageBytes;
+      bar += 8;
+      xs += kStageBytes >> 4;
+      if (++slot == kStages) {
+        slot = 0;
+        codes -= kStages * kStageBytes;
+        bar = bars;
+        xs = static_cast<uint32_t>(x0);
+        phase ^= 1u;
+      }
     }
-    if (!stop && b1 > b0 && (half == 0 || both)) {
-      stop = !(wait(d_bar, &d_ready[half], turn ^ 1u) && got);
+    if (some) {
+      expect(d_bar, &d_ready[half], turn ^ 1u);
       tc_fence_after();
       add();
       tc_fence_before();
     }
-    stop = __syncthreads_or(stop);   // the ring is free: every product is done
+    const bool stop = __syncthreads_or(!got);   // the ring is free: every product is done
     if (stop && row == 0) {
       // what is under way has landed before the CTA can exit
       tc_commit(&done[half]);
       drain_wait(&done[half], 0);
-      for (int s = 0; s < kStages && s < loaded; ++s)
-        drain_wait(&full[s], static_cast<uint32_t>((loaded - 1 - s) / kStages) & 1u);
+      const int asked = b1 - b0 - max(to_load, 0);
+      for (int s = 0; s < kStages && s < asked; ++s)
+        drain_wait(&full[s], static_cast<uint32_t>((asked - 1 - s) / kStages) & 1u);
     }
     uint16_t* out = p.out + static_cast<int64_t>(row0) * p.ld_out + i;
     float* part = reinterpret_cast<float*>(smem);
@@ -485,9 +516,10 @@ int launch_grouped_w4_many(const W4Args& a, int R, cudaStream_t s) {
   const int64_t tiles = (a.max_rows / R + live) * ni;
   MOE_REQUIRE(tiles * p.splits <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
   CUtensorMap tw, tx;
-  int rc = make_tmap_codes4(&tw, a.codes, a.Kd / 2, static_cast<uint64_t>(a.E) * a.N, kHalf);
+  p.code_rows = a.N % kI == 0 ? kI : kHalf;
+  int rc = make_tmap_codes4(&tw, a.codes, a.Kd / 2, static_cast<uint64_t>(a.E) * a.N, p.code_rows);
   if (rc != MOE_OK) return rc;
-  rc = make_tmap_rows16(&tx, a.x, a.Kd, a.M_cap, a.ld_x, R / 2);
+  rc = make_tmap_rows16(&tx, a.x, a.Kd, a.M_cap, a.ld_x, R);
   if (rc != MOE_OK) return rc;
   auto* launch = a.group == 128  ? (a.half ? launch_rows<true, 128> : launch_rows<false, 128>)
                  : a.group == 64 ? (a.half ? launch_rows<true, 64> : launch_rows<false, 64>)
