@@ -84,6 +84,7 @@ struct W4Args {
 // Its form for chunks of 8 rows, with the scales and zero points of 32 weight
 // rows in at most kW4FewScaleBytes.
 constexpr int kW4FewScaleBytes = 128 * 1024;
+inline int w4_few_pitch(int groups) { return groups + (groups % 8 == 0 ? 8 : 0); }
 int launch_grouped_w4_few(const W4Args& a, cudaStream_t s);
 
 // Launches the tcgen05 block-scaled kernel (N % 256 == 0).

@@ -14,11 +14,11 @@
 // multiplies by its scale and adds up in fp32 registers. So nothing is rounded
 // but the sums and, once, the result.
 //
-// Bound: a 128 x 128 block of codes has 360 cycles at HBM's rate on an SM; making
-// its values is 43 instructions a scheduler and 32 values, all in all 350 a
-// warp, and 4 warps a scheduler (their accumulators fill the registers) issue in
-// 58 % of the cycles. 64 experts of 4096 x 7168 with 8, 16 and 32 rows each take
-// 228, 230 and 245 us (4.4, 4.4 and 4.2 TB/s), 32 experts with 64 rows 194.
+// Bound: a 128 x 128 block of codes has 360 cycles at HBM's rate on an SM. It is
+// 350 instructions of each of four warps, half of them the making of the values,
+// on four schedulers; four warps a scheduler (their sums fill the registers)
+// issue in 58 % of the cycles. 64 experts of 4096 x 7168 with 32 rows each take
+// 245 us (4.2 TB/s).
 // What got there, in us for 32 rows: one CTA of four dequantising warps, a TMA
 // and an MMA warp, sums waited for at once 490; the next values made meanwhile
 // 386; no warps of their own for the loads and products, which poll for their
@@ -57,7 +57,10 @@ constexpr int kTmemCols = 2 * kHalfCols;
 constexpr int step_k(int group, int R) { return 64 * group / R < 128 ? 64 * group / R : 128; }
 
 constexpr int stage_bytes(int R) { return kCodeBytes + R * BC * 2; }
-constexpr int stages_for(int R) { return 96 * 1024 / stage_bytes(R); }
+constexpr int kMaxStages = 4;
+constexpr int stages_for(int R) {
+  return 96 * 1024 / stage_bytes(R) < kMaxStages ? 96 * 1024 / stage_bytes(R) : kMaxStages;
+}
 constexpr int ring_bytes(int R) { return stages_for(R) * stage_bytes(R) + 1024; }
 
 struct W4Params {
@@ -490,6 +493,7 @@ int launch(const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int6
 template <bool Half, int kGroup>
 int launch_rows(int R, const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int64_t tiles,
                 cudaStream_t s) {
+  if (R <= 16) return launch<Half, kGroup, 16>(tw, tx, p, tiles, s);
   if constexpr (kGroup > 32)
     if (R > 32) return launch<Half, kGroup, 64>(tw, tx, p, tiles, s);
   return launch<Half, kGroup, 32>(tw, tx, p, tiles, s);
@@ -561,17 +565,19 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
                          static_cast<uint16_t*>(out), ld_out, d_status};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Which form, by the mean rows of an expert with rows and the weights read.
-  // Up to four rows mma.sync is the faster (64 experts of 2048 x 4096: 41, 54 and
-  // 64 us for 1, 2 and 4 rows, here 57, 68 and 78), from eight on this form (86 and
-  // 79); with fewer weights its few large tiles leave SMs idle longer: 8 experts
-  // of 4096 x 4096 take 27 us there and 31 here with 8 rows, 41 and 33 with 16; of
-  // 1024 x 1024 5.2 and 9.0 with 8, 9.4 and 11.5 with 32.
+  // Up to four rows mma.sync is the faster (64 experts of 2048 x 4096 with 1, 2 and
+  // 4 rows: 41, 54 and 63 us, here 52, 65 and 72), from eight on this form (76
+  // there, 72 here); with fewer weights its few large tiles leave SMs idle longer:
+  // 8 experts of 4096 x 4096 take 26 us there and 30 here with 8 rows, 39 and 32
+  // with 16; of 1024 x 1024 5.4 and 8.7 with 8, 9.4 and 11.5 with 32.
   const int64_t weights = live * N * Kd;
-  const int64_t scale_bytes = 32ll * (Kd / group) * 3;
-  if ((mean <= 4 || (mean <= 8 && weights <= (1ll << 27)) || (mean <= 32 && weights <= (1ll << 23))) &&
+  const int64_t scale_bytes = 32ll * moe::w4_few_pitch(Kd / group) * 3;
+  if ((mean <= 4 || (mean <= 8 && weights <= (1ll << 28)) || (mean <= 32 && weights <= (1ll << 23))) &&
       scale_bytes <= moe::kW4FewScaleBytes)
     return moe::launch_grouped_w4_few(a, s);
-  // Rows of a tile: 16 rows an expert (64 of 4096 x 7168) take 231 us with 32, 239
-  // with 64; 32 rows 316 and 249.
-  return moe::launch_grouped_w4_many(a, mean <= 16 || group == 32 ? 32 : 64, s);
+  // Rows of a tile: 64 experts of 2048 x 4096 with 8 rows each take 72, 76 and 79
+  // us with 16, 32 and 64, with 16 rows 92, 78 and 80, with 32 rows 151, 100 and 84;
+  // scales of 32 values (64 rows of their sums do not fit) 89 and 114 us with 8
+  // rows, 179 and 157 with 32.
+  return moe::launch_grouped_w4_many(a, mean <= 12 ? 16 : (mean <= 24 || group == 32 ? 32 : 64), s);
 }

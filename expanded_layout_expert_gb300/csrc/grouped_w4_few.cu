@@ -46,6 +46,7 @@ struct FewParams {
   const uint16_t* scales;
   const uint8_t* zeros;
   int E, N, Kd, groups;   // groups along Kd
+  int pitch;              // of a row's scales in shared memory
   int64_t M_cap;
   uint16_t* out;
   int64_t ld_out;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 7) grouped_w4_few_kernel(const FewPa
   const int n_rows = min(kTile, p.N - i0);
   const uint32_t base = smem_u32(smem);
   uint8_t* s_scales = smem + kRing;
-  uint8_t* s_zeros = s_scales + kTile * p.groups * 2;
+  uint8_t* s_zeros = s_scales + kTile * p.pitch * 2;
   // a lane copies 16 bytes of rows g, g + 8, g + 16 and g + 24 a step; rows past
   // the last are the last once more, and not stored
   const uint32_t place = g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
@@ -132,14 +133,29 @@ __global__ void __launch_bounds__(kThreads, 7) grouped_w4_few_kernel(const FewPa
     }
     copies_commit();
   };
-  // the scales and zero points of the tile's rows lie together
+  // The scales and zero points of the tile's rows lie together; where their rows
+  // are whole vectors, the copies are kept apart by one, so that the eight rows
+  // that are read at a time lie in different banks.
   {
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(p.scales + w_row * p.groups);
-    for (int i = threadIdx.x * 16; i < n_rows * p.groups * 2; i += kThreads * 16)
-      copy16(smem_u32(s_scales) + i, src + i, true);
-    if (kZeros)
-      for (int i = threadIdx.x * 8; i < n_rows * p.groups; i += kThreads * 8)
-        copy8(smem_u32(s_zeros) + i, p.zeros + w_row * p.groups + i);
+    const uint8_t* scales = reinterpret_cast<const uint8_t*>(p.scales + w_row * p.groups);
+    const uint8_t* zeros = p.zeros + w_row * p.groups;
+    if (p.pitch != p.groups) {
+      const int r = threadIdx.x / 4;   // four lanes a row
+      static_assert(kThreads == 4 * kTile, "a row of scales for every four threads");
+      if (r < n_rows) {
+        for (int i = t * 16; i < p.groups * 2; i += 64)
+          copy16(smem_u32(s_scales) + r * p.pitch * 2 + i, scales + r * p.groups * 2 + i, true);
+        if (kZeros)
+          for (int i = t * 8; i < p.groups; i += 32)
+            copy8(smem_u32(s_zeros) + r * p.pitch + i, zeros + r * p.groups + i);
+      }
+    } else {
+      for (int i = threadIdx.x * 16; i < n_rows * p.groups * 2; i += kThreads * 16)
+        copy16(smem_u32(s_scales) + i, scales + i, true);
+      if (kZeros)
+        for (int i = threadIdx.x * 8; i < n_rows * p.groups; i += kThreads * 8)
+          copy8(smem_u32(s_zeros) + i, zeros + i);
+    }
     copies_commit();
   }
 #pragma unroll
@@ -164,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 7) grouped_w4_few_kernel(const FewPa
   // rows g, g + 8, g + 16 and g + 24 in the scales and zero points
   int at[4];
 #pragma unroll
-  for (int h = 0; h < 4; ++h) at[h] = min(h * 8 + g, n_rows - 1) * p.groups;
+  for (int h = 0; h < 4; ++h) at[h] = min(h * 8 + g, n_rows - 1) * p.pitch;
   copies_wait<kStages - 1>();
   __syncthreads();   // the scales are there
 
@@ -287,6 +303,7 @@ int launch_grouped_w4_few(const W4Args& a, cudaStream_t s) {
   p.N = a.N;
   p.Kd = a.Kd;
   p.groups = a.Kd / a.group;
+  p.pitch = w4_few_pitch(p.groups);
   p.M_cap = a.M_cap;
   p.out = a.out;
   p.ld_out = a.ld_out;
@@ -294,7 +311,7 @@ int launch_grouped_w4_few(const W4Args& a, cudaStream_t s) {
   const int64_t tiles =
       (a.max_rows / kRows + std::min<int64_t>(a.E, a.max_rows)) * ((a.N + kTile - 1) / kTile);
   MOE_REQUIRE(tiles <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
-  const size_t bytes = kRing + static_cast<size_t>(kTile) * p.groups * (a.zeros != nullptr ? 3 : 2);
+  const size_t bytes = kRing + static_cast<size_t>(kTile) * p.pitch * (a.zeros != nullptr ? 3 : 2);
   auto* launch = a.group == 128  ? (a.half ? launch_zeros<true, 128> : launch_zeros<false, 128>)
                  : a.group == 64 ? (a.half ? launch_zeros<true, 64> : launch_zeros<false, 64>)
                                  : (a.half ? launch_zeros<true, 32> : launch_zeros<false, 32>);

@@ -119,6 +119,40 @@ def test_rows_of_one_expert(mx, rows, group):
     check(mx, [0, rows, 2], 328, 640, group, BF16, True, seed=rows)
 
 
+# rows of six experts, with more weights than the form for few rows takes: tiles of
+# 16, 32 and 64 rows, one and several of them, and experts without rows
+CROWDS = {"16": [10, 0, 3, 40, 1, 6], "32": [16, 33, 0, 17, 30, 9], "64": [64, 5, 130, 0, 65, 31]}
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["", "zeros"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("N,Kd,group", [(1096, 1952, 32), (1032, 2048, 32), (1160, 1984, 64), (1288, 1728, 64),
+                                        (1024, 2176, 128), (1296, 2304, 128)])
+@pytest.mark.parametrize("rows", CROWDS)
+def test_more_rows(mx, rows, N, Kd, group, dtype, zeros):
+    """Sizes that end inside tiles, stages and steps."""
+    counts = CROWDS[rows]
+    mean = -(-sum(counts) // len(counts))
+    assert len(counts) * N * Kd > 1 << 23 and (mean <= 12) == (rows == "16") and (mean > 24) == (rows == "64")
+    check(mx, counts, N, Kd, group, dtype, zeros, align=8, slack=2, pairs=sum(counts), seed=len(rows))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_contractions_split_over_a_cluster(mx, group):
+    """Few tiles and a long contraction: several CTAs a tile."""
+    check(mx, [40], 264, 8192, group, BF16, True, pairs=40)
+    check(mx, [33, 12], 128, 16384 + 128, group, F16, False, pairs=45)
+    check(mx, [200], 72, 4096, group, BF16, True, pairs=200)
+
+
+def test_single_tokens_over_long_contractions(mx):
+    """The form for few rows: scales of a row that are whole vectors in shared
+    memory, and not; more of them than it takes."""
+    for Kd, group in ((4096, 32), (4096 + 32, 32), (6528, 64), (7168, 128), (7168 - 128, 128)):
+        check(mx, [1, 0, 2, 8, 1], 200, Kd, group, BF16, True, pairs=12)
+    check(mx, [1, 3], 40, 65536, 32, F16, True, pairs=4)
+
+
 def test_long_contraction_and_many_experts(mx):
     check(mx, [2, 0, 40], 72, 16384, 128, BF16, True)
     check(mx, [i % 3 for i in range(1024)], 16, 64, 32, F16, False)
