@@ -403,3 +403,44 @@ def test_router_and_return_on_other_streams_and_captured(mx):
             assert torch.equal(a, b)
     # the weights sum to one: the return of the tokens' own rows doubles them
     close(held[2], 2 * x.double(), (2.0 ** -8 + 1e-6) * 2 * x.double().abs(), "return")
+
+
+def test_offsets_past_32_bits(mx):
+    """Rows of 4.6 GB: the last ones go back to tokens, and get their gradients."""
+    M, H, T, K = 320_000, 7168, 3, 2
+    rows = torch.zeros(M, H, dtype=BF16, device="cuda")
+    src = torch.tensor([[0, M - 1], [M - 2, 1], [-1, M - 3]], dtype=torch.int32, device="cuda")
+    used = src[src >= 0].long()
+    g = gen(2)
+    rows[used] = normal(g, len(used), H, dtype=BF16)
+    one = torch.full((1,), M, dtype=torch.int32, device="cuda")
+    lay = mx.Layout(psum=one, start=torch.zeros_like(one), total=one, m_indices=one[:0], src2dst=src,
+                    tile_prefix=one[:0], E=1, align=1, M_cap=M)
+    w, dy = normal(g, T, K), normal(g, T, H, dtype=BF16)
+    out = mx.combine_rows(rows, lay, w)
+    drows, dw = mx.combine_rows_backward(dy, rows, lay, w)
+    for t in range(T):
+        exact, size = torch.zeros(H, dtype=F64, device="cuda"), 0
+        for k in range(K):
+            r = int(src[t, k])
+            if r < 0:
+                assert dw[t, k] == 0
+                continue
+            term = rows[r].double() * w[t, k].double()
+            exact, size = exact + term, size + term.abs()
+            close(drows[r], dy[t].double() * w[t, k].double(),
+                  (2.0 ** -8 + 2.0 ** -23) * (dy[t].double() * w[t, k].double()).abs() + TINY[BF16], "drows")
+            terms = dy[t].double() * rows[r].double()
+            close(dw[t, k], terms.sum(), (H + 8) * 2.0 ** -24 * terms.abs().sum(), "dtopk_w")
+        close(out[t], exact, 2.0 ** -8 * exact.abs() + 2.0 ** -21 * size + TINY[BF16], "combine")
+
+
+def test_route_infinite_logits(mx):
+    """+inf is chosen first; a softmax over it has no value, sigmoids have one."""
+    logits = torch.tensor([[0.0, INF, -1.0, 2.0]], device="cuda")
+    ids, w = mx.route_topk(logits, 2)
+    assert ids.tolist() == [[1, 3]] and w.isnan().all()
+    ids, w = mx.route_topk(logits, 2, score="sigmoid")
+    assert ids.tolist() == [[1, 3]] and w[0, 0] == 1
+    ids, w = mx.route_topk(logits, 3, bias=torch.tensor([0.0, -INF, 5.0, NAN], device="cuda"), score="sigmoid")
+    assert ids.tolist() == [[2, 0, -1]] and w[0, 2] == 0

@@ -204,3 +204,74 @@ def test_results_do_not_change_from_run_to_run(mx):
     first = mx.grouped_matmul_w4(x, codes, scales, lay, zeros=z)
     for _ in range(5):
         assert torch.equal(first, mx.grouped_matmul_w4(x, codes, scales, lay, zeros=z))
+
+
+def test_many_experts_with_more_rows(mx):
+    check(mx, [i % 21 for i in range(1024)], 136, 96, 32, BF16, True, pairs=sum(i % 21 for i in range(1024)))
+    check(mx, [0] * 500 + [70, 0, 31] + [0] * 521, 264, 128, 128, F16, False, pairs=101)
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_offsets_past_32_bits(mx, rows):
+    """Codes of 2.3 GB, with rows at the first and the last expert."""
+    E, N, Kd, group = 160, 4096, 7168, 128
+    counts = [rows] + [0] * (E - 2) + [rows]
+    lay, bounds = layout_of(mx, counts, pairs=2 * rows)
+    g = gen(rows)
+    x = normal(g, 2 * rows, Kd, dtype=BF16)
+    codes, scales, z = weights(g, E, N, Kd, group, BF16, True)
+    out = mx.grouped_matmul_w4(x, codes, scales, lay, zeros=z)
+    for e in (0, E - 1):
+        a, b = bounds[e]
+        X, W = x[a:b].double(), dense(codes, scales, z, e)
+        exact = X @ W.T
+        tol = U[BF16] * exact.abs() + (Kd + 16) * 2.0 ** -23 * (X.abs() @ W.abs().T)
+        assert ((out[a:b].double() - exact).abs() <= tol).all(), e
+
+
+def test_not_finite_in_tiles_of_more_rows(mx):
+    """Rows of x past the chunk's in its tile, other experts' weights in the tile of
+    weight rows, scales and rows that are not finite."""
+    counts = [40, 33, 61]
+    lay, _ = layout_of(mx, counts, pairs=sum(counts))
+    g = gen(6)
+    x = normal(g, sum(counts), 2048, dtype=BF16)
+    codes, scales, z = weights(g, 3, 1480, 2048, 128, BF16, True)
+    clean = mx.grouped_matmul_w4(x, codes, scales, lay, zeros=z)
+    x2, s2 = x.clone(), scales.clone()
+    x2[40], x2[70, 100], s2[1, 1479, 2], s2[2, 0, 0] = NAN, INF, INF, NAN
+    y = mx.grouped_matmul_w4(x2, codes, s2, lay, zeros=z)
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[40], hit[70], hit[40:73, 1479], hit[73:, 0] = True, True, True, True
+    assert not y[hit].isfinite().any()
+    assert torch.equal(y[~hit], clean[~hit])
+
+
+def test_more_rows_than_said_are_flagged(mx):
+    """A wrong bound on the rows, in the form for more of them."""
+    lay, _ = layout_of(mx, [200, 300], pairs=100)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    codes, scales, _ = weights(gen(0), 2, 64, 64, 64, BF16, False)
+    mx.grouped_matmul_w4(normal(gen(1), 500, 64, dtype=BF16), codes, scales, lay, status=status)
+    assert status.item() == -5
+
+
+def test_calls_on_two_streams_at_once(mx):
+    """Both forms share nothing between calls."""
+    g = gen(9)
+    cases = []
+    for counts, pairs in (([1, 2, 0, 1], 4), ([40, 50, 3, 64], 157)):
+        lay, _ = layout_of(mx, counts, pairs=pairs)
+        x = normal(g, sum(counts), 1024, dtype=BF16)
+        w = weights(g, 4, 1032, 1024, 64, BF16, True)
+        cases.append((x, w, lay, mx.grouped_matmul_w4(x, w[0], w[1], lay, zeros=w[2])))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for i in range(40):
+        x, w, lay, want = cases[i % 2]
+        s = streams[i % 4]
+        got.append((mx.grouped_matmul_w4(x, w[0], w[1], lay, zeros=w[2], stream=s), want))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, b)
