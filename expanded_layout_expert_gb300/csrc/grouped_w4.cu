@@ -113,9 +113,9 @@ struct GroupStream {
   uint2 s0, s1;
   uint32_t z0, z1;
   uint32_t s[2], z;   // the four
-  MOE_DEV void load() {
-    s1 = __ldg(scales + min(next, last));
-    if (zeros != nullptr) z1 = __ldg(zeros + min(next, last));
+  MOE_DEV void load(uint2& s, uint32_t& z) {
+    s = __ldg(scales + min(next, last));
+    if (zeros != nullptr) z = __ldg(zeros + min(next, last));
   }
   MOE_DEV void begin(const uint2* sc, const uint32_t* ze, int64_t first, int64_t values) {
     scales = sc + (first >> 2);
@@ -124,11 +124,9 @@ struct GroupStream {
     skew = static_cast<int>(first) & 3;
     z = 0x01010101u * kW4Zero;
     next = 0;
-    load();
-    s0 = s1;
-    z0 = z1;
+    load(s0, z0);   // neither is waited for here
     next = 1;
-    load();
+    load(s1, z1);
   }
   MOE_DEV void refill() {
     const bool up = skew & 2;
@@ -139,7 +137,7 @@ struct GroupStream {
     s0 = s1;
     z0 = z1;
     ++next;
-    load();
+    load(s1, z1);
   }
   template <int n>   // n of the four are used up: 1, 2 or 4
   MOE_DEV void pass() {
