@@ -7,6 +7,7 @@
 // Bytes: a row's 2H per pair, read (and, in the gradient, written), and 2H per
 // token: both are bound by HBM.
 #include <algorithm>
+#include <type_traits>
 
 #include "dtype16.cuh"
 #include "host_util.h"
@@ -182,10 +183,21 @@ __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
   }
 }
 
-// A warp for each token where there are tokens for every warp that fits, or a warp
-// holds a row at once; else a block.
-bool many_tokens(int64_t T, int nvec) {
-  return T >= static_cast<int64_t>(device_sm_count()) * 32 || nvec <= 32;
+// Warps for a token in the gradient. 16 warps are resident on an SM (124 registers
+// a thread), so a rule on T by whole rounds of them: 8 a token while every token is
+// in the first round, or nearly, with long rows; then 2, while those make one round
+// or, with long rows, rounds enough that a short last one counts more than the
+// sums' two barriers; 1 between and with short rows. us at 1 / 2 / 8, K = 8:
+//    256 x 7168  35 /  21 /  13      1536 x 1024  12 /  13 /  19
+//    512 x 7168  40 /  27 /  24      1536 x 7168  62 /  65 /  64
+//    768 x 7168  43 /  33 /  35      3000 x 7168 122 / 113 / 116
+//    768 x 1024 6.8 / 5.8 / 8.1      8192 x 1024  49 /  50 /  88
+int backward_warps(int64_t T, int nvec) {
+  const int64_t sms = device_sm_count();
+  if (nvec <= 32) return 1;
+  if (T <= 2 * sms || (T <= 4 * sms && nvec >= 512)) return 8;
+  if (T <= 8 * sms) return 2;
+  return T <= 16 * sms || nvec <= 128 ? 1 : 2;
 }
 constexpr int kCombineBlocks = 64;
 
@@ -251,13 +263,18 @@ extern "C" int moe_combine_rows_backward(const void* dy, int64_t ld_dy, const vo
   MOE_REQUIRE_DEVICE();
   const int nvec = H / 8;
   const int64_t most = static_cast<int64_t>(moe::device_sm_count()) * (2048 / moe::kThreads) * 8;
-  const bool many = moe::many_tokens(T, nvec);
-  const int64_t need = many ? (T + moe::kThreads / 32 - 1) / (moe::kThreads / 32) : T;
+  const int warps = moe::backward_warps(T, nvec);
+  const int tokens = moe::kThreads / 32 / warps;   // of a block at a time
+  const int64_t need = (T + tokens - 1) / tokens;
   const int64_t blocks = need < most ? need : most;
   if (pad + blocks == 0) return MOE_OK;
-  auto* kernel = dtype == MOE_F16
-                     ? (many ? moe::combine_rows_backward_kernel<true, 1> : moe::combine_rows_backward_kernel<true, 8>)
-                     : (many ? moe::combine_rows_backward_kernel<false, 1> : moe::combine_rows_backward_kernel<false, 8>);
+  auto pick = [warps](auto half) {
+    constexpr bool kHalf = decltype(half)::value;
+    return warps == 1   ? moe::combine_rows_backward_kernel<kHalf, 1>
+           : warps == 2 ? moe::combine_rows_backward_kernel<kHalf, 2>
+                        : moe::combine_rows_backward_kernel<kHalf, 8>;
+  };
+  auto* kernel = dtype == MOE_F16 ? pick(std::true_type{}) : pick(std::false_type{});
   kernel<<<static_cast<unsigned>(pad + blocks), moe::kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       static_cast<const uint16_t*>(dy), ld_dy, static_cast<const uint16_t*>(rows), ld_rows, topk_w, src2dst,
       psum, d_n_valid, T, nvec, K, align, M_cap, static_cast<uint16_t*>(drows), ld_drows, dtopk_w,

@@ -275,7 +275,7 @@ def test_combine_rows(mx, T, H, K, E, align, residual, weighted, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("weighted", [True, False], ids=["w", "plain"])
 @pytest.mark.parametrize("in_place", [False, True], ids=["", "in place"])
-@pytest.mark.parametrize("T,H,K,E,align", COMBINE + [(5000, 264, 2, 6, 16)])
+@pytest.mark.parametrize("T,H,K,E,align", COMBINE + [(5000, 264, 2, 6, 16), (701, 1032, 9, 16, 8), (450, 4104, 2, 6, 1)])
 def test_combine_rows_backward(mx, T, H, K, E, align, in_place, weighted, dtype):
     lay = pairs(mx, T, K, E, align, seed=T * 3 + H)
     src = lay.src2dst.long()
