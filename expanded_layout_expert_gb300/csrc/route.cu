@@ -3,15 +3,18 @@
 //   key_e = fl32(l_e + b_e);  ids = the K largest keys, ties to the lowest e
 //   softmax: w_k = c p[i_k], p = softmax(l) over E, or over the chosen
 //   sigmoid: w_k = c s[i_k], s = 1 / (1 + e^-l), or c s[i_k] / sum_j s[i_j]
-// A group of lanes takes a row: a warp, or, for up to 64 experts and 8 pairs, 8
-// lanes. Lane i of a group of n holds the logits and keys of experts i, i + n, ...
+// A group of lanes takes a row: a warp, or 8 lanes where there are many rows of few
+// experts. Lane i of a group of n holds the logits and keys of experts i, i + n, ...
 // Keys are mapped to unsigned integers of the same order; a round finds the
-// largest of the group and the lowest expert that has it. Up to eight keys a lane
-// are kept sorted (a stable insertion sort), so that a round looks at one key a
-// lane and the chosen lane moves up; more are searched again each round.
+// largest of the group and the lowest expert that has it. A lane keeps its keys in
+// sorted runs of up to six (a stable insertion sort): a round looks at the runs'
+// heads, and the chosen one's run moves up.
 //
 // Bytes: a row's logits and 8K (12K and twice the logits back). The instructions
-// of a row set the time, not the bytes.
+// of a row set the time, not the bytes: 32768 x 160 fp32, K = 8, take 17 us (1.4
+// TB/s; issue slots 85 % busy), their gradient 10.7 us (4.1 TB/s, 61 % of HBM).
+// Every key searched again each round took 36 us, one sorted run of 5 by a warp
+// 19; 1024 experts in runs of 4, 19 us for 5120 rows, were 30 unsorted.
 #include "dtype16.cuh"
 #include "host_util.h"
 
@@ -143,13 +146,16 @@ MOE_DEV float weight_of(float l, bool ok, bool sigmoid, bool renormalize, float 
   return ok ? s / all : 0.0f;
 }
 
+// Keys of a sorted run, of the n of a lane.
+constexpr int run_of(int n) { return n % 4 == 0 ? 4 : n; }
+
 template <int kLanes, int kN>
 __global__ void __launch_bounds__(kThreads) route_topk_kernel(
     const void* __restrict__ logits, int64_t ld, int dtype, const float* __restrict__ bias,
     const int32_t* __restrict__ d_n_valid, int64_t T, int E, int K, bool sigmoid, bool renormalize,
     float factor, int32_t* __restrict__ ids, float* __restrict__ weights) {
   constexpr int kRows = kThreads / kLanes;   // of a block
-  constexpr bool kSorted = kN <= 8;
+  constexpr int kRun = run_of(kN);
   const int lane = threadIdx.x % kLanes;
   const int64_t nv = valid_rows(d_n_valid, T);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
@@ -183,11 +189,12 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(
         if (at[j] < E) sum += expf(l[j] - m);
       sum = group_sum<kLanes>(sum);
     }
-    if (kSorted) {
 #pragma unroll
-      for (int i = 1; i < kN; ++i)
+    for (int h = 0; h < kN; h += kRun)
 #pragma unroll
-        for (int j = i; j > 0; --j) {
+      for (int i = h + 1; i < h + kRun; ++i)
+#pragma unroll
+        for (int j = i; j > h; --j) {
           const bool up = u[j] > u[j - 1];
           const uint32_t hi = max(u[j], u[j - 1]), lo = min(u[j], u[j - 1]);
           u[j - 1] = hi;
@@ -196,37 +203,29 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(
           at[j - 1] = a;
           at[j] = c;
         }
-    }
     int my = -1;
     for (int k = 0; k < K; ++k) {
       uint32_t best = u[0];
       int e = at[0];
-      if (!kSorted) {
 #pragma unroll
-        for (int j = 1; j < kN; ++j)
-          if (u[j] > best) {
-            best = u[j];
-            e = at[j];
-          }
+      for (int h = kRun; h < kN; h += kRun) {
+        e = u[h] > best ? at[h] : e;
+        best = max(best, u[h]);
       }
       const uint32_t top = group_max<kLanes>(best);
       if (kLanes == 32 && top == 0) break;
       const int first = static_cast<int>(group_min<kLanes>(best == top ? static_cast<uint32_t>(e) : ~0u));
       if (lane == k && top != 0) my = first;
-      if (kSorted) {
-        if (e == first) {   // an expert is one lane's
 #pragma unroll
-          for (int j = 0; j + 1 < kN; ++j) {
+      for (int h = 0; h < kN; h += kRun)
+        if (at[h] == first) {   // an expert is one lane's
+#pragma unroll
+          for (int j = h; j + 1 < h + kRun; ++j) {
             u[j] = u[j + 1];
             at[j] = at[j + 1];
           }
-          u[kN - 1] = 0;
+          u[h + kRun - 1] = 0;
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if (at[j] == first) u[j] = 0;
-      }
     }
     const bool ok = my >= 0;
     const float w = weight_of<kLanes>(ok ? load_logit(logits, t * ld + my, dtype) : 0.0f, ok, sigmoid,
@@ -379,10 +378,20 @@ extern "C" int moe_route_topk(const void* logits, int64_t ld, int dtype, const f
                                      reinterpret_cast<cudaStream_t>(stream)>>>(                \
       logits, ld, dtype, bias, d_n_valid, T, E, K, score == MOE_SCORE_SIGMOID, renormalize != 0, \
       factor, topk_ids, topk_w)
-  if (E <= 64 && K <= 8)
-    MOE_NARROW(E, LAUNCH);
-  else
+  // 8 lanes a row save instructions, a warp time where all rows run at once (8
+  // and 32 lanes, K = 8: 1024 x 64 3.7 and 2.7 us, 4096 x 32 3.3 and 3.6, 4096 x 64
+  // 3.9 and 3.7, 16384 x 64 5.8 and 8.3, 8192 x 96 5.1 and 5.6, 32768 x 96 12.4 and
+  // 15.4, x 128 17.1 and 16.5, x 160 17.0 and 18.9, x 192 22.0 and 21.6).
+  const int64_t sms = moe::device_sm_count();
+  const int64_t enough = E <= 64 ? 24 * sms : (E <= 96 ? 48 * sms : 128 * sms);
+  if (K > 8 || T < enough || E > 160 || (E > 96 && E <= 128))
     MOE_WIDE(E, LAUNCH);
+  else if (E <= 64)
+    MOE_NARROW(E, LAUNCH);
+  else if (E <= 96)
+    LAUNCH(8, 12);
+  else
+    LAUNCH(8, 20);
 #undef LAUNCH
   return moe::check_launch("route_topk_kernel");
 }
@@ -411,7 +420,12 @@ extern "C" int moe_route_topk_backward(const float* dtopk_w, const void* logits,
                                               reinterpret_cast<cudaStream_t>(stream)>>>(          \
       dtopk_w, logits, ld, dtype, topk_ids, d_n_valid, T, E, K, score == MOE_SCORE_SIGMOID,       \
       renormalize != 0, factor, dlogits, ld_d)
-  if (K > 8 || E > 256)
+  // as above (8 and 32 lanes, K = 8: 1024 x 64 3.3 and 3.1 us, 4096 x 64 3.4 and 3.6,
+  // 2048 x 128 4.0 and 3.2, 8192 x 128 4.6 and 5.4, 4096 x 256 5.4 and 4.6, 8192 x
+  // 256 6.6 and 6.8, 32768 x 160 10.7 and 15.0)
+  const int64_t sms = moe::device_sm_count();
+  const int64_t enough = E <= 64 ? 16 * sms : (E <= 128 ? 24 * sms : 48 * sms);
+  if (K > 8 || E > 256 || T < enough)
     MOE_WIDE(E, LAUNCH);
   else if (E <= 64)
     MOE_NARROW(E, LAUNCH);

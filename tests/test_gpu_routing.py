@@ -123,7 +123,20 @@ SHAPES = [(1, 1), (2, 2), (8, 2), (33, 5), (64, 8), (100, 1), (160, 8), (257, 32
 @pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=["f32", "bf16", "fp16"])
 @pytest.mark.parametrize("E,K", SHAPES)
 def test_route(mx, E, K, dtype, score, renormalize, biased):
-    T, factor = 41, 2.5
+    check_route(mx, 41, E, K, dtype, score, renormalize, biased)
+
+
+@pytest.mark.parametrize("score,renormalize", [("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("E,K", [(1, 1), (8, 2), (15, 4), (31, 8), (48, 6), (64, 8), (65, 8), (96, 1), (97, 8), (128, 7),
+                                 (129, 8), (160, 8), (161, 8), (192, 8), (256, 8), (64, 9), (512, 8), (768, 3)])
+def test_route_rows_for_eight_lanes(mx, E, K, dtype, score, renormalize):
+    """Rows enough for the forms in which a warp takes four at a time, a last part of a warp's among them."""
+    check_route(mx, 20001, E, K, dtype, score, renormalize, E % 2 == 0)
+
+
+def check_route(mx, T, E, K, dtype, score, renormalize, biased):
+    factor = 2.5
     g = gen(E * 5 + K)
     wide = normal(g, T, E + 3, dtype=dtype, std=2.0)
     logits = wide[:, 1:E + 1]   # a stride, and an address that fits the type alone
