@@ -5,7 +5,9 @@
 // Sums in fp32 in a fixed order, each 16-bit result rounded once.
 //
 // Bytes: a row's 2H per pair, read (and, in the gradient, written), and 2H per
-// token: both are bound by HBM.
+// token: both are bound by HBM. 16384 tokens of H = 7168 with 8 pairs by Zipf: 364 us
+// (6.2 TB/s), the gradient 555 us (6.9 TB/s, what a copy reaches). 256 tokens: 8 us,
+// a chain of three reads of which each waits for the one before.
 #include <algorithm>
 #include <type_traits>
 
@@ -28,7 +30,9 @@ MOE_DEV int64_t valid_rows(const int32_t* d_n_valid, int64_t T) {
 
 // `parts` warps take a token, each a share of its columns, a 16-byte vector a lane
 // at a time; lane k holds pair k's row and weight, and the vectors of kDeep rows
-// are asked for before their sum.
+// are asked for before their sum. (The Zipf case with a branch at each gather 608 us,
+// gathers predicated and no branch in the sum 389, four at a time instead of eight
+// 366, blocks of 128 threads instead of 256 364.)
 constexpr int kDeep = 4;
 constexpr int kCombineThreads = 128;
 
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
   }
 }
 
-// Warps for a token in the gradient. 16 warps are resident on an SM (124 registers
+// Warps for a token in the gradient. 16 warps are resident on an SM (126 registers
 // a thread), so a rule on T by whole rounds of them: 8 a token while every token is
 // in the first round, or nearly, with long rows; then 2, while those make one round
 // or, with long rows, rounds enough that a short last one counts more than the

@@ -270,6 +270,7 @@ def test_results_are_made_on_the_calls_stream(monkeypatch, name):
 
 def test_kernels_do_not_spill():
     from expanded_layout_expert_gb300 import build
-    for src in ("route.cu", "combine_rows.cu"):
+    for src in ("route.cu", "combine_rows.cu", "grouped_w4.cu", "grouped_w4_few.cu"):
+        allowed = 8 if src == "grouped_w4_few.cu" else 0   # a value outside the loop
         for name, v in build.ptxas_usage(src).items():
-            assert v["spill_st"] == 0 and v["stack"] == 0, (name, v)
+            assert v["spill_st"] <= allowed and v["stack"] <= allowed, (name, v)
