@@ -16,17 +16,20 @@
 //
 // Bound: a 128 x 128 block of codes has 360 cycles at HBM's rate on an SM. It is
 // 350 instructions of each of four warps, half of them the making of the values,
-// on four schedulers; four warps a scheduler (their sums fill the registers)
-// issue in 58 % of the cycles. 64 experts of 4096 x 7168 with 32 rows each take
-// 245 us (4.2 TB/s).
+// on four schedulers, each step a chain from the sums to the values, the barrier and
+// the products; the four warpgroups of an SM cover for each other (a CTA alone takes
+// 0.83 us a block, two 1.07). 64 experts of 4096 x 7168 with 32 rows each take 234 us
+// (4.4 TB/s), with 8 rows 198 (5.0 TB/s).
 // What got there, in us for 32 rows: one CTA of four dequantising warps, a TMA
 // and an MMA warp, sums waited for at once 490; the next values made meanwhile
 // 386; no warps of their own for the loads and products, which poll for their
 // turn with half of all instructions, 374; the operands of those known to be
 // uniform 300; 256 rows a CTA, so that four stages fit, 279; the warpgroups'
-// barriers apart 249; the loop's arithmetic off the uniform pipe 247.
-// Eight warps for 128 rows, three CTAs, were slower (362), and so were sums
-// fetched while the next values are made (267).
+// barriers apart 249; the loop's arithmetic off the uniform pipe 245; sums first and
+// then the values, in few registers, 243; the scales moved up between them 234.
+// Eight warps for 128 rows, three CTAs, were slower (362), and so were sums fetched
+// while the next values are made (267) and the contraction split in two for fuller
+// waves (279): the start of a CTA takes 7 us.
 //
 // With few tiles the contraction is split over the CTAs of a cluster, whose
 // partial sums meet in a fixed order through distributed shared memory.
@@ -57,11 +60,13 @@ constexpr int kTmemCols = 2 * kHalfCols;
 constexpr int step_k(int group, int R) { return 64 * group / R < 128 ? 64 * group / R : 128; }
 
 constexpr int stage_bytes(int R) { return kCodeBytes + R * BC * 2; }
-constexpr int kMaxStages = 4;
-constexpr int stages_for(int R) {
-  return 96 * 1024 / stage_bytes(R) < kMaxStages ? 96 * 1024 / stage_bytes(R) : kMaxStages;
-}
-constexpr int ring_bytes(int R) { return stages_for(R) * stage_bytes(R) + 1024; }
+// What the ring takes is lost to L1, where the scales' sectors wait for their next
+// use, so the more scales a row has, the fewer stages (20 rows each for 64 experts of
+// 4096 x 7168 take, with 4 and 3 stages, 213 and 213 us in groups of 128, 254 and 234
+// in groups of 64, 408 and 286 in groups of 32; 8 rows 198 and 203, 226 and 220, 251
+// and 236; five stages for 8 rows in groups of 32, 332). Two stages are too few (364).
+constexpr int stages_for(int group, int R) { return group <= 2 * R ? 3 : 4; }
+constexpr int ring_bytes(int group, int R) { return stages_for(group, R) * stage_bytes(R) + 1024; }
 
 struct W4Params {
   const int32_t* start;
@@ -188,7 +193,7 @@ template <bool Half, int kGroup, int kR>
 __global__ void __launch_bounds__(kThreads, 2)
     grouped_w4_kernel(const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmX, const W4Params p) {
-  constexpr int kStages = stages_for(kR);
+  constexpr int kStages = stages_for(kGroup, kR);
   constexpr int kStageBytes = stage_bytes(kR);
   constexpr int kGroups = BC / kGroup;   // of a stage
   constexpr int kStep = step_k(kGroup, kR);
@@ -196,8 +201,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kEnds = kStep / kGroup;  // groups of a step
   constexpr int kACols = kStep / 2;
   constexpr int kChunks = kStep / 32;    // of 32 values, a 16-byte vector of codes
-  // made before the products of the step before are waited for, as registers allow
-  constexpr int kAhead = kR <= 32 ? 2 : 1;
   static_assert(kEnds >= 1 && kACols + kEnds * kR <= kHalfCols, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -317,8 +320,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool some = left > 0;
     bool first = true;
     for (int n = 0; left > 0; --left, ++n) {
-      if (n % (4 / kGroups) == 0) groups.refill();
-      expect(bar, &full[slot], phase);
 #pragma unroll
       for (int h = 0; h < kSteps; ++h) {
         auto values = [&](int c, uint32_t (&v)[16]) {   // of chunk c of the step
@@ -334,23 +335,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           w4_values<Half>(w.z, o, v + 8);
           w4_values<Half>(w.w, o, v + 12);
         };
-        {
-          uint32_t ahead[kAhead][16];
+        if (h > 0 || !first) {
+          expect(d_bar, &d_ready[half], turn ^ 1u);
+          tc_fence_after();
+          add();
+        }
+        if (h == 0) {
+          if (n % (4 / kGroups) == 0) groups.refill();
+          expect(bar, &full[slot], phase);
+        }
 #pragma unroll
-          for (int c = 0; c < kAhead; ++c) values(c, ahead[c]);
-          if (h > 0 || !first) {
-            expect(d_bar, &d_ready[half], turn ^ 1u);
-            tc_fence_after();
-            add();
-          }
-#pragma unroll
-          for (int c = 0; c < kAhead; ++c) tc_st16(my_tmem + c * 16, ahead[c]);
-#pragma unroll
-          for (int c = kAhead; c < kChunks; ++c) {
-            uint32_t v[16];
-            values(c, v);
-            tc_st16(my_tmem + c * 16, v);
-          }
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t v[16];
+          values(c, v);
+          tc_st16(my_tmem + c * 16, v);
         }
 #pragma unroll
         for (int q = 0; q < kEnds; ++q) {   // a group past the contraction has products with zeros
@@ -464,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <bool Half, int kGroup, int kR>
 int launch(const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int64_t tiles, cudaStream_t s) {
   auto* kernel = grouped_w4_kernel<Half, kGroup, kR>;
-  constexpr int kSmem = ring_bytes(kR);
+  constexpr int kSmem = ring_bytes(kGroup, kR);
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -497,7 +495,10 @@ int launch_rows(int R, const CUtensorMap& tw, const CUtensorMap& tx, const W4Par
   return launch<Half, kGroup, 32>(tw, tx, p, tiles, s);
 }
 
+// R: rows of a tile, 16, 32 or 64; at most 32 with scales of 32 values, whose sums
+// have no room for more.
 int launch_grouped_w4_many(const W4Args& a, int R, cudaStream_t s) {
+  if (a.group == 32) R = std::min(R, 32);
   W4Params p;
   p.start = a.start;
   p.psum = a.psum;
@@ -564,18 +565,19 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Which form, by the mean rows of an expert with rows and the weights read.
   // Up to four rows mma.sync is the faster (64 experts of 2048 x 4096 with 1, 2 and
-  // 4 rows: 41, 54 and 63 us, here 52, 65 and 72), from eight on this form (76
-  // there, 72 here); with fewer weights its few large tiles leave SMs idle longer:
-  // 8 experts of 4096 x 4096 take 26 us there and 30 here with 8 rows, 39 and 32
-  // with 16; of 1024 x 1024 5.4 and 8.7 with 8, 9.4 and 11.5 with 32.
+  // 4 rows: 41, 53 and 62 us, here 48, 58 and 67), from six on this form (69 there,
+  // 68 here; with 8 rows 83 and 68); with fewer weights its few large tiles leave SMs
+  // idle longer: 8 experts of 4096 x 4096 take 26 us there and 27 here with 8 rows, 39
+  // and 30 with 16, 32 of 2048 x 4096 with 8 in groups of 64 52 and 47; 8 of 1024 x
+  // 1024 5.4 and 8.1 with 8, 9.9 and 11.4 with 32.
   const int64_t weights = live * N * Kd;
   const int64_t scale_bytes = 32ll * moe::w4_few_pitch(Kd / group) * 3;
-  if ((mean <= 4 || (mean <= 8 && weights <= (1ll << 28)) || (mean <= 32 && weights <= (1ll << 23))) &&
+  if ((mean <= 4 || (mean <= 8 && weights <= (1ll << 27)) || (mean <= 32 && weights <= (1ll << 23))) &&
       scale_bytes <= moe::kW4FewScaleBytes)
     return moe::launch_grouped_w4_few(a, s);
-  // Rows of a tile: 64 experts of 2048 x 4096 with 8 rows each take 72, 76 and 79
-  // us with 16, 32 and 64, with 16 rows 92, 78 and 80, with 32 rows 151, 100 and 84;
-  // scales of 32 values (64 rows of their sums do not fit) 89 and 114 us with 8
-  // rows, 179 and 157 with 32.
-  return moe::launch_grouped_w4_many(a, mean <= 12 ? 16 : (mean <= 24 || group == 32 ? 32 : 64), s);
+  // Rows of a tile: 64 experts of 2048 x 4096 with 8 rows each take 68, 71 and 77
+  // us with 16, 32 and 64, with 16 rows 86, 72 and 78, with 32 rows 141, 92 and 82;
+  // scales of 32 values (64 rows of their sums do not fit) 84 and 91 us with 8
+  // rows, 171 and 135 with 32.
+  return moe::launch_grouped_w4_many(a, mean <= 12 ? 16 : (mean <= 24 ? 32 : 64), s);
 }

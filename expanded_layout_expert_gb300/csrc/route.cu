@@ -21,7 +21,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxK = 32;
 constexpr int kMaxE = 1024;
 constexpr uint32_t kAll = 0xffffffffu;
