@@ -11,10 +11,11 @@
 // heads, and the chosen one's run moves up.
 //
 // Bytes: a row's logits and 8K (12K and twice the logits back). The instructions
-// of a row set the time, not the bytes: 32768 x 160 fp32, K = 8, take 17 us (1.4
-// TB/s; issue slots 85 % busy), their gradient 10.7 us (4.1 TB/s, 61 % of HBM).
-// Every key searched again each round took 36 us, one sorted run of 5 by a warp
-// 19; 1024 experts in runs of 4, 19 us for 5120 rows, were 30 unsorted.
+// of a row set the time, not the bytes: 32768 x 160 fp32, K = 8, sigmoid, take 15.0 us
+// (1.5 TB/s; issue slots 65 % busy, the pipe of comparisons and selects 62 %), their
+// softmax gradient 10.5 us (4.2 TB/s). Every key searched again each round took 36 us,
+// one sorted run of 5 by a warp 19, runs by 8 lanes in blocks of 256 threads 17; 1024
+// experts, 5120 rows, took 30 us unsorted and 18 in runs of 4.
 #include "dtype16.cuh"
 #include "host_util.h"
 
@@ -379,19 +380,22 @@ extern "C" int moe_route_topk(const void* logits, int64_t ld, int dtype, const f
       logits, ld, dtype, bias, d_n_valid, T, E, K, score == MOE_SCORE_SIGMOID, renormalize != 0, \
       factor, topk_ids, topk_w)
   // 8 lanes a row save instructions, a warp time where all rows run at once (8
-  // and 32 lanes, K = 8: 1024 x 64 3.7 and 2.7 us, 4096 x 32 3.3 and 3.6, 4096 x 64
-  // 3.9 and 3.7, 16384 x 64 5.8 and 8.3, 8192 x 96 5.1 and 5.6, 32768 x 96 12.4 and
-  // 15.4, x 128 17.1 and 16.5, x 160 17.0 and 18.9, x 192 22.0 and 21.6).
-  const int64_t sms = moe::device_sm_count();
-  const int64_t enough = E <= 64 ? 24 * sms : (E <= 96 ? 48 * sms : 128 * sms);
-  if (K > 8 || T < enough || E > 160 || (E > 96 && E <= 128))
+  // and 32 lanes, K = 8: 1024 x 64 3.5 and 2.7 us, 4096 x 32 3.3 and 3.5, 4096 x 64
+  // 3.9 and 3.6, 16384 x 64 5.6 and 8.3, 4096 x 96 4.4 and 3.7, 8192 x 96 5.0 and 5.7,
+  // 16384 x 160 10.1 and 10.9, 32768 x 128 14.8 and 16.4, x 192 20.7 and 21.4).
+  const int64_t enough = (E <= 64 ? 24 : 48) * static_cast<int64_t>(moe::device_sm_count());
+  if (K > 8 || E > 192 || T < enough)
     MOE_WIDE(E, LAUNCH);
   else if (E <= 64)
     MOE_NARROW(E, LAUNCH);
   else if (E <= 96)
     LAUNCH(8, 12);
-  else
+  else if (E <= 128)
+    LAUNCH(8, 16);
+  else if (E <= 160)
     LAUNCH(8, 20);
+  else
+    LAUNCH(8, 24);
 #undef LAUNCH
   return moe::check_launch("route_topk_kernel");
 }
@@ -420,9 +424,9 @@ extern "C" int moe_route_topk_backward(const float* dtopk_w, const void* logits,
                                               reinterpret_cast<cudaStream_t>(stream)>>>(          \
       dtopk_w, logits, ld, dtype, topk_ids, d_n_valid, T, E, K, score == MOE_SCORE_SIGMOID,       \
       renormalize != 0, factor, dlogits, ld_d)
-  // as above (8 and 32 lanes, K = 8: 1024 x 64 3.3 and 3.1 us, 4096 x 64 3.4 and 3.6,
-  // 2048 x 128 4.0 and 3.2, 8192 x 128 4.6 and 5.4, 4096 x 256 5.4 and 4.6, 8192 x
-  // 256 6.6 and 6.8, 32768 x 160 10.7 and 15.0)
+  // as above (8 and 32 lanes, K = 8: 1024 x 64 3.1 and 3.0 us, 4096 x 64 3.3 and 3.5,
+  // 2048 x 128 3.7 and 3.1, 8192 x 128 4.6 and 5.4, 4096 x 256 5.4 and 4.2, 8192 x
+  // 256 6.4 and 6.4, 32768 x 160 10.5 and 15.0)
   const int64_t sms = moe::device_sm_count();
   const int64_t enough = E <= 64 ? 16 * sms : (E <= 128 ? 24 * sms : 48 * sms);
   if (K > 8 || E > 256 || T < enough)

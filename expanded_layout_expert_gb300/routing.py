@@ -128,7 +128,7 @@ def combine_rows_backward(dy: torch.Tensor, rows: torch.Tensor, lay,
     if drows is None:
         drows = _new(torch.zeros, (lay.M_cap, H), dy.dtype, dy, stream)
     if dtopk_w is None:
-        dtopk_w = _new(torch.zeros, (T, K), torch.float32, dy, stream)
+        dtopk_w = _new(torch.empty if n_valid is None else torch.zeros, (T, K), torch.float32, dy, stream)
     yp, ld_y = _rows(dy, "dy", T, H, dy.dtype, dev)
     rp, ld_r = _rows(rows, "rows", lay.M_cap, H, dy.dtype, dev)
     dp, ld_d = _rows(drows, "drows", lay.M_cap, H, dy.dtype, dev)

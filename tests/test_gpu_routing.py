@@ -129,7 +129,7 @@ def test_route(mx, E, K, dtype, score, renormalize, biased):
 @pytest.mark.parametrize("score,renormalize", [("softmax", False), ("sigmoid", True)])
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("E,K", [(1, 1), (8, 2), (15, 4), (31, 8), (48, 6), (64, 8), (65, 8), (96, 1), (97, 8), (128, 7),
-                                 (129, 8), (160, 8), (161, 8), (192, 8), (256, 8), (64, 9), (512, 8), (768, 3)])
+                                 (129, 8), (160, 8), (161, 8), (192, 8), (193, 8), (256, 8), (64, 9), (512, 8), (768, 3)])
 def test_route_rows_for_eight_lanes(mx, E, K, dtype, score, renormalize):
     """Rows enough for the forms in which a warp takes four at a time, a last part of a warp's among them."""
     check_route(mx, 20001, E, K, dtype, score, renormalize, E % 2 == 0)
