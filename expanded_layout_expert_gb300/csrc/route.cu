@@ -425,11 +425,10 @@ extern "C" int moe_route_topk_backward(const float* dtopk_w, const void* logits,
       dtopk_w, logits, ld, dtype, topk_ids, d_n_valid, T, E, K, score == MOE_SCORE_SIGMOID,       \
       renormalize != 0, factor, dlogits, ld_d)
   // as above (8 and 32 lanes, K = 8: 1024 x 64 3.1 and 3.0 us, 4096 x 64 3.3 and 3.5,
-  // 2048 x 128 3.7 and 3.1, 8192 x 128 4.6 and 5.4, 4096 x 256 5.4 and 4.2, 8192 x
-  // 256 6.4 and 6.4, 32768 x 160 10.5 and 15.0)
-  const int64_t sms = moe::device_sm_count();
-  const int64_t enough = E <= 64 ? 16 * sms : (E <= 128 ? 24 * sms : 48 * sms);
-  if (K > 8 || E > 256 || T < enough)
+  // 2048 x 128 3.7 and 3.1, 4096 x 128 4.0 and 3.7, 8192 x 128 4.6 and 5.4, 32768 x 160
+  // 10.5 and 15.0, but 8192 x 256 6.4 and 6.4)
+  const int64_t enough = (E <= 64 ? 16 : 32) * static_cast<int64_t>(moe::device_sm_count());
+  if (K > 8 || E > 192 || T < enough)
     MOE_WIDE(E, LAUNCH);
   else if (E <= 64)
     MOE_NARROW(E, LAUNCH);
@@ -439,10 +438,8 @@ extern "C" int moe_route_topk_backward(const float* dtopk_w, const void* logits,
     LAUNCH(8, 16);
   else if (E <= 160)
     LAUNCH(8, 20);
-  else if (E <= 192)
-    LAUNCH(8, 24);
   else
-    LAUNCH(8, 32);
+    LAUNCH(8, 24);
 #undef LAUNCH
   return moe::check_launch("route_topk_backward_kernel");
 }
