@@ -224,6 +224,7 @@ extern "C" int moe_combine_rows(const void* rows, int64_t ld_rows, int dtype, co
               "moe_combine_rows: rows, residual and out must be 16-byte aligned");
   MOE_REQUIRE(residual != out || residual == nullptr || ld_res == ld_out,
               "moe_combine_rows: in place needs the same row stride for residual and out");
+  MOE_REQUIRE(rows != out || T == 0 || M_cap == 0, "moe_combine_rows: out must not be rows");
   MOE_REQUIRE_DEVICE();
   if (T == 0) return MOE_OK;
   // warps for a token: one where there are tokens for every warp that fits, up to
@@ -264,6 +265,7 @@ extern "C" int moe_combine_rows_backward(const void* dy, int64_t ld_dy, const vo
   const int64_t pad_per_expert = (align - 1 + moe::kPadRowsPerBlock - 1) / moe::kPadRowsPerBlock;
   const int64_t pad = M_cap == 0 ? 0 : pad_per_expert * E;
   MOE_REQUIRE(pad < (1ll << 30), "moe_combine_rows_backward: grid too large");
+  MOE_REQUIRE(dy != drows || T == 0 || M_cap == 0, "moe_combine_rows_backward: drows must not be dy");
   MOE_REQUIRE_DEVICE();
   const int nvec = H / 8;
   const int64_t most = static_cast<int64_t>(moe::device_sm_count()) * (2048 / moe::kThreads) * 8;

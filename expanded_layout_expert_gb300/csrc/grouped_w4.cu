@@ -557,6 +557,7 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
   const int64_t mean = live > 0 ? (max_rows + live - 1) / live : 0;
   MOE_REQUIRE((max_rows / 8 + live) * ((N + 31) / 32) <= INT32_MAX,
               "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
+  MOE_REQUIRE(x != out || max_rows == 0, "moe_grouped_mm_w4: out must not be x");
   MOE_REQUIRE_DEVICE();
   if (max_rows == 0) return MOE_OK;
   const moe::W4Args a = {x,  ld_x, codes, scales,   zeros, group,

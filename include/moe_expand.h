@@ -527,7 +527,7 @@ int moe_route_topk_backward(const float* dtopk_w, const void* logits, int64_t ld
  * NULL: 1). Other rows of out are not written. A token without pairs gets its
  * residual. The weight of a k without a pair is not used, whatever it is.
  *   rows     device 16-bit [M_cap, ld_rows >= H] of dtype; residual, out [T, ld >= H]
- *            of the same; out may be residual itself (same stride)
+ *            of the same; out may be residual itself (same stride), not rows
  * H and the strides are multiples of 8, pointers 16-byte aligned, K <= 32. A
  * row >= M_cap is skipped and sets MOE_ERR_DEVICE_CHECK.
  */
@@ -544,7 +544,8 @@ int moe_combine_rows(const void* rows, int64_t ld_rows, int dtype, const float* 
  * moe_expand_rows does. Other rows are not written. drows may be rows itself
  * (same stride): a place is read before it is written. src2dst names a row
  * once, as moe_expand_layout's does.
- *   dy [T, ld_dy >= H], rows, drows [M_cap, ld >= H]: device 16-bit of dtype;
+ *   dy [T, ld_dy >= H], rows, drows [M_cap, ld >= H]: device 16-bit of dtype,
+ *   drows not dy;
  *   dtopk_w device fp32 [T, K]
  */
 int moe_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, int64_t ld_rows,
@@ -565,7 +566,7 @@ int moe_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, i
  *   scales   device, of dtype, [E, N, Kd/group]; group 32, 64 or 128
  *   zeros    device uint8 [E, N, Kd/group], values 0 to 15 (only the low four
  *            bits are used); NULL: 8 everywhere
- *   x, out   16-bit of dtype, [M_cap, ld >= Kd] and [M_cap, ld >= N]
+ *   x, out   16-bit of dtype, [M_cap, ld >= Kd] and [M_cap, ld >= N], not the same
  *   max_rows as in moe_grouped_mm
  * N and the row strides are multiples of 8, Kd a multiple of group, pointers
  * 16-byte aligned (zeros: 8), E <= 1024.

@@ -82,6 +82,7 @@ def test_combine_refuses(capi, p):
     _refused(capi, call(res=p, ld_r=60), "strides")
     _refused(capi, call(rows=p + 8), "aligned")
     _refused(capi, call(out=p + 4096, res=p + 4096, ld_r=72), "in place")
+    _refused(capi, call(), "out must not be rows")
 
     def back(dy=p, rows=p, ld=64, dt=1, src=p, psum=p, T=4, H=64, K=2, E=4, align=1, M=8, drows=p + 4096, ld_d=64,
              dw=p):
@@ -99,6 +100,7 @@ def test_combine_refuses(capi, p):
     _refused(capi, back(drows=p, ld_d=72), "in place")
     _refused(capi, back(drows=p + 4), "aligned")
     _refused(capi, back(E=1 << 20, align=1 << 20), "grid too large")
+    _refused(capi, back(drows=p), "drows must not be dy")
 
 
 def test_w4_refuses(capi, p):
@@ -125,6 +127,7 @@ def test_w4_refuses(capi, p):
     _refused(capi, call(codes=p + 8), "aligned")
     _refused(capi, call(out=p + 2), "aligned")
     _refused(capi, call(N=1 << 30, K=64, ld=1 << 30, M=1 << 30, most=1 << 30), "32-bit")
+    _refused(capi, call(), "out must not be x")
 
 
 def test_python_refuses():
