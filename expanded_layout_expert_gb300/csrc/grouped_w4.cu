@@ -7,7 +7,7 @@
 // The weights are the tensor core's first operand, read from tensor memory:
 //   D[i, r] = sum_c W[i, c] X[r, c],
 // a tile being 256 weight rows, 128 to each of two warpgroups, by kR activation
-// rows (32 or 64) of one expert. TMA brings 128 contracted values at a time, 64
+// rows (16 to 64) of one expert. TMA brings 128 contracted values at a time, 64
 // bytes of codes a weight row and the rows of x; a thread takes one weight row,
 // makes its codes 16-bit values (w4.cuh: exact) and stores them into its lane of
 // tensor memory. Each scale group has sums of its own there, which the thread
@@ -18,15 +18,16 @@
 // 350 instructions of each of four warps, half of them the making of the values,
 // on four schedulers, each step a chain from the sums to the values, the barrier and
 // the products; the four warpgroups of an SM cover for each other (a CTA alone takes
-// 0.83 us a block, two 1.07). 64 experts of 4096 x 7168 with 32 rows each take 234 us
-// (4.4 TB/s), with 8 rows 198 (5.0 TB/s).
+// 0.83 us a block, two 1.07). 64 experts of 4096 x 7168 with 32 rows each take 224 us
+// (4.6 TB/s), with 8 rows 198 (5.0 TB/s).
 // What got there, in us for 32 rows: one CTA of four dequantising warps, a TMA
 // and an MMA warp, sums waited for at once 490; the next values made meanwhile
 // 386; no warps of their own for the loads and products, which poll for their
 // turn with half of all instructions, 374; the operands of those known to be
 // uniform 300; 256 rows a CTA, so that four stages fit, 279; the warpgroups'
 // barriers apart 249; the loop's arithmetic off the uniform pipe 245; sums first and
-// then the values, in few registers, 243; the scales moved up between them 234.
+// then the values, in few registers, 243; the scales moved up between them 234;
+// tiles of 48 rows for them instead of 64 224.
 // Eight warps for 128 rows, three CTAs, were slower (362), and so were sums fetched
 // while the next values are made (267) and the contraction split in two for fuller
 // waves (279): the start of a CTA takes 7 us.
@@ -57,15 +58,16 @@ constexpr int kTmemCols = 2 * kHalfCols;
 
 // Contracted values of a step, a batch of products: their sums, of every scale
 // group apart, have 64 columns.
-constexpr int step_k(int group, int R) { return 64 * group / R < 128 ? 64 * group / R : 128; }
+constexpr int step_k(int group, int R) { return 64 / R * group < 128 ? 64 / R * group : 128; }
 
 constexpr int stage_bytes(int R) { return kCodeBytes + R * BC * 2; }
 // What the ring takes is lost to L1, where the scales' sectors wait for their next
 // use, so the more scales a row has, the fewer stages (20 rows each for 64 experts of
 // 4096 x 7168 take, with 4 and 3 stages, 213 and 213 us in groups of 128, 254 and 234
 // in groups of 64, 408 and 286 in groups of 32; 8 rows 198 and 203, 226 and 220, 251
-// and 236; five stages for 8 rows in groups of 32, 332). Two stages are too few (364).
-constexpr int stages_for(int group, int R) { return group <= 2 * R ? 3 : 4; }
+// and 236; five stages for 8 rows in groups of 32, 332). Two stages are too few (364), and
+// for more than 32 rows two CTAs have no room for four.
+constexpr int stages_for(int group, int R) { return R > 32 || group <= 2 * R ? 3 : 4; }
 constexpr int ring_bytes(int group, int R) { return stages_for(group, R) * stage_bytes(R) + 1024; }
 
 struct W4Params {
@@ -490,12 +492,14 @@ template <bool Half, int kGroup>
 int launch_rows(int R, const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int64_t tiles,
                 cudaStream_t s) {
   if (R <= 16) return launch<Half, kGroup, 16>(tw, tx, p, tiles, s);
-  if constexpr (kGroup > 32)
-    if (R > 32) return launch<Half, kGroup, 64>(tw, tx, p, tiles, s);
+  if constexpr (kGroup > 32) {
+    if (R > 48) return launch<Half, kGroup, 64>(tw, tx, p, tiles, s);
+    if (R > 32) return launch<Half, kGroup, 48>(tw, tx, p, tiles, s);
+  }
   return launch<Half, kGroup, 32>(tw, tx, p, tiles, s);
 }
 
-// R: rows of a tile, 16, 32 or 64; at most 32 with scales of 32 values, whose sums
+// R: rows of a tile, 16, 32, 48 or 64; at most 32 with scales of 32 values, whose sums
 // have no room for more.
 int launch_grouped_w4_many(const W4Args& a, int R, cudaStream_t s) {
   if (a.group == 32) R = std::min(R, 32);
@@ -577,8 +581,9 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
       scale_bytes <= moe::kW4FewScaleBytes)
     return moe::launch_grouped_w4_few(a, s);
   // Rows of a tile: 64 experts of 2048 x 4096 with 8 rows each take 68, 71 and 77
-  // us with 16, 32 and 64, with 16 rows 86, 72 and 78, with 32 rows 141, 92 and 82;
-  // scales of 32 values (64 rows of their sums do not fit) 84 and 91 us with 8
-  // rows, 171 and 135 with 32.
-  return moe::launch_grouped_w4_many(a, mean <= 12 ? 16 : (mean <= 24 ? 32 : 64), s);
+  // us with 16, 32 and 64, with 16 rows 86, 72 and 78; with 32 rows 91, 79 and 81 with
+  // 32, 48 and 64 (in groups of 64 101, 91 and 102), with 26 rows 73, 78 and 81, with
+  // 44 rows 121, 92 and 84; scales of 32 values (more rows of their sums do not fit) 84
+  // and 91 us with 8 rows in tiles of 16 and 32, 171 and 135 with 32.
+  return moe::launch_grouped_w4_many(a, mean <= 12 ? 16 : (mean <= 26 ? 32 : (mean <= 40 ? 48 : 64)), s);
 }

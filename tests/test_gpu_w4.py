@@ -120,8 +120,9 @@ def test_rows_of_one_expert(mx, rows, group):
 
 
 # rows of six experts, with more weights than the form for few rows takes: tiles of
-# 16, 32 and 64 rows, one and several of them, and experts without rows
-CROWDS = {"16": [10, 0, 3, 40, 1, 6], "32": [16, 33, 0, 17, 30, 9], "64": [64, 5, 130, 0, 65, 31]}
+# 16, 32, 48 and 64 rows, one and several of them, and experts without rows
+CROWDS = {"16": [10, 0, 3, 40, 1, 6], "32": [16, 33, 0, 17, 30, 9],
+          "48": [48, 33, 97, 0, 19, 13], "64": [64, 5, 130, 0, 65, 31]}
 
 
 @pytest.mark.parametrize("zeros", [False, True], ids=["", "zeros"])
@@ -133,7 +134,8 @@ def test_more_rows(mx, rows, N, Kd, group, dtype, zeros):
     """Sizes that end inside tiles, stages and steps."""
     counts = CROWDS[rows]
     mean = -(-sum(counts) // len(counts))
-    assert len(counts) * N * Kd > 1 << 23 and (mean <= 12) == (rows == "16") and (mean > 24) == (rows == "64")
+    tile = "16" if mean <= 12 else "32" if mean <= 26 else "48" if mean <= 40 else "64"
+    assert len(counts) * N * Kd > 1 << 23 and tile == rows
     check(mx, counts, N, Kd, group, dtype, zeros, align=8, slack=2, pairs=sum(counts), seed=len(rows))
 
 
