@@ -263,8 +263,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     // A wait that gave up, here or in another warp, ends the waits and the loads;
     // the rest of the loop goes on with whatever there is, and nothing is stored.
     bool got = true;
+    // The lanes leave it together: what follows wants the whole warp (the loads and
+    // stores of tensor memory are .aligned), and before it one lane may have issued
+    // products or copies.
     auto expect = [&](uint32_t bar, uint64_t* at, uint32_t parity) {
-      if (got) got = wait(bar, at, parity);
+      if (got)
+        got = wait(bar, at, parity);
+      else
+        __syncwarp();
     };
     // By one lane. The copies are few, because the warp that asks for them keeps
     // the other three waiting: 256 rows of codes at once where all are the
