@@ -257,20 +257,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool both = i0 + kHalf < p.N;   // else the second warpgroup has no rows
     const int half = warp >> 2, row = threadIdx.x & (kHalf - 1);
     const uint32_t bars = smem_u32(full), d_bar = smem_u32(&d_ready[half]);
-    auto wait = [&](uint32_t bar, uint64_t* at, uint32_t parity) {
-      return try_wait(bar, parity) || mbar_wait_warp(at, parity, abort_flag, p.status);
-    };
     // A wait that gave up, here or in another warp, ends the waits and the loads;
     // the rest of the loop goes on with whatever there is, and nothing is stored.
+    // The first test is made all the same: the lanes meet in it, as what follows wants
+    // them to (the loads and stores of tensor memory are .aligned), after one of them
+    // has issued products or copies.
     bool got = true;
-    // The lanes leave it together: what follows wants the whole warp (the loads and
-    // stores of tensor memory are .aligned), and before it one lane may have issued
-    // products or copies.
     auto expect = [&](uint32_t bar, uint64_t* at, uint32_t parity) {
-      if (got)
-        got = wait(bar, at, parity);
-      else
-        __syncwarp();
+      const bool there = try_wait(bar, parity);
+      if (!there && got) got = mbar_wait_warp(at, parity, abort_flag, p.status);
     };
     // By one lane. The copies are few, because the warp that asks for them keeps
     // the other three waiting: 256 rows of codes at once where all are the

@@ -26,11 +26,13 @@ def block(text, at):
 
 def test_lanes_meet_before_tensor_memory_is_read_or_written():
     """Loads and stores of tensor memory are warp-wide. One lane issues the
-    products and copies of a step before; the wait after it makes the lanes meet,
-    also once a wait has given up and is not taken any more."""
+    products and copies of a step before; the test of the barrier after it makes the
+    lanes meet, also once a wait has given up."""
     text = kernel()
     expect = block(text, text.index("auto expect ="))
-    assert re.fullmatch(r"\{\s*if \(got\)\s*got = wait\(bar, at, parity\);\s*else\s*__syncwarp\(\);\s*\}", expect)
+    assert re.match(r"\{\s*const bool there = try_wait\(bar, parity\);", expect)
+    source = code(NAME)
+    assert re.search(r"return __all_sync\(0xffffffffu, \w+ != 0\);\s*\}$", block(source, source.index("bool try_wait(")))
     sums = list(re.finditer(r"\badd\(\);", text))
     assert len(sums) == 2   # of the loop and after it
     for m in sums:
@@ -52,3 +54,4 @@ def test_cluster_barriers_and_tmem_release():
         assert "__syncwarp();" in function_body(text, m.start())[-100:]
         seen += 1
     assert seen == 1
+
