@@ -69,6 +69,19 @@ constexpr int stage_bytes(int R) { return kCodeBytes + R * BC * 2; }
 // for more than 32 rows two CTAs have no room for four.
 constexpr int stages_for(int group, int R) { return R > 32 || group <= 2 * R ? 3 : 4; }
 constexpr int ring_bytes(int group, int R) { return stages_for(group, R) * stage_bytes(R) + 1024; }
+// Two CTAs an SM is the most, because tensor memory has room for no third: nothing
+// counts its columns when a CTA is placed, and an allocation waits for them without
+// a limit, for CTAs perhaps that wait for their cluster's others behind it. Shared memory is
+// counted, so every CTA takes enough of the SM's 228 KB (1 KB of them its own
+// overhead) that no third fits, nor one of the 16-bit product for few rows (97 KB and up
+// to 128 columns) beside two. The other kernels with tensor memory take all registers. It
+// costs tiles of 16 rows in groups of 32 some L1 (64 experts of 4096 x 7168, 8 rows
+// each: 230 -> 236 us), the others nothing.
+constexpr int kMinSmem = 77 * 1024;
+constexpr int smem_bytes(int group, int R) {
+  return ring_bytes(group, R) > kMinSmem ? ring_bytes(group, R) : kMinSmem;
+}
+static_assert(512 / kTmemCols == 2 && 3 * (kMinSmem + 1024) > 228 * 1024, "two CTAs an SM at most");
 
 struct W4Params {
   const int32_t* start;
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <bool Half, int kGroup, int kR>
 int launch(const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int64_t tiles, cudaStream_t s) {
   auto* kernel = grouped_w4_kernel<Half, kGroup, kR>;
-  constexpr int kSmem = ring_bytes(kGroup, kR);
+  constexpr int kSmem = smem_bytes(kGroup, kR);
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);

@@ -55,3 +55,43 @@ def test_cluster_barriers_and_tmem_release():
         seen += 1
     assert seen == 1
 
+
+def constants(name, *wanted):
+    """The source's one-line constants and the named functions, as C++."""
+    text = code(name)
+    lines = re.findall(r"^constexpr int \w+ = [\w *+/()]+;", text, re.M)
+    for f in wanted:
+        m = re.search(rf"^(?:constexpr )?int {f}\([^)]*\) ", text, re.M)
+        lines.append(m.group(0) + block(text, m.end() - 1))
+    return "\n".join(lines)
+
+
+def test_ctas_of_an_sm_find_room_in_tensor_memory(tmp_path):
+    """What may lie on an SM together, by shared memory alone, holds at most 512
+    columns: an allocation that waits has no limit, and CTAs of clusters that wait
+    for one another would then wait for ever."""
+    import itertools
+    import subprocess
+    launch = code(NAME)[code(NAME).index("int launch("):]
+    f = re.search(r"constexpr int kSmem = (\w+)\(kGroup, kR\);", launch).group(1)
+    wanted = ["step_k", "stage_bytes", "stages_for", "ring_bytes"] + ([f] if f != "ring_bytes" else [])
+    src = tmp_path / "smem.cpp"
+    src.write_text(f"""#include <cstdio>
+namespace w4 {{ {constants(NAME, *wanted)} }}
+namespace few {{ {constants("grouped_mm16_few.cu", "stages_for", "ring_bytes")} }}
+int main() {{
+  for (int g = 32; g <= 128; g *= 2)
+    for (int R = 16; R <= (g == 32 ? 32 : 64); R += 16)
+      std::printf("%d %d\\n", w4::{f}(g, R), w4::kTmemCols);
+  for (int R = 16; R <= 128; R *= 2) std::printf("%d %d\\n", few::ring_bytes(R), R < 32 ? 32 : R);
+}}
+""")
+    exe = tmp_path / "smem"
+    subprocess.run(["g++", "-std=c++17", "-w", str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    ctas = sorted({tuple(map(int, line.split())) for line in out.splitlines()})
+    assert len(ctas) >= 8 and {c for _, c in ctas} == {32, 64, 128, 256}
+    for n in (2, 3, 4):
+        for some in itertools.combinations_with_replacement(ctas, n):
+            if sum(b + 1024 for b, _ in some) <= 228 * 1024:   # 1 KB a CTA is the system's
+                assert sum(c for _, c in some) <= 512, some
