@@ -84,6 +84,8 @@ SIGNATURES = {
     "moe_grouped_mm_w4": (I32, [P, I64, P, P, P, I32, P, P, I32, I32, I32, I32, I64, I64, P, I64, P, P]),
     "moe_gemm_set_trace": (I32, [P]),
     "moe_selftest_bounded_wait": (I32, [I64, P, P, P]),
+    "moe_selftest_w4_wait": (I32, [P, I64, P, P, P, P, P, I32, I32, I32, I64, I64, P, I64, I64, I32, I32, P,
+                                   P]),
     "moe_last_error_string": (C.c_char_p, []),
     "moe_device_supported": (I32, [I32]),
 }

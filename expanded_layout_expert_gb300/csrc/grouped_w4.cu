@@ -83,6 +83,12 @@ constexpr int smem_bytes(int group, int R) {
 }
 static_assert(512 / kTmemCols == 2 && 3 * (kMinSmem + 1024) > 228 * 1024, "two CTAs an SM at most");
 
+// A copy that is left out: that of stage `block` of CTA `cta`; and how long waits wait.
+struct W4Drop {
+  long long limit;
+  int cta, block;
+};
+
 struct W4Params {
   const int32_t* start;
   const int32_t* psum;
@@ -97,6 +103,7 @@ struct W4Params {
   uint16_t* out;
   int64_t ld_out;
   int32_t* status;
+  W4Drop drop = {};       // read by the kernel that moe_selftest_w4_wait runs, alone
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands, K = 16. B's descriptor comes
@@ -204,7 +211,8 @@ MOE_DEV bool elect_one() {
   return one != 0;
 }
 
-template <bool Half, int kGroup, int kR>
+// kDrop: one copy is left out (p.drop), so that the wait for it runs out.
+template <bool Half, int kGroup, int kR, bool kDrop = false>
 __global__ void __launch_bounds__(kThreads, 2)
     grouped_w4_kernel(const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmX, const W4Params p) {
@@ -220,7 +228,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t full[kStages], d_ready[2], done[2];
+  // full[s]: the barrier of a place in the ring; full[kStages + s]: the stages up to the
+  // last one asked for there, of this CTA's
+  __shared__ uint64_t full[2 * kStages], d_ready[2], done[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_used[kStages];
   __shared__ int s_warp_sum[kThreads / 32], s_found[3];
@@ -237,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       s_used[s] = 0;
+      full[kStages + s] = 0;
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&d_ready[h], 1);
@@ -278,12 +289,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool got = true;
     auto expect = [&](uint32_t bar, uint64_t* at, uint32_t parity) {
       const bool there = try_wait(bar, parity);
-      if (!there && got) got = mbar_wait_warp(at, parity, abort_flag, p.status);
+      if (!there && got)
+        got = mbar_wait_warp(at, parity, abort_flag, p.status, kDrop ? p.drop.limit : kWaitLimitCycles);
     };
     // By one lane. The copies are few, because the warp that asks for them keeps
     // the other three waiting: 256 rows of codes at once where all are the
     // expert's, and all of the tile's rows of x, needed or not.
     auto load = [&](int b, int stage) {
+      if (kDrop && static_cast<int>(blockIdx.x) == p.drop.cta && b - b0 == p.drop.block) return;
+      full[kStages + stage] = static_cast<uint32_t>(b - b0 + 1);
       uint8_t* sw = smem + stage * kStageBytes;
       uint8_t* sx = sw + kCodeBytes;
       const uint32_t bar = smem_u32(&full[stage]);
@@ -420,13 +434,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_before();
     }
     const bool stop = __syncthreads_or(!got);   // the ring is free: every product is done
-    if (stop && row == 0) {
-      // what is under way has landed before the CTA can exit
-      tc_commit(&done[half]);
-      drain_wait(&done[half], 0);
-      const int asked = b1 - b0 - max(to_load, 0);
-      for (int s = 0; s < kStages && s < asked; ++s)
-        drain_wait(&full[s], static_cast<uint32_t>((asked - 1 - s) / kStages) & 1u);
+    if (stop) {
+      // Nothing of this CTA is under way when it exits or gives back its tensor memory:
+      // neither products, a warpgroup's all being one lane's (elect.sync's choice is the
+      // same every time), nor copies. Of those a place has one under way at most, and
+      // none behind one that was left out, for the next is asked for by a warp that has
+      // waited for the one before.
+      if ((warp & 3) == 0 && elect_one()) {
+        tc_commit(&done[half]);
+        drain_wait(&done[half], 0);
+      }
+      if (warp == 1 && elect_one())
+        for (int s = 0; s < kStages; ++s) {
+          const int upto = static_cast<int>(full[kStages + s]);
+          if (upto > 0 && !drain_wait(&full[s], static_cast<uint32_t>((upto - 1) / kStages) & 1u)) break;
+        }
     }
     uint16_t* out = p.out + static_cast<int64_t>(row0) * p.ld_out + i;
     float* part = reinterpret_cast<float*>(smem);
@@ -475,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <bool Half, int kGroup, int kR>
+template <bool Half, int kGroup, int kR, bool kDrop = false>
 int launch(const CUtensorMap& tw, const CUtensorMap& tx, const W4Params& p, int64_t tiles, cudaStream_t s) {
-  auto* kernel = grouped_w4_kernel<Half, kGroup, kR>;
+  auto* kernel = grouped_w4_kernel<Half, kGroup, kR, kDrop>;
   constexpr int kSmem = smem_bytes(kGroup, kR);
   static std::atomic<bool> attr_set[64];
   int dev = 0;
@@ -514,8 +536,8 @@ int launch_rows(int R, const CUtensorMap& tw, const CUtensorMap& tx, const W4Par
 }
 
 // R: rows of a tile, 16, 32, 48 or 64; at most 32 with scales of 32 values, whose sums
-// have no room for more.
-int launch_grouped_w4_many(const W4Args& a, int R, cudaStream_t s) {
+// have no room for more. With `drop`: bf16, groups of 128 and R = 32.
+int launch_grouped_w4_many(const W4Args& a, int R, cudaStream_t s, const W4Drop* drop = nullptr) {
   if (a.group == 32) R = std::min(R, 32);
   W4Params p;
   p.start = a.start;
@@ -542,10 +564,37 @@ int launch_grouped_w4_many(const W4Args& a, int R, cudaStream_t s) {
   if (rc != MOE_OK) return rc;
   rc = make_tmap_rows16(&tx, a.x, a.Kd, a.M_cap, a.ld_x, R);
   if (rc != MOE_OK) return rc;
-  auto* launch = a.group == 128  ? (a.half ? launch_rows<true, 128> : launch_rows<false, 128>)
-                 : a.group == 64 ? (a.half ? launch_rows<true, 64> : launch_rows<false, 64>)
-                                 : (a.half ? launch_rows<true, 32> : launch_rows<false, 32>);
-  return launch(R, tw, tx, p, tiles, s);
+  if (drop != nullptr) {
+    p.drop = *drop;
+    return launch<false, 128, 32, true>(tw, tx, p, tiles, s);
+  }
+  auto* pick = a.group == 128  ? (a.half ? launch_rows<true, 128> : launch_rows<false, 128>)
+               : a.group == 64 ? (a.half ? launch_rows<true, 64> : launch_rows<false, 64>)
+                               : (a.half ? launch_rows<true, 32> : launch_rows<false, 32>);
+  return pick(R, tw, tx, p, tiles, s);
+}
+
+int check(const W4Args& a) {
+  MOE_REQUIRE(a.start && a.psum, "moe_grouped_mm_w4: null segments");
+  MOE_REQUIRE(a.E > 0 && a.E <= kW4MaxE, "moe_grouped_mm_w4: E must be in [1, 1024]");
+  MOE_REQUIRE(a.group == 32 || a.group == 64 || a.group == 128, "moe_grouped_mm_w4: group must be 32, 64 or 128");
+  MOE_REQUIRE(a.N > 0 && a.N % 8 == 0 && a.Kd > 0 && a.Kd % a.group == 0,
+              "moe_grouped_mm_w4: N must be a positive multiple of 8, Kd of the group");
+  MOE_REQUIRE(a.M_cap >= 0 && a.M_cap <= INT32_MAX && a.max_rows >= 0 && a.max_rows <= a.M_cap,
+              "moe_grouped_mm_w4: M_cap and max_rows must fit each other and 32 bits");
+  MOE_REQUIRE(a.codes && a.scales && (a.M_cap == 0 || (a.x && a.out)),
+              "moe_grouped_mm_w4: operands must be non-null");
+  MOE_REQUIRE(a.ld_x >= a.Kd && a.ld_out >= a.N && a.ld_x % 8 == 0 && a.ld_out % 8 == 0,
+              "moe_grouped_mm_w4: a row stride must be a multiple of 8, at least the row");
+  MOE_REQUIRE(aligned(a.x, 16) && aligned(a.codes, 16) && aligned(a.out, 16) && aligned(a.scales, 16) &&
+                  aligned(a.zeros, 8),
+              "moe_grouped_mm_w4: x, codes, scales and out must be 16-byte aligned, zeros 8-byte");
+  MOE_REQUIRE(static_cast<int64_t>(a.E) * a.N <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit row numbers");
+  const int64_t live = std::min<int64_t>(a.E, a.max_rows);
+  MOE_REQUIRE((a.max_rows / 8 + live) * ((a.N + 31) / 32) <= INT32_MAX,
+              "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
+  MOE_REQUIRE(a.x != a.out || a.max_rows == 0, "moe_grouped_mm_w4: out must not be x");
+  return MOE_OK;
 }
 
 }  // namespace
@@ -556,31 +605,16 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
                                  const int32_t* psum, int dtype, int E, int N, int Kd, int64_t M_cap,
                                  int64_t max_rows, void* out, int64_t ld_out, int32_t* d_status,
                                  moe_stream_t stream) {
-  MOE_REQUIRE(start && psum, "moe_grouped_mm_w4: null segments");
   MOE_REQUIRE(dtype == MOE_BF16 || dtype == MOE_F16, "moe_grouped_mm_w4: dtype must be MOE_BF16 or MOE_F16");
-  MOE_REQUIRE(E > 0 && E <= moe::kW4MaxE, "moe_grouped_mm_w4: E must be in [1, 1024]");
-  MOE_REQUIRE(group == 32 || group == 64 || group == 128, "moe_grouped_mm_w4: group must be 32, 64 or 128");
-  MOE_REQUIRE(N > 0 && N % 8 == 0 && Kd > 0 && Kd % group == 0,
-              "moe_grouped_mm_w4: N must be a positive multiple of 8, Kd of the group");
-  MOE_REQUIRE(M_cap >= 0 && M_cap <= INT32_MAX && max_rows >= 0 && max_rows <= M_cap,
-              "moe_grouped_mm_w4: M_cap and max_rows must fit each other and 32 bits");
-  MOE_REQUIRE(codes && scales && (M_cap == 0 || (x && out)), "moe_grouped_mm_w4: operands must be non-null");
-  MOE_REQUIRE(ld_x >= Kd && ld_out >= N && ld_x % 8 == 0 && ld_out % 8 == 0,
-              "moe_grouped_mm_w4: a row stride must be a multiple of 8, at least the row");
-  MOE_REQUIRE(moe::aligned(x, 16) && moe::aligned(codes, 16) && moe::aligned(out, 16) &&
-                  moe::aligned(scales, 16) && moe::aligned(zeros, 8),
-              "moe_grouped_mm_w4: x, codes, scales and out must be 16-byte aligned, zeros 8-byte");
-  MOE_REQUIRE(static_cast<int64_t>(E) * N <= INT32_MAX, "moe_grouped_mm_w4: sizes exceed 32-bit row numbers");
-  const int64_t live = std::min<int64_t>(E, max_rows);
-  const int64_t mean = live > 0 ? (max_rows + live - 1) / live : 0;
-  MOE_REQUIRE((max_rows / 8 + live) * ((N + 31) / 32) <= INT32_MAX,
-              "moe_grouped_mm_w4: sizes exceed 32-bit tile numbers");
-  MOE_REQUIRE(x != out || max_rows == 0, "moe_grouped_mm_w4: out must not be x");
-  MOE_REQUIRE_DEVICE();
-  if (max_rows == 0) return MOE_OK;
   const moe::W4Args a = {x,  ld_x, codes, scales,   zeros, group,
                          start, psum, dtype == MOE_F16, E, N, Kd, M_cap, max_rows,
                          static_cast<uint16_t*>(out), ld_out, d_status};
+  const int rc = moe::check(a);
+  if (rc != MOE_OK) return rc;
+  MOE_REQUIRE_DEVICE();
+  if (max_rows == 0) return MOE_OK;
+  const int64_t live = std::min<int64_t>(E, max_rows);
+  const int64_t mean = (max_rows + live - 1) / live;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Which form, by the mean rows of an expert with rows and the weights read.
   // Up to four rows mma.sync is the faster (64 experts of 2048 x 4096 with 1, 2 and
@@ -600,4 +634,23 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
   // 44 rows 121, 92 and 84; scales of 32 values (more rows of their sums do not fit) 84
   // and 91 us with 8 rows in tiles of 16 and 32, 171 and 135 with 32.
   return moe::launch_grouped_w4_many(a, mean <= 12 ? 16 : (mean <= 26 ? 32 : (mean <= 40 ? 48 : 64)), s);
+}
+
+extern "C" int moe_selftest_w4_wait(const void* x, int64_t ld_x, const uint8_t* codes, const void* scales,
+                                    const uint8_t* zeros, const int32_t* start, const int32_t* psum, int E,
+                                    int N, int Kd, int64_t M_cap, int64_t max_rows, void* out, int64_t ld_out,
+                                    int64_t limit_cycles, int cta, int block, int32_t* d_status,
+                                    moe_stream_t stream) {
+  const moe::W4Args a = {x,  ld_x, codes, scales,   zeros, 128,
+                         start, psum, false, E, N, Kd, M_cap, max_rows,
+                         static_cast<uint16_t*>(out), ld_out, d_status};
+  const int rc = moe::check(a);
+  if (rc != MOE_OK) return rc;
+  MOE_REQUIRE(d_status, "moe_selftest_w4_wait: null status");
+  MOE_REQUIRE(limit_cycles > 0 && limit_cycles <= moe::kWaitLimitCycles,
+              "moe_selftest_w4_wait: limit must be in (0, 4e9] cycles");
+  MOE_REQUIRE_DEVICE();
+  if (max_rows == 0) return MOE_OK;
+  const moe::W4Drop drop = {limit_cycles, cta, block};
+  return moe::launch_grouped_w4_many(a, 32, reinterpret_cast<cudaStream_t>(stream), &drop);
 }

@@ -601,6 +601,18 @@ int moe_gemm_set_trace(uint64_t* d_trace);
 int moe_selftest_bounded_wait(int64_t limit_cycles, int32_t* d_status, int64_t* d_out,
                               moe_stream_t stream);
 
+/* Runs moe_grouped_mm_w4's form for more rows (bf16, groups of 128, tiles of 32
+ * rows) with waits of at most limit_cycles and without the copy of stage `block`
+ * (128 contracted values) of CTA `cta` (one per 256 columns of out, within each
+ * chunk of 32 rows; -1: all copies are made): the wait for it runs out,
+ * *d_status becomes MOE_ERR_TIMEOUT, and the rest of out is as always. For the
+ * library's tests. Arguments as in moe_grouped_mm_w4. */
+int moe_selftest_w4_wait(const void* x, int64_t ld_x, const uint8_t* codes, const void* scales,
+                         const uint8_t* zeros, const int32_t* start, const int32_t* psum, int E, int N,
+                         int Kd, int64_t M_cap, int64_t max_rows, void* out, int64_t ld_out,
+                         int64_t limit_cycles, int cta, int block, int32_t* d_status,
+                         moe_stream_t stream);
+
 /* Host. Text of the last error raised on this thread (never NULL). */
 const char* moe_last_error_string(void);
 

@@ -95,3 +95,39 @@ int main() {{
         for some in itertools.combinations_with_replacement(ctas, n):
             if sum(b + 1024 for b, _ in some) <= 228 * 1024:   # 1 KB a CTA is the system's
                 assert sum(c for _, c in some) <= 512, some
+
+
+def test_selftest_of_the_waits_refuses():
+    """What moe_grouped_mm_w4 refuses, a missing status and limits out of range,
+    before any CUDA call."""
+    import ctypes
+
+    from expanded_layout_expert_gb300 import _capi, build
+    build.build()
+    buf = (ctypes.c_uint8 * 4096)()
+    p = (ctypes.addressof(buf) + 255) // 256 * 256
+
+    def call(x=p, N=64, Kd=128, most=8, out=p + 1024, limit=1000, status=p):
+        return _capi.load().moe_selftest_w4_wait(x, Kd, p, p, None, p, p, 2, N, Kd, 8, most, out, N, limit, 0, 0,
+                                                 status, None)
+
+    for kw, text in ((dict(x=None), "non-null"), (dict(N=60), "multiple of 8"), (dict(Kd=64), "Kd of the group"),
+                     (dict(most=9), "max_rows"), (dict(out=p), "out must not be x"), (dict(status=None), "null status"),
+                     (dict(limit=0), "limit"), (dict(limit=1 << 33), "limit")):
+        assert call(**kw) == _capi.MOE_ERR_INVALID_ARG
+        assert text in _capi.load().moe_last_error_string().decode(), kw
+
+
+def test_what_is_under_way_is_waited_for_after_a_wait_gave_up():
+    """Products by the lane that issued them, copies by what was asked for: the
+    loop's own count goes on without asking."""
+    text = kernel()
+    load = block(text, text.index("auto load ="))
+    asked = load.index("full[kStages + stage] = static_cast<uint32_t>(b - b0 + 1);")
+    assert asked < load.index("mbar_arrive_expect_tx(")
+    drain = block(text, text.index("if (stop)"))
+    assert "to_load" not in drain and "asked" not in drain
+    issue = re.search(r"if \((\(warp & 3\) == 0) && elect_one\(\)\) \{\s*tc_fence_after\(\);", text).group(1)
+    assert re.search(re.escape(f"if ({issue} && elect_one()) {{") + r"\s*tc_commit\(&done\[half\]\);\s*"
+                     r"drain_wait\(&done\[half\], 0\);", drain)
+    assert "full[kStages + s]" in drain
