@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int half = warp >> 2, row = threadIdx.x & (kHalf - 1);
     const uint32_t bars = smem_u32(full), d_bar = smem_u32(&d_ready[half]);
     // A wait that gave up, here or in another warp, ends the waits and the loads;
-    // the rest of the loop goes on with whatever there is, and nothing is stored.
+    // the rest of the loop goes on with whatever there is, and nothing of the tile is
+    // stored.
     // The first test is made all the same: the lanes meet in it, as what follows wants
     // them to (the loads and stores of tensor memory are .aligned), after one of them
     // has issued products or copies.
@@ -465,6 +466,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (splits > 1) {
       cluster_sync();
+      // A CTA that gave up has no partials, and its flag is up: then no one stores.
+      const int lane = threadIdx.x & 31;
+      int lost = 0;
+      if (lane < splits)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(lost) : "r"(cta_smem(&s_abort, lane)) : "memory");
+      const bool whole = !__any_sync(0xffffffffu, lost != 0);
       // this CTA's share of the rows: the partials of all CTAs, in order
       const int ra = rows * rank / splits, rb = rows * (rank + 1) / splits;
       uint32_t from[8];
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           if (c < splits) sum += v[c];
-        if (i_ok && !stop) out[r * p.ld_out] = static_cast<uint16_t>(pack2<Half>(sum, 0.0f) & 0xffffu);
+        if (i_ok && whole) out[r * p.ld_out] = static_cast<uint16_t>(pack2<Half>(sum, 0.0f) & 0xffffu);
       }
       cluster_sync();   // no CTA leaves while its partials are read
     }

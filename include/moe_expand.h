@@ -570,6 +570,8 @@ int moe_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, i
  *   max_rows as in moe_grouped_mm
  * N and the row strides are multiples of 8, Kd a multiple of group, pointers
  * 16-byte aligned (zeros: 8), E <= 1024.
+ * A tile of out whose operands do not come in time is not written
+ * (MOE_ERR_TIMEOUT).
  */
 int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* codes, const void* scales,
                       const uint8_t* zeros, int group, const int32_t* start, const int32_t* psum,

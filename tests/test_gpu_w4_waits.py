@@ -78,3 +78,28 @@ def test_a_block_that_there_is_not(case):
     for cta, block in ((0, 7), (9, 0), (1 << 30, 3)):
         out, status = c.run(cta, block)
         assert status == 0 and torch.equal(out, want)
+
+
+@pytest.fixture(scope="module")
+def shared(mx):  # noqa: F811
+    """Contractions of 64 stages split over the eight CTAs of a cluster: three chunks
+    of rows, two tiles of columns."""
+    c = Case(mx, [40, 12], 264, 8192, 52)
+    return c, c.whole()
+
+
+@pytest.mark.parametrize("rank", [0, 3, 7])
+@pytest.mark.parametrize("tile,rows,columns", [(0, (0, 32), (0, 256)), (3, (32, 40), (256, 264)),
+                                               (4, (40, 52), (0, 256))])
+@pytest.mark.parametrize("block", [0, 5])
+def test_no_one_of_the_cluster_stores(shared, tile, rows, columns, rank, block):
+    """The others of a cluster have their own sums, but not the tile's."""
+    c, want = shared
+    out, status = c.run(tile * 8 + rank, block)
+    assert status == TIMEOUT
+    lost = torch.zeros_like(out, dtype=torch.bool)
+    lost[rows[0]:rows[1], columns[0]:columns[1]] = True
+    assert (out[lost] == KEPT).all()
+    assert torch.equal(out[~lost], want[~lost])
+    again, status = c.run(-1, 0)
+    assert status == 0 and torch.equal(again, want)
