@@ -41,8 +41,8 @@ MOE_DEV void store_logit(void* p, int64_t i, int dtype, float v) {
         static_cast<uint16_t>((dtype == MOE_F16 ? pack2<true>(v, 0.0f) : pack2<false>(v, 0.0f)) & 0xffffu);
 }
 
-// A lane's part of a row, from place `at` on in steps of kLanes; places from E on
-// are -inf.
+// A lane's part of a row that begins at element `row`: every kLanes-th logit from the
+// lane's own on; places from E on are -inf.
 template <int kLanes, int kN>
 MOE_DEV void load_part(const void* p, int64_t row, int lane, int E, int dtype, float (&l)[kN]) {
   if (dtype == MOE_F32) {
