@@ -14,12 +14,18 @@
 // multiplies by its scale and adds up in fp32 registers. So nothing is rounded
 // but the sums and, once, the result.
 //
-// Bound: a 128 x 128 block of codes has 360 cycles at HBM's rate on an SM. It is
-// 350 instructions of each of four warps, half of them the making of the values,
-// on four schedulers, each step a chain from the sums to the values, the barrier and
-// the products; the four warpgroups of an SM cover for each other (a CTA alone takes
-// 0.83 us a block, two 1.07). 64 experts of 4096 x 7168 with 32 rows each take 224 us
-// (4.6 TB/s), with 8 rows 198 (5.0 TB/s).
+// Bound: no single unit (issue slots are half used, HBM at 0.7 to 0.77 of a copy's rate).
+// 64 experts of 4096 x 7168 take, with 32 and with 8 rows each, 218 us (4.7 TB/s; the
+// bytes alone 152) and 194 us (5.1 TB/s; 147). With parts taken out for timing: the
+// products 216 and 191, the sums 213 and 187, the making of the values 203 and 167, all
+// three 203 and 169, the copies of x 213 and 191, those and the three 178 and 166, the
+// stores to tensor memory as well 169 and 156. One stage of a tile's 56 alone, so the
+// starts and ends of 1024 tiles in 3.4 rounds of 304, takes 30 and 26.
+// So with few rows it is the making of the values, half of the 350 instructions that
+// each of four warps has for 128 x 128 codes, in a chain from the sums to the values,
+// the barrier and the products (the SM's four warpgroups cover for each other); with
+// more rows x stands behind it, brought anew for every 256 weight rows; and the starts
+// behind both.
 // What got there, in us for 32 rows: one CTA of four dequantising warps, a TMA
 // and an MMA warp, sums waited for at once 490; the next values made meanwhile
 // 386; no warps of their own for the loads and products, which poll for their
@@ -27,10 +33,10 @@
 // uniform 300; 256 rows a CTA, so that four stages fit, 279; the warpgroups'
 // barriers apart 249; the loop's arithmetic off the uniform pipe 245; sums first and
 // then the values, in few registers, 243; the scales moved up between them 234;
-// tiles of 48 rows for them instead of 64 224.
+// tiles of 48 rows for them instead of 64 224; no branch in front of a barrier's test 218.
 // Eight warps for 128 rows, three CTAs, were slower (362), and so were sums fetched
 // while the next values are made (267) and the contraction split in two for fuller
-// waves (279): the start of a CTA takes 7 us.
+// waves (279).
 //
 // With few tiles the contraction is split over the CTAs of a cluster, whose
 // partial sums meet in a fixed order through distributed shared memory.
@@ -62,11 +68,13 @@ constexpr int step_k(int group, int R) { return 64 / R * group < 128 ? 64 / R * 
 
 constexpr int stage_bytes(int R) { return kCodeBytes + R * BC * 2; }
 // What the ring takes is lost to L1, where the scales' sectors wait for their next
-// use, so the more scales a row has, the fewer stages (20 rows each for 64 experts of
-// 4096 x 7168 take, with 4 and 3 stages, 213 and 213 us in groups of 128, 254 and 234
-// in groups of 64, 408 and 286 in groups of 32; 8 rows 198 and 203, 226 and 220, 251
-// and 236; five stages for 8 rows in groups of 32, 332). Two stages are too few (364), and
-// for more than 32 rows two CTAs have no room for four.
+// use, so the more scales a row has, the fewer stages (64 experts of 4096 x 7168 with 20
+// rows each take, with 4 and 3 stages, 203 and 208 us in groups of 128, 253 and 231
+// in groups of 64, 401 and 278 in groups of 32; with 8 rows 194 and 200, 224 and 218, 246
+// and 238). Tiles of 16 rows in groups of 64 keep four all the same, for short
+// contractions: 64 experts of 2048 x 4096 73 and 74 us, without zero points 71 and 73, 16
+// of 4096 x 4096 with 12 rows 46.9 and 47.6, 160 of 1536 x 5120 164 and 166. Two
+// stages are too few, and for more than 32 rows two CTAs have no room for four.
 constexpr int stages_for(int group, int R) { return R > 32 || group <= 2 * R ? 3 : 4; }
 constexpr int ring_bytes(int group, int R) { return stages_for(group, R) * stage_bytes(R) + 1024; }
 // Two CTAs an SM is the most, because tensor memory has room for no third: nothing
@@ -625,21 +633,22 @@ extern "C" int moe_grouped_mm_w4(const void* x, int64_t ld_x, const uint8_t* cod
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Which form, by the mean rows of an expert with rows and the weights read.
   // Up to four rows mma.sync is the faster (64 experts of 2048 x 4096 with 1, 2 and
-  // 4 rows: 41, 53 and 62 us, here 48, 58 and 67), from six on this form (69 there,
-  // 68 here; with 8 rows 83 and 68); with fewer weights its few large tiles leave SMs
-  // idle longer: 8 experts of 4096 x 4096 take 26 us there and 27 here with 8 rows, 39
-  // and 30 with 16, 32 of 2048 x 4096 with 8 in groups of 64 52 and 47; 8 of 1024 x
-  // 1024 5.4 and 8.1 with 8, 9.9 and 11.4 with 32.
+  // 4 rows: 42, 54 and 61 us, here 54, 59 and 66), from six on this form (70 there,
+  // 66 here; with 8 rows 84 and 66); with fewer weights its few large tiles leave SMs
+  // idle longer: 8 experts of 4096 x 4096 take 20 us there and 27 here with 8 rows, 34
+  // and 29 with 16, 32 of 2048 x 4096 with 8 in groups of 64 52 and 46; 8 of 1024 x
+  // 1024 5.2 and 7.9 with 8, 8.5 and 10.9 with 32.
   const int64_t weights = live * N * Kd;
   const int64_t scale_bytes = 32ll * moe::w4_few_pitch(Kd / group) * 3;
   if ((mean <= 4 || (mean <= 8 && weights <= (1ll << 27)) || (mean <= 32 && weights <= (1ll << 23))) &&
       scale_bytes <= moe::kW4FewScaleBytes)
     return moe::launch_grouped_w4_few(a, s);
-  // Rows of a tile: 64 experts of 2048 x 4096 with 8 rows each take 68, 71 and 77
-  // us with 16, 32 and 64, with 16 rows 86, 72 and 78; with 32 rows 91, 79 and 81 with
-  // 32, 48 and 64 (in groups of 64 101, 91 and 102), with 26 rows 73, 78 and 81, with
-  // 44 rows 121, 92 and 84; scales of 32 values (more rows of their sums do not fit) 84
-  // and 91 us with 8 rows in tiles of 16 and 32, 171 and 135 with 32.
+  // Rows of a tile, by the mean of the rows there may be (max_rows: what there are,
+  // only the device knows): 64 experts of 2048 x 4096 with 8 rows each take 66, 68
+  // and 75 us with 16, 32 and 64, with 16 rows 83, 69 and 76; with 32 rows 87, 77 and 80
+  // with 32, 48 and 64 (in groups of 64 98, 90 and 98), with 26 rows 71, 76 and 79, with
+  // 44 rows 115, 90 and 82; scales of 32 values (more rows of their sums do not fit) 84
+  // and 88 us with 8 rows in tiles of 16 and 32, 167 and 130 with 32.
   return moe::launch_grouped_w4_many(a, mean <= 12 ? 16 : (mean <= 26 ? 32 : (mean <= 40 ? 48 : 64)), s);
 }
 

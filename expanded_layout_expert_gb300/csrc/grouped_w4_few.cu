@@ -10,10 +10,11 @@
 // products in fp32; the scale multiplies that sum in fp32.
 //
 // mma.sync has a quarter of tcgen05's rate, enough for 8 rows at HBM's. What
-// bounds the kernel is the making of the values, ten instructions for eight, six
-// of them on the pipe with half a warp a cycle: one token of 8 out of 64 experts
-// of 4096 x 7168 takes 27.5 us (4.4 TB/s of codes and scales; 22.5 without the
-// copies, 24.4 with the codes taken as they are). A block of four warps does 32
+// bounds the kernel is no one thing: one token of 8 out of 64 experts of 4096 x 7168 takes
+// 27.4 us (4.4 TB/s of codes and scales, whose bytes alone take 17.9), 26.5 with the codes taken
+// as they are, 25.8 without reading x, 22.4 without the copies, 14.0 without all three and 7.1
+// with one step of the loop: the start (segments found, the first copies
+// asked for and come) and the end of a single wave. A block of four warps does 32
 // weight rows by one expert's chunk; the warps take every fourth 128 contracted
 // values and meet once, at the end, in shared memory in a fixed order. Blocks
 // are small so that those of a single token all fit the GPU at once (with six
